@@ -1,9 +1,10 @@
 """Ahead-of-time build of the HIP library for gfx950 (hipcc, no JIT).
 
 ``python -m moe_matmul_amd.build`` compiles ``csrc/nvfp4_grouped_gemm.hip``
-into ``moe_matmul_amd/libnvfp4_grouped_gemm.so`` next to this file, and the
-mainloop measurement kernels ``csrc/mainloop_probe.hip`` into
-``moe_matmul_amd/libnvfp4_mainloop_probe.so``.
+into ``moe_matmul_amd/libnvfp4_grouped_gemm.so`` next to this file, the operators
+around it (``csrc/moe_*.hip``, ``csrc/nvfp4_quantize.hip``) into
+``moe_matmul_amd/libnvfp4_moe.so``, and the mainloop measurement kernels
+``csrc/mainloop_probe.hip`` into ``moe_matmul_amd/libnvfp4_mainloop_probe.so``.
 """
 from __future__ import annotations
 
@@ -17,6 +18,10 @@ ROOT = os.path.dirname(HERE)
 SOURCES = [os.path.join(HERE, "csrc", "nvfp4_grouped_gemm.hip")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libnvfp4_grouped_gemm.so")
+# the operators around the GEMM in a layer of experts (include/nvfp4_moe.h)
+MOE_SOURCES = [os.path.join(HERE, "csrc", f) for f in
+               ("moe_route.hip", "moe_plan.hip", "nvfp4_quantize.hip", "moe_combine.hip", "moe_few.hip")]
+MOE_LIB = os.path.join(HERE, "libnvfp4_moe.so")
 # measurement kernels behind the mainloop choice (not part of the GEMM)
 PROBE_SOURCES = [os.path.join(HERE, "csrc", "mainloop_probe.hip")]
 PROBE_LIB = os.path.join(HERE, "libnvfp4_mainloop_probe.so")
@@ -38,11 +43,18 @@ def hipcc() -> str:
 
 
 def build(verbose: bool = False) -> str:
-    """Compile the library and the probe library (always, even if built copies
-    exist); return the library's path."""
+    """Compile the library, the operators' library and the probe library (always,
+    even if built copies exist); return the library's path."""
     _compile(SOURCES, LIB, verbose)
+    build_moe(verbose)
     _compile(PROBE_SOURCES, PROBE_LIB, verbose)
     return LIB
+
+
+def build_moe(verbose: bool = False) -> str:
+    """Compile the operators' library alone; return its path."""
+    _compile(MOE_SOURCES, MOE_LIB, verbose)
+    return MOE_LIB
 
 
 def _compile(sources, lib, verbose):

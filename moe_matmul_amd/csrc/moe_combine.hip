@@ -1,0 +1,225 @@
+// The combine: weighted sums of the experts' rows of every token, and its
+// gradients.
+#include "moe_common.h"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+
+struct CombineArgs {
+  const void* c;
+  int64_t c_stride, tokens, out_stride, dy_stride;
+  const int32_t *slot_rows, *ids;
+  const float *weights, *alpha;
+  const void* residual;
+  void* out;
+  const void* dy;
+  void* dc;
+  float* dweights;
+  int topk, n, chunks, c_vec, out_vec, dy_vec;
+};
+
+// A slot's row (-1: none) and its expert's factor.
+__device__ inline int64_t slot_row(const CombineArgs& a, int64_t slot, float& factor) {
+  int64_t row = a.slot_rows == nullptr ? slot : a.slot_rows[slot];
+  factor = 1.f;
+  if (a.ids != nullptr) {
+    const int id = a.ids[slot];
+    if (id < 0) row = -1;
+    else if (a.alpha != nullptr && row >= 0) factor = a.alpha[id];
+  }
+  return row;
+}
+
+// Eight columns of a token to a thread; its rows are read at once and added in
+// slot order. Bound by memory: each row of c is read once, in 16-byte pieces.
+template <class C, class Out, int K>
+__global__ void __launch_bounds__(kThreads) nvfp4_moe_combine_kernel(CombineArgs a) {
+  const uint32_t index = blockIdx.x * kThreads + threadIdx.x;
+  const int64_t token = index / (uint32_t)a.chunks;
+  const int col = (int)(index % (uint32_t)a.chunks) * 8;
+  if (token >= a.tokens) return;
+  float sum[8];
+  if (a.residual != nullptr) {
+    load8<Out>(a.residual, token * a.out_stride + col, a.out_vec, sum);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum[i] = 0.f;
+  }
+  for (int from = 0; from < a.topk; from += K) {
+    float w[K], v[K][8];
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+      w[j] = 0.f;
+      if (from + j < a.topk) {
+        const int64_t slot = token * a.topk + from + j;
+        float factor;
+        const int64_t row = slot_row(a, slot, factor);
+        if (row >= 0) {
+          w[j] = (a.weights == nullptr ? 1.f : a.weights[slot]) * factor;
+          load8<C>(a.c, row * a.c_stride + col, a.c_vec, v[j]);
+          continue;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[j][i] = 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < K; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] = fmaf(w[j], v[j][i], sum[i]);
+  }
+  store8<Out>(a.out, token * a.out_stride + col, a.out_vec, sum);
+}
+
+// A workgroup per token: dy is read once, its rows of c once, dc written once.
+// The sums of d weights go thread by thread, then lanes, then waves: always in
+// the same order.
+template <class C, class Dy, int K>
+__global__ void __launch_bounds__(kThreads) nvfp4_moe_combine_backward_kernel(CombineArgs a) {
+  __shared__ float s_sum[K][kThreads / 64];
+  const int64_t token = blockIdx.x;
+  int64_t row[K];
+  float w[K], factor[K], sum[K];
+#pragma unroll
+  for (int j = 0; j < K; ++j) {
+    row[j] = -1;
+    w[j] = factor[j] = sum[j] = 0.f;
+    if (j < a.topk) {
+      const int64_t slot = token * a.topk + j;
+      row[j] = slot_row(a, slot, factor[j]);
+      if (row[j] >= 0) w[j] = (a.weights == nullptr ? 1.f : a.weights[slot]) * factor[j];
+    }
+  }
+  for (int col = threadIdx.x * 8; col < a.n; col += kThreads * 8) {
+    float dy[8];
+    load8<Dy>(a.dy, token * a.dy_stride + col, a.dy_vec, dy);
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+      if (row[j] < 0) continue;
+      float v[8], d[8];
+      load8<C>(a.c, row[j] * a.c_stride + col, a.c_vec, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        sum[j] = fmaf(dy[i], v[i], sum[j]);
+        d[i] = w[j] * dy[i];
+      }
+      store8<C>(a.dc, row[j] * a.c_stride + col, a.c_vec, d);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < K; ++j) {
+    float s = sum[j];
+    for (int d = 1; d < 64; d *= 2) s += __shfl_xor(s, d);
+    if (threadIdx.x % 64 == 0) s_sum[j][threadIdx.x / 64] = s;
+  }
+  __syncthreads();
+  if ((int)threadIdx.x < a.topk) {
+    float s = 0.f;
+    for (int i = 0; i < kThreads / 64; ++i) s += s_sum[threadIdx.x][i];
+    const int64_t slot = token * a.topk + threadIdx.x;
+    float f;
+    const int64_t r = slot_row(a, slot, f);
+    a.dweights[slot] = r >= 0 ? s * f : 0.f;
+  }
+}
+
+int check_combine(const CombineArgs& a, int c_dtype, int dtype, int64_t stride, const void* p, const void* q) {
+  if (!known_type(c_dtype) || !known_type(dtype)) return NVFP4_ERR_INVALID;
+  if (a.tokens < 0 || a.tokens >= (int64_t)1 << 30 || a.topk < 1 || a.topk > NVFP4_MOE_MAX_TOPK) return NVFP4_ERR_INVALID;
+  if (a.n < 0 || a.n % 8 || a.c_stride < a.n || stride < a.n) return NVFP4_ERR_INVALID;
+  if (a.c_stride > (int64_t)1 << 30 || stride > (int64_t)1 << 30) return NVFP4_ERR_INVALID;
+  if (a.alpha != nullptr && a.ids == nullptr) return NVFP4_ERR_INVALID;
+  if (a.tokens > 0 && a.n > 0 && (a.c == nullptr || p == nullptr || q == nullptr)) return NVFP4_ERR_INVALID;
+  if (!aligned(a.slot_rows, 4) || !aligned(a.ids, 4) || !aligned(a.weights, 4) || !aligned(a.alpha, 4))
+    return NVFP4_ERR_MISALIGNED;
+  if (!aligned(a.c, element_bytes(c_dtype)) || !aligned(p, element_bytes(dtype))) return NVFP4_ERR_MISALIGNED;
+  return NVFP4_OK;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+int nvfp4_moe_combine(const void* c, int c_dtype, int64_t c_stride, int64_t tokens, int topk, int n,
+                      const int32_t* slot_rows, const float* weights, const float* alpha, const int32_t* ids,
+                      const void* residual, void* out, int out_dtype, int64_t out_stride, void* stream) {
+  CombineArgs a = {};
+  a.c = c;
+  a.c_stride = c_stride;
+  a.tokens = tokens;
+  a.out_stride = out_stride;
+  a.slot_rows = slot_rows;
+  a.ids = ids;
+  a.weights = weights;
+  a.alpha = alpha;
+  a.residual = residual;
+  a.out = out;
+  a.topk = topk;
+  a.n = n;
+  if (int rc = check_combine(a, c_dtype, out_dtype, out_stride, out, out)) return rc;
+  if (!aligned(residual, element_bytes(out_dtype))) return NVFP4_ERR_MISALIGNED;
+  if (tokens == 0 || n == 0) return NVFP4_OK;
+  a.chunks = n / 8;
+  a.c_vec = wide_rows(c, c_dtype, c_stride);
+  a.out_vec = wide_rows(out, out_dtype, out_stride) && aligned(residual, 16);
+  const int64_t blocks = ceil_div64(tokens * a.chunks, kThreads);
+  if (blocks >= (int64_t)1 << 24) return NVFP4_ERR_INVALID;
+  const hipStream_t st = (hipStream_t)stream;
+  return with_type(c_dtype, [&](auto t) {
+    return with_type(out_dtype, [&](auto u) {
+      using C = decltype(t);
+      using O = decltype(u);
+      if (topk <= 1) nvfp4_moe_combine_kernel<C, O, 1><<<(unsigned)blocks, kThreads, 0, st>>>(a);
+      else if (topk <= 2) nvfp4_moe_combine_kernel<C, O, 2><<<(unsigned)blocks, kThreads, 0, st>>>(a);
+      else if (topk <= 4) nvfp4_moe_combine_kernel<C, O, 4><<<(unsigned)blocks, kThreads, 0, st>>>(a);
+      else nvfp4_moe_combine_kernel<C, O, 8><<<(unsigned)blocks, kThreads, 0, st>>>(a);
+      return launched();
+    });
+  });
+}
+
+int nvfp4_moe_combine_backward(const void* dy, int dy_dtype, int64_t dy_stride, const void* c, int c_dtype,
+                               int64_t c_stride, int64_t tokens, int topk, int n, const int32_t* slot_rows,
+                               const float* weights, const float* alpha, const int32_t* ids, void* dc,
+                               float* dweights, void* stream) {
+  CombineArgs a = {};
+  a.c = c;
+  a.c_stride = c_stride;
+  a.tokens = tokens;
+  a.dy = dy;
+  a.dy_stride = dy_stride;
+  a.slot_rows = slot_rows;
+  a.ids = ids;
+  a.weights = weights;
+  a.alpha = alpha;
+  a.dc = dc;
+  a.dweights = dweights;
+  a.topk = topk;
+  a.n = n;
+  if (int rc = check_combine(a, c_dtype, dy_dtype, dy_stride, dy, dc)) return rc;
+  if (tokens > 0 && dweights == nullptr) return NVFP4_ERR_INVALID;
+  if (tokens >= (int64_t)1 << 24) return NVFP4_ERR_INVALID;
+  if (!aligned(dc, element_bytes(c_dtype)) || !aligned(dweights, 4)) return NVFP4_ERR_MISALIGNED;
+  if (tokens == 0) return NVFP4_OK;
+  a.c_vec = wide_rows(c, c_dtype, c_stride) && aligned(dc, 16);
+  a.dy_vec = wide_rows(dy, dy_dtype, dy_stride);
+  const hipStream_t st = (hipStream_t)stream;
+  return with_type(c_dtype, [&](auto t) {
+    return with_type(dy_dtype, [&](auto u) {
+      using C = decltype(t);
+      using D = decltype(u);
+      if (topk <= 2) nvfp4_moe_combine_backward_kernel<C, D, 2><<<(unsigned)tokens, kThreads, 0, st>>>(a);
+      else if (topk <= 4) nvfp4_moe_combine_backward_kernel<C, D, 4><<<(unsigned)tokens, kThreads, 0, st>>>(a);
+      else if (topk <= 8) nvfp4_moe_combine_backward_kernel<C, D, 8><<<(unsigned)tokens, kThreads, 0, st>>>(a);
+      else nvfp4_moe_combine_backward_kernel<C, D, 16><<<(unsigned)tokens, kThreads, 0, st>>>(a);
+      return launched();
+    });
+  });
+}
+
+}  // extern "C"

@@ -1,0 +1,450 @@
+"""A layer of experts around the NVFP4 grouped GEMM, on PyTorch tensors.
+
+Each function checks its tensors, allocates the outputs that are not given and
+enqueues one operator of ``include/nvfp4_moe.h`` (which states the mathematics,
+the limits and what happens at the edges) on ``stream``, by default torch's
+current stream. Nothing is synchronised; after the first call of a shape no call
+reads from the device, so calls can be captured in a graph. Tensors that are
+used on another stream than the one they were made on are the caller's to keep
+alive (``Tensor.record_stream``), as everywhere in torch.
+
+``FeedForward`` runs them together: route -> plan -> quantise -> grouped GEMM ->
+gated activation -> grouped GEMM -> combine, or, for a few tokens, the experts'
+products with activations as they are.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _moe_binding as c
+from ._binding import nvfp4_grouped_gemm_device, nvfp4_sf_bytes
+
+_TYPES = {torch.float32: c.NVFP4_MOE_F32, torch.float16: c.NVFP4_MOE_F16, torch.bfloat16: c.NVFP4_MOE_BF16}
+_SCORES = {"softmax": c.NVFP4_MOE_SOFTMAX, "sigmoid": c.NVFP4_MOE_SIGMOID}
+
+
+def _type(t: torch.Tensor, what: str) -> int:
+    try:
+        return _TYPES[t.dtype]
+    except KeyError:
+        raise ValueError(f"{what} must be fp32, fp16 or bf16, not {t.dtype}") from None
+
+
+def _gpu(t: torch.Tensor, what: str) -> torch.device:
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be on a GPU")
+    return t.device
+
+
+def _like(t, what, shape, dtype, device):
+    """A contiguous tensor of that shape and type, on that device."""
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, not "
+                         f"{t.dtype} {tuple(t.shape)} {tuple(t.stride())} on {t.device}")
+    return t
+
+
+def _out(t, what, shape, dtype, device):
+    return torch.empty(shape, dtype=dtype, device=device) if t is None else _like(t, what, shape, dtype, device)
+
+
+def _rows(t: torch.Tensor, what: str, width=None) -> int:
+    """Row stride of a 2-d tensor with adjacent columns."""
+    if t.dim() != 2 or (width is not None and t.shape[1] != width):
+        raise ValueError(f"{what} must have shape [rows, {'columns' if width is None else width}], not {tuple(t.shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what} must have adjacent columns (strides {tuple(t.stride())})")
+    # a single row's stride says nothing, and broadcast rows are all the same
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"{what} must have rows that do not overlap (strides {tuple(t.stride())})")
+    return max(t.stride(0), t.shape[1]) if t.shape[0] > 1 else t.shape[1]
+
+
+def _at(t) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
+class _On:
+    """The stream to enqueue on, with its device current."""
+
+    __slots__ = ("guard", "stream")
+
+    def __init__(self, device, stream):
+        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+        self.stream = stream if stream is not None else torch.cuda.current_stream(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return getattr(self.stream, "cuda_stream", self.stream)
+
+    def __exit__(self, *e):
+        if self.guard is not None:
+            self.guard.__exit__(*e)
+
+
+def _choice(score, topk, groups, topk_groups, group_best, renormalize, scale):
+    if score not in _SCORES:
+        raise ValueError(f"score must be 'softmax' or 'sigmoid', not {score!r}")
+    return ctypes.byref(c.nvfp4_moe_choice(_SCORES[score], topk, groups, groups if topk_groups is None else topk_groups,
+                                           group_best, bool(renormalize), scale))
+
+
+# ---- routing ------------------------------------------------------------------
+
+def route(logits, topk, *, score="softmax", bias=None, groups=1, topk_groups=None, group_best=1, renormalize=True,
+          scale=1.0, ids=None, weights=None, stream=None):
+    """Expert ids (int32) and weights (fp32) [tokens, topk] of ``logits`` [tokens, experts].
+
+    ``score`` of all logits, plus ``bias`` [experts] (fp32) for the choice alone; with ``groups``, only the
+    ``topk_groups`` groups of experts whose best ``group_best`` (1 or 2) choice values sum highest stay eligible;
+    ``renormalize``: divide by the sum of the chosen; times ``scale``. -inf masks an expert; slots that no expert is
+    left for get id -1 and weight 0."""
+    device = _gpu(logits, "logits")
+    stride = _rows(logits, "logits")
+    tokens, experts = logits.shape
+    if bias is not None:
+        _like(bias, "bias", (experts,), torch.float32, device)
+    ids = _out(ids, "ids", (tokens, topk), torch.int32, device)
+    weights = _out(weights, "weights", (tokens, topk), torch.float32, device)
+    with _On(device, stream) as s:
+        c.nvfp4_moe_route(logits.data_ptr(), _type(logits, "logits"), tokens, experts, stride, _at(bias),
+                          _choice(score, topk, groups, topk_groups, group_best, renormalize, scale), ids.data_ptr(),
+                          weights.data_ptr(), s)
+    return ids, weights
+
+
+def route_backward(logits, ids, dweights, *, score="softmax", renormalize=True, scale=1.0, dlogits=None, stream=None):
+    """Gradient of ``route``'s weights with respect to the logits (their type, every element written), the chosen
+    ``ids`` held fixed."""
+    device = _gpu(logits, "logits")
+    stride = _rows(logits, "logits")
+    tokens, experts = logits.shape
+    topk = ids.shape[-1]
+    _like(ids, "ids", (tokens, topk), torch.int32, device)
+    _like(dweights, "dweights", (tokens, topk), torch.float32, device)
+    if dlogits is None:
+        dlogits = torch.empty((tokens, experts), dtype=logits.dtype, device=device)
+    elif dlogits.dtype != logits.dtype or dlogits.device != device or dlogits.shape != logits.shape:
+        raise ValueError("dlogits must have the logits' shape, type and device")
+    with _On(device, stream) as s:
+        c.nvfp4_moe_route_backward(logits.data_ptr(), _type(logits, "logits"), tokens, experts, stride,
+                                   _choice(score, topk, 1, 1, 1, renormalize, scale), ids.data_ptr(),
+                                   dweights.data_ptr(), dlogits.data_ptr(), _rows(dlogits, "dlogits"), s)
+    return dlogits
+
+
+# ---- the plan --------------------------------------------------------------------
+
+class Product:
+    """A grouped product over rows sorted by expert, ``c[row] = a[row] . b[expert]``, and the group tables that
+    ``plan`` fills for ``nvfp4_grouped_gemm_device``."""
+
+    def __init__(self, a, sfa, b, sfb, out):
+        device = _gpu(b, "b")
+        experts, n, half = b.shape
+        self.n, self.k, self.experts = n, 2 * half, experts
+        rows = a.shape[0]
+        self.a, self.out = _like(a, "a", (rows, half), torch.uint8, device), _like(out, "out", (rows, n), torch.float16, device)
+        self.b, self.sfb = _operand(b, sfb)
+        self.sfa = _like(sfa, "sfa", (max(sfa.shape[0], c.nvfp4_moe_sf_bytes(rows, experts, self.k)),), torch.uint8, device)
+        # sizes int32 [experts][4], then the two address tables, each from a multiple of 16 bytes on
+        self._tables = torch.empty(experts * 56 + 32, dtype=torch.uint8, device=device)
+        sizes = self._tables.data_ptr()
+        abc = sizes + 16 * experts
+        self.tables = (sizes, abc, (abc + 24 * experts + 15) // 16 * 16)
+
+    def entry(self):
+        return c.nvfp4_moe_product(self.n, self.k, self.a.data_ptr(), self.b.data_ptr(), self.out.data_ptr(),
+                                   self.sfa.data_ptr(), self.sfb.data_ptr(), *self.tables)
+
+    def run(self, tile_config=-1, status=None, stream=None):
+        """Enqueue the product, after a ``plan`` that this one was given to."""
+        with _On(self.b.device, stream) as s:
+            nvfp4_grouped_gemm_device(*self.tables, self.experts, tile_config, _at(status), s)
+        return self.out
+
+
+class Plan:
+    """Where the rows of every slot lie: ``offsets`` and ``atoms`` [experts + 1], ``slot_rows`` [tokens, topk] and
+    ``row_slots`` [tokens * topk] (all int32), and the ``ids`` that they were made from."""
+
+    def __init__(self, ids, experts):
+        self.ids, self.experts = ids, experts
+        self.tokens, self.topk = ids.shape
+        slots = self.tokens * self.topk
+        both = torch.empty(2 * (experts + 1 + slots), dtype=torch.int32, device=ids.device)
+        self.offsets, self.atoms, rows, self.row_slots = both.split((experts + 1, experts + 1, slots, slots))
+        self.slot_rows = rows.view(ids.shape)
+
+    @property
+    def rows(self) -> int:
+        """The most rows there can be (those that are there: ``offsets[experts]``, on the device)."""
+        return self.tokens * self.topk
+
+
+def plan(ids, experts, products=(), *, stream=None) -> Plan:
+    """Sort the slots of ``ids`` [tokens, topk] (int32) by expert, and fill the tables of ``products``."""
+    device = _gpu(ids, "ids")
+    if ids.dim() != 2:
+        raise ValueError(f"ids must have shape [tokens, topk], not {tuple(ids.shape)}")
+    _like(ids, "ids", ids.shape, torch.int32, device)
+    p = Plan(ids, experts)
+    entries = (c.nvfp4_moe_product * len(products))(*[q.entry() for q in products]) if products else None
+    for q in products:
+        if q.experts != experts or q.a.shape[0] < p.rows:
+            raise ValueError("a product must have the plan's experts and room for its rows")
+    need = c.nvfp4_moe_plan_workspace_bytes(p.tokens, p.topk, experts)
+    workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    with _On(device, stream) as s:
+        c.nvfp4_moe_plan(ids.data_ptr(), p.tokens, p.topk, experts, p.offsets.data_ptr(), p.atoms.data_ptr(),
+                         p.slot_rows.data_ptr(), p.row_slots.data_ptr(), entries, len(products), _at(workspace), need, s)
+    return p
+
+
+# ---- quantisation ------------------------------------------------------------------
+
+def _operand(b, sfb):
+    """Stacked weights [experts, n, k/2] with their scales [experts, nvfp4_sf_bytes(n, k)]."""
+    if b.dim() != 3:
+        raise ValueError(f"b must have shape [experts, n, k/2], not {tuple(b.shape)}")
+    device = _gpu(b, "b")
+    _like(b, "b", b.shape, torch.uint8, device)
+    _like(sfb, "sfb", (b.shape[0], nvfp4_sf_bytes(b.shape[1], 2 * b.shape[2])), torch.uint8, device)
+    return b, sfb
+
+
+def quantize(x, *, plan=None, scale=1.0, a=None, sfa=None, stream=None):
+    """NVFP4 codes and tiled scales of ``x * scale``.
+
+    Without a plan: x [m, k] or [l, m, k] -> a [..., k/2] (uint8) and sfa (uint8, ``nvfp4_sf_bytes(m, k, l)``). With
+    one: x [tokens, k] -> a [tokens * topk, k/2], each token's row at the rows of its slots, and sfa of the rows
+    sorted by expert."""
+    device = _gpu(x, "x")
+    kind = _type(x, "x")
+    k = x.shape[-1]
+    if k % 32:
+        raise ValueError(f"rows must have a multiple of 32 elements, not {k}")
+    if plan is not None:
+        stride = _rows(x, "x")
+        if x.shape[0] != plan.tokens or plan.ids.device != device:
+            raise ValueError(f"x must have the plan's {plan.tokens} tokens, on its device")
+        a = _out(a, "a", (plan.rows, k // 2), torch.uint8, device)
+        sfa = _out(sfa, "sfa", (c.nvfp4_moe_sf_bytes(plan.rows, plan.experts, k),), torch.uint8, device)
+        need = c.nvfp4_moe_dispatch_workspace_bytes(plan.tokens, plan.topk, k, plan.experts)
+        workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+        with _On(device, stream) as s:
+            c.nvfp4_moe_dispatch(x.data_ptr(), kind, plan.tokens, plan.topk, k, stride, scale, plan.ids.data_ptr(),
+                                 plan.slot_rows.data_ptr(), plan.row_slots.data_ptr(), plan.offsets.data_ptr(),
+                                 plan.atoms.data_ptr(), plan.experts, a.data_ptr(), sfa.data_ptr(), _at(workspace),
+                                 need, s)
+        return a, sfa
+    if x.dim() not in (2, 3):
+        raise ValueError(f"x must have shape [m, k] or [l, m, k], not {tuple(x.shape)}")
+    l, m = (x.shape[0], x.shape[1]) if x.dim() == 3 else (1, x.shape[0])
+    stride = _rows(x[0] if x.dim() == 3 and l else x.view(-1, k) if x.dim() == 3 else x, "x")
+    batch = x.stride(0) if x.dim() == 3 else 0
+    a = _out(a, "a", (*x.shape[:-1], k // 2), torch.uint8, device)
+    sfa = _out(sfa, "sfa", (nvfp4_sf_bytes(m, k, l),), torch.uint8, device)
+    if l:
+        with _On(device, stream) as s:
+            c.nvfp4_moe_quantize(x.data_ptr(), kind, l, m, k, batch, stride, scale, a.data_ptr(), sfa.data_ptr(), s)
+    return a, sfa
+
+
+def swiglu_quantize(x, *, plan=None, alpha=None, scale=1.0, a=None, sfa=None, stream=None):
+    """NVFP4 codes and scales of ``silu(g * alpha) * (u * alpha) * scale``, g and u the halves of each row of ``x``
+    [rows, 2k]: rows of one group, or with a plan rows sorted by expert, ``alpha`` [experts] (fp32) by expert."""
+    device = _gpu(x, "x")
+    stride = _rows(x, "x")
+    rows, k = x.shape[0], x.shape[1] // 2
+    if x.shape[1] % 64:
+        raise ValueError(f"the halves of a row must have a multiple of 32 elements (row of {x.shape[1]})")
+    experts = 1 if plan is None else plan.experts
+    if plan is not None and (rows != plan.rows or plan.ids.device != device):
+        raise ValueError(f"x must have the plan's {plan.rows} rows, on its device")
+    if alpha is not None:
+        _like(alpha, "alpha", (experts,), torch.float32, device)
+    a = _out(a, "a", (rows, k // 2), torch.uint8, device)
+    sfa = _out(sfa, "sfa", (nvfp4_sf_bytes(rows, k) if plan is None else c.nvfp4_moe_sf_bytes(rows, experts, k),),
+               torch.uint8, device)
+    with _On(device, stream) as s:
+        c.nvfp4_moe_swiglu(x.data_ptr(), _type(x, "x"), rows, k, stride, _at(alpha), scale,
+                           0 if plan is None else plan.offsets.data_ptr(), 0 if plan is None else plan.atoms.data_ptr(),
+                           experts, a.data_ptr(), sfa.data_ptr(), s)
+    return a, sfa
+
+
+def dequantize(a, sfa, *, plan=None, dtype=torch.float16, out=None, stream=None):
+    """The values that NVFP4 rows stand for: a [m, k/2] or [l, m, k/2] -> [..., k]. With a plan, of rows sorted by
+    expert; rows that no slot has are not written."""
+    device = _gpu(a, "a")
+    if a.dim() not in (2, 3) or (plan is not None and a.dim() != 2):
+        raise ValueError(f"a must have shape [m, k/2] (or, without a plan, [l, m, k/2]), not {tuple(a.shape)}")
+    _like(a, "a", a.shape, torch.uint8, device)
+    l, m, k = a.shape[0] if a.dim() == 3 else 1, a.shape[-2], 2 * a.shape[-1]
+    if plan is not None and (m != plan.rows or plan.ids.device != device):
+        raise ValueError(f"a must have the plan's {plan.rows} rows, on its device")
+    need = nvfp4_sf_bytes(m, k, l) if plan is None else c.nvfp4_moe_sf_bytes(m, plan.experts, k)
+    _like(sfa, "sfa", (need,), torch.uint8, device)
+    if out is not None:
+        dtype = out.dtype
+    out = _out(out, "out", (*a.shape[:-1], k), dtype, device)
+    if l:
+        with _On(device, stream) as s:
+            c.nvfp4_moe_dequantize(a.data_ptr(), sfa.data_ptr(), l, m, k, 0 if plan is None else plan.offsets.data_ptr(),
+                                   0 if plan is None else plan.atoms.data_ptr(), 1 if plan is None else plan.experts,
+                                   out.data_ptr(), _type(out, "out"), k, s)
+    return out
+
+
+# ---- the combine ----------------------------------------------------------------------
+
+def _slots(weights, rows, alpha, ids, slots_of, device):
+    """Checked (tokens, topk, row address, ids) of a combine's slots; ``rows`` a Plan, a tensor or None."""
+    if isinstance(rows, Plan):
+        ids, rows = rows.ids, rows.slot_rows
+    given = weights if weights is not None else rows
+    if given is None or given.dim() != 2:
+        raise ValueError("weights or rows must have shape [tokens, topk]")
+    shape = given.shape
+    if weights is not None:
+        _like(weights, "weights", shape, torch.float32, device)
+    if rows is not None:
+        _like(rows, "rows", shape, torch.int32, device)
+    elif slots_of.shape[0] != shape[0] * shape[1]:
+        raise ValueError(f"without rows, c must have a row for each of the {shape[0] * shape[1]} slots")
+    if ids is not None:
+        _like(ids, "ids", shape, torch.int32, device)
+    if alpha is not None:
+        if ids is None:
+            raise ValueError("alpha needs ids")
+        _like(alpha, "alpha", (alpha.shape[0],), torch.float32, device)
+    return shape[0], shape[1], rows, ids
+
+
+def combine(x, weights, rows=None, *, alpha=None, ids=None, residual=None, dtype=None, out=None, stream=None):
+    """``out[t] = residual[t] + sum_j weights[t, j] * alpha[ids[t, j]] * x[rows[t, j]]``, summed in fp32 in slot order.
+
+    ``x`` [rows, n]: the experts' rows; ``rows``: a Plan, int32 [tokens, topk] (-1: no row), or None where the slots'
+    rows follow each other; ``weights`` fp32 [tokens, topk] or None for 1. ``dtype`` of the result: that of ``out``
+    or ``residual``, else x's."""
+    device = _gpu(x, "x")
+    stride = _rows(x, "x")
+    n = x.shape[1]
+    tokens, topk, rows, ids = _slots(weights, rows, alpha, ids, x, device)
+    if dtype is None:
+        dtype = out.dtype if out is not None else residual.dtype if residual is not None else x.dtype
+    out = _out(out, "out", (tokens, n), dtype, device)
+    if residual is not None:
+        _like(residual, "residual", (tokens, n), dtype, device)
+    with _On(device, stream) as s:
+        c.nvfp4_moe_combine(x.data_ptr(), _type(x, "x"), stride, tokens, topk, n, _at(rows), _at(weights), _at(alpha),
+                            _at(ids), _at(residual), out.data_ptr(), _type(out, "out"), n, s)
+    return out
+
+
+def combine_backward(dy, x, weights, rows=None, *, alpha=None, ids=None, dc=None, stream=None):
+    """(d x, d weights) of ``combine``; rows of d x that no slot has are not written."""
+    device = _gpu(x, "x")
+    stride = _rows(x, "x")
+    tokens, topk, rows, ids = _slots(weights, rows, alpha, ids, x, device)
+    dy_stride = _rows(dy, "dy", x.shape[1])
+    if dy.shape[0] != tokens or dy.device != device:
+        raise ValueError(f"dy must have {tokens} rows, on {device}")
+    if dc is None:
+        dc = torch.empty_strided(x.shape, (stride, 1), dtype=x.dtype, device=device)
+    elif dc.shape != x.shape or dc.dtype != x.dtype or dc.device != device or _rows(dc, "dc") != stride:
+        raise ValueError("dc must have x's shape, strides, type and device")
+    dweights = torch.empty((tokens, topk), dtype=torch.float32, device=device)
+    with _On(device, stream) as s:
+        c.nvfp4_moe_combine_backward(dy.data_ptr(), _type(dy, "dy"), dy_stride, x.data_ptr(), _type(x, "x"), stride, tokens,
+                                     topk, x.shape[1], _at(rows), _at(weights), _at(alpha), _at(ids), dc.data_ptr(),
+                                     dweights.data_ptr(), s)
+    return dc, dweights
+
+
+# ---- a few tokens ------------------------------------------------------------------------
+
+def few_tokens(x, ids, b, sfb, *, alpha=None, swiglu=False, dtype=None, out=None, stream=None):
+    """The experts' products of a few tokens: out [tokens, topk, n] = alpha[id] * b[id] . x, and with ``swiglu``
+    silu of the first half times the second, [tokens, topk, n/2].
+
+    ``x`` (fp16 or bf16) [tokens, k], or [tokens, topk, k] with a row for each slot; ``ids`` int32 [tokens, topk];
+    ``b``, ``sfb``: stacked NVFP4 weights. Slots without an expert give zeros."""
+    device = _gpu(x, "x")
+    if ids.dim() != 2:
+        raise ValueError(f"ids must have shape [tokens, topk], not {tuple(ids.shape)}")
+    tokens, topk = ids.shape
+    _like(ids, "ids", ids.shape, torch.int32, device)
+    b, sfb = _operand(b, sfb)
+    experts, n, k = b.shape[0], b.shape[1], 2 * b.shape[2]
+    if x.dim() == 3:
+        _like(x, "x", (tokens, topk, k), x.dtype, device)
+        stride = k
+    else:
+        stride = _rows(x, "x", k)
+        if x.shape[0] != tokens:
+            raise ValueError(f"x must have {tokens} rows, not {x.shape[0]}")
+    if b.device != device:
+        raise ValueError(f"b must be on {device}")
+    if alpha is not None:
+        _like(alpha, "alpha", (experts,), torch.float32, device)
+    if dtype is None:
+        dtype = x.dtype if out is None else out.dtype
+    out = _out(out, "out", (tokens, topk, n // 2 if swiglu else n), dtype, device)
+    with _On(device, stream) as s:
+        c.nvfp4_moe_few_tokens(x.data_ptr(), _type(x, "x"), stride, x.dim() == 3, ids.data_ptr(), tokens, topk, experts, n, k,
+                               b.data_ptr(), sfb.data_ptr(), _at(alpha), bool(swiglu), out.data_ptr(), _type(out, "out"), s)
+    return out
+
+
+# ---- the layer ---------------------------------------------------------------------------
+
+class FeedForward:
+    """The experts' gated feed-forward with NVFP4 weights:
+    ``y[t] = sum_j w[t, j] * down[e] . (silu(gate[e] . x[t]) * (up[e] . x[t]))``, e = ids[t, j].
+
+    ``b1``, ``sfb1``: gate rows, then up rows, [experts, 2 * inner, hidden / 2]; ``b2``, ``sfb2``: [experts, hidden,
+    inner / 2]; ``alpha1``, ``alpha2``: factors on each expert's products (fp32 [experts])."""
+
+    #: up to this many slots an expert's product reads the weights once and the activations are not quantised
+    FEW_SLOTS = 64
+
+    def __init__(self, b1, sfb1, b2, sfb2, *, alpha1=None, alpha2=None):
+        (self.b1, self.sfb1), (self.b2, self.sfb2) = _operand(b1, sfb1), _operand(b2, sfb2)
+        self.experts, self.hidden, self.inner = b1.shape[0], 2 * b1.shape[2], 2 * b2.shape[2]
+        if tuple(b1.shape[:2]) != (b2.shape[0], 2 * self.inner) or b2.shape[1] != self.hidden or b1.device != b2.device:
+            raise ValueError(f"b1 {tuple(b1.shape)} and b2 {tuple(b2.shape)} do not fit together")
+        self.alpha1, self.alpha2 = alpha1, alpha2
+
+    def __call__(self, x, ids, weights, *, residual=None, stream=None):
+        """y [tokens, hidden] of ``x``'s type, by the products that suit the number of tokens."""
+        run = self.few if ids.numel() <= self.FEW_SLOTS and x.dtype != torch.float32 else self.grouped
+        return run(x, ids, weights, residual=residual, stream=stream)
+
+    def few(self, x, ids, weights, *, residual=None, stream=None):
+        h = few_tokens(x, ids, self.b1, self.sfb1, alpha=self.alpha1, swiglu=True, stream=stream)
+        y = few_tokens(h, ids, self.b2, self.sfb2, alpha=self.alpha2, stream=stream)
+        return combine(y.view(-1, self.hidden), weights, ids=ids, residual=residual, dtype=x.dtype, stream=stream)
+
+    def grouped(self, x, ids, weights, *, residual=None, stream=None):
+        rows, device, e = ids.numel(), self.b1.device, self.experts
+        new = lambda *shape, dtype=torch.uint8: torch.empty(shape, dtype=dtype, device=device)  # noqa: E731
+        first = Product(new(rows, self.hidden // 2), new(c.nvfp4_moe_sf_bytes(rows, e, self.hidden)), self.b1, self.sfb1,
+                        new(rows, 2 * self.inner, dtype=torch.float16))
+        second = Product(new(rows, self.inner // 2), new(c.nvfp4_moe_sf_bytes(rows, e, self.inner)), self.b2, self.sfb2,
+                         new(rows, self.hidden, dtype=torch.float16))
+        p = plan(ids, e, (first, second), stream=stream)
+        quantize(x, plan=p, a=first.a, sfa=first.sfa, stream=stream)
+        tile = self._tile(rows)
+        swiglu_quantize(first.run(tile, stream=stream), plan=p, alpha=self.alpha1, a=second.a, sfa=second.sfa, stream=stream)
+        return combine(second.run(tile, stream=stream), weights, p, alpha=self.alpha2, residual=residual, dtype=x.dtype,
+                       stream=stream)
+
+    def _tile(self, rows):
+        """The grouped GEMM's tile configuration for an expert's mean number of rows."""
+        mean = rows // self.experts
+        return 4 if mean <= 64 else 3 if mean <= 128 else 2
