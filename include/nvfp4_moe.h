@@ -226,7 +226,8 @@ int nvfp4_moe_combine_backward(const void* dy, int dy_dtype, int64_t dy_stride, 
  *   x      device [tokens][k], or with per_slot [tokens*topk][k], rows x_stride apart
  *   b, sfb device uint8 [experts][n][k/2] and [experts][nvfp4_sf_bytes(n, k, 1)], 16-byte aligned
  *   out    device [tokens*topk][n, or n/2 with swiglu] of out_dtype, rows without gaps
- * tokens * topk <= NVFP4_MOE_MAX_FEW_SLOTS; k % 32 == 0; n % 8 == 0 (swiglu: n % 16 == 0).
+ * tokens * topk <= NVFP4_MOE_MAX_FEW_SLOTS; k % 32 == 0; n % 8 == 0
+ * (swiglu: n % 16 == 0); the codes of an expert below 2^31 bytes.
  */
 int nvfp4_moe_few_tokens(const void* x, int dtype, int64_t x_stride, int per_slot, const int32_t* ids,
                          int64_t tokens, int topk, int experts, int n, int k, const void* b, const void* sfb,

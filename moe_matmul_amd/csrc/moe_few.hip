@@ -5,10 +5,18 @@
 namespace moe {
 namespace {
 
-constexpr int kWaves = 8;
+constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
-constexpr int kStep = 128;       // K-elements of a step: 32 (16 bytes of codes) for each of a wave's four lane groups
-constexpr int kStageItems = 4;   // 16-byte pieces of x that a lane stages at a time
+constexpr int kStep = 256;    // K-elements of a step: 128 bytes of a weight row, and four scale atoms
+constexpr int kStepBytes = kStep / 2;
+constexpr int kPieces = kStepBytes / 16;  // 16-byte pieces of a row's step
+constexpr int kDepth = 2;     // steps of weights in flight, in registers
+constexpr int kMinWaves = 3;
+constexpr int kHold = 4;      // pieces of x that a thread has under way
+constexpr int kMaxRows = 16;  // slots of a pass: rows of the matrix instruction
+constexpr int kStageElements = 16384;  // of x in shared memory, at most (32 KB)
+constexpr int kEnoughWaves = 768;
+constexpr int kPad = 8;       // elements after a staged row: rows start in different banks
 
 struct FewArgs {
   const void* x;
@@ -18,8 +26,13 @@ struct FewArgs {
   const float* alpha;
   void* out;
   int slots, topk, per_slot, experts, n, k, x_vec, out_dtype;
-  int columns;  // of out
-  int tiles;    // workgroups of a slot
+  int columns;    // of out
+  int tiles;      // workgroups of an expert
+  int by_expert;  // a workgroup's expert is its number (else that of the slot of that number)
+  int stage;      // elements of x that fit in shared memory, with their padding
+  int rows;       // slots of a pass: 1, 2, 4, 8 or 16
+  int slots_at;   // where the slots of the expert lie after that, in bytes
+  int k_waves;    // waves that share K; the others of a workgroup have other columns
 };
 
 // Eight codes of one dword times their scale, as f16: both factors and the
@@ -33,265 +46,394 @@ __device__ inline f16x8 dequant8(uint32_t w, _Float16 s) {
   return f16x8{p0.x, p0.y, p1.x, p1.y, p2.x, p2.y, p3.x, p3.y};
 }
 
-// What a lane reads for one K-step: 32 codes of each of its weight rows, and the
-// scale words of those rows.
-template <int SUB> struct Weights {
-  u32x4 codes[SUB];
-  uint32_t scales[SUB];
+// What a lane reads for one K-step of U runs of 16 weight rows: codes as they
+// lie in memory, eight lanes to the 128 bytes of a row, and the word of four
+// scales of the row and atom that the lane multiplies.
+template <int U> struct Weights {
+  u32x4 codes[U][2];
+  uint32_t scales[U];
 };
 
-// A lane's weight rows of a tile: SUB of them, 32 apart, so that (from a row
-// that is a multiple of 32 * SUB, plus 0 .. 31) their scales lie side by side in
-// the tiled layout.
-template <int SUB> struct Operand {
-  const uint8_t* codes[SUB];   // at this lane's K offset
-  const uint8_t* scales[SUB];  // the words of this lane's first atom
+// N words at an address that is a multiple of their size.
+template <int N> __device__ inline void load_words(const uint8_t* p, uint32_t* w) {
+  typedef uint32_t words __attribute__((ext_vector_type(N)));
+  const words v = *(const words*)p;
+#pragma unroll
+  for (int i = 0; i < N; ++i) w[i] = v[i];
+}
 
-  __device__ inline void at(const FewArgs& a, int expert, int row0, int lane) {
-    const int group = lane / 16, kt = ceil_div(a.k, kAtomK);
-    const int64_t atom0 = (int64_t)expert * ceil_div(a.n, kAtomRows);
+// A wave's weight rows: H halves of SUB runs of 16 rows. The runs of a half are
+// 32 rows apart, where the tiled layout has their scales side by side. The
+// matrix instruction wants a run's row lane % 16 in a lane, K-elements lane / 16
+// * 64 .. + 63 of the step; loaded like that, a quarter of a wave would touch 16
+// cache lines for 16 bytes each, and the address unit, not memory, would set
+// the pace (16 x 16-byte pieces a load: 3.3 TB/s). So rows are loaded whole
+// lines at a time and change lanes through shared memory.
+template <int H, int SUB> struct Operand {
+  static constexpr int U = H * SUB;
+  const uint8_t *codes, *scales;       // of the expert
+  uint32_t row_at[U][2], scale_at[U];  // bytes: of the rows that this lane loads (lane / 8 and + 8), and multiplies
+  int last_code, last_atom, lane;
+  bool apart;  // a half does not begin at a multiple of 32 * SUB rows: its runs' scales do not lie together
+
+  // Lanes past the end of K read its end; x is 0 there, and scales() makes their scales 0.
+  __device__ inline Weights<U> load(int step) const {
+    Weights<U> w;
+    const uint32_t code = min(step * kStepBytes + lane % 8 * 16, last_code);
+    const uint32_t scale = min(step * (kStep / kAtomK) + lane / 16, last_atom) * kAtomBytes;
 #pragma unroll
-    for (int s = 0; s < SUB; ++s) {
-      const int row = min(row0 + 32 * s + lane % 16, a.n - 1);  // columns past n are computed and dropped
-      codes[s] = a.b + ((int64_t)expert * a.n + row) * (a.k / 2) + group * 16;
-      scales[s] = a.sfb + ((atom0 + row / kAtomRows) * kt + group / 2) * kAtomBytes + atom_row(row % kAtomRows);
-    }
-  }
-  __device__ inline Weights<SUB> load(const FewArgs& a, int step, int lane) const {
-    Weights<SUB> w;
-    const bool there = step * kStep + lane / 16 * 32 < a.k;
-    const int64_t code = (int64_t)step * (kStep / 2), scale = (int64_t)step * (kStep / kAtomK) * kAtomBytes;
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-    for (int s = 0; s < SUB; ++s) {
-      w.codes[s] = there ? *(const u32x4*)(codes[s] + code) : u32x4{0u, 0u, 0u, 0u};
-      w.scales[s] = there ? *(const uint32_t*)(scales[s] + scale) : 0u;
+      for (int i = 0; i < 2; ++i) w.codes[u][i] = __builtin_nontemporal_load((const u32x4*)(codes + (row_at[u][i] + code)));
+    if (H == 1 || !apart) {
+#pragma unroll
+      for (int h = 0; h < H; ++h) load_words<SUB>(scales + (scale_at[h * SUB] + scale), w.scales + h * SUB);
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u) load_words<1>(scales + (scale_at[u] + scale), w.scales + u);
     }
     return w;
   }
+  // Which bytes of a scale word lie within K.
+  __device__ inline uint32_t scale_mask(int step) const {
+    const int atom = step * (kStep / kAtomK) + lane / 16;
+    return atom < last_atom ? ~0u : atom > last_atom ? 0u : last_code % (kAtomK / 2) == 0 ? 0xFFFFu : ~0u;
+  }
 };
 
-// A workgroup computes a tile of weight rows (SWIGLU: the tile's rows of both
-// halves) for all slots of one expert, MT of them at a time; its eight waves
-// split K. The first slot of an expert does the work of all of them, the others
-// leave at once, so no order of slots has to be made before. Weights go from
-// memory to registers, two steps ahead; a wave's part of x goes through its own
-// shared memory, as f16. bf16 rows are scaled by a power of two for that, which
-// brings the largest of a wave's part of a row to 2^14 .. 2^15: all elements down
-// to 2^-32 of it keep their eight bits, and what smaller ones lose is below
-// 2^-39 of it, far under the rounding of the fp32 sums. Waves' sums are joined
-// in shared memory, in wave order.
-template <class X, int SUB, bool SWIGLU, int MT>
-__global__ void __launch_bounds__(kThreads) nvfp4_few_tokens_kernel(FewArgs a) {
-  constexpr int kStageK = kStageItems * 64 * 8 / MT;           // K-elements of a stage
-  constexpr int kStageRow = kStageK + 8;                       // padded: rows start in different banks
-  constexpr int kHalves = SWIGLU ? 2 : 1;
-  constexpr int kStageBytes = kWaves * MT * kStageRow * 2;
-  constexpr int kTileN = 16 * SUB;
-  constexpr int kSumBytes = kWaves * MT * kTileN * 4;
-  __shared__ __attribute__((aligned(16))) uint8_t s_shared[kStageBytes > kSumBytes ? kStageBytes : kSumBytes];
-  __shared__ uint16_t s_slots[NVFP4_MOE_MAX_FEW_SLOTS];
-  __shared__ float s_unscale[kWaves][MT];
-  __shared__ int s_count;
+// Where the 16-byte piece p of row r of a run's step lies in shared memory, in
+// pieces: without bank conflicts for the eight lanes that write a row, and for
+// 16 lanes that read a piece of 16 rows.
+__device__ inline int piece_at(int r, int p) { return r * kPieces + (p ^ (r / 2 & 7)); }
 
-  const int slot = blockIdx.x / a.tiles, tile = blockIdx.x % a.tiles;
-  const int wave = threadIdx.x / 64, lane = threadIdx.x & 63;
-  // tile -> its first weight row: runs of 16 rows that are 32 apart, within 32 * SUB rows
-  const int row0 = tile / 2 * (32 * SUB) + tile % 2 * 16;
-  const int expert = a.ids[slot];
-  if ((unsigned)expert >= (unsigned)a.experts) {
-    for (int i = threadIdx.x; i < kTileN; i += kThreads) {
+__device__ inline void store_any(void* out, int dtype, int64_t at, float y) {
+  if (dtype == NVFP4_MOE_F32) store1<F32>(out, at, y);
+  else if (dtype == NVFP4_MOE_F16) store1<F16>(out, at, y);
+  else store1<BF16>(out, at, y);
+}
+
+// The largest of a wave's values, in lane 63: along rows of 16 lanes, then from row to row.
+template <int kCtrl> __device__ inline uint32_t max_from(uint32_t v) {
+  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kCtrl, 0xF, 0xF, true));
+}
+__device__ inline uint32_t wave_max(uint32_t v) {
+  v = max_from<0x111>(v);  // row_shr 1, 2, 4, 8
+  v = max_from<0x112>(v);
+  v = max_from<0x114>(v);
+  v = max_from<0x118>(v);
+  v = max_from<0x142>(v);  // row_bcast 15, 31
+  return max_from<0x143>(v);
+}
+
+// The exponent field of the power of two that brings a row's largest element to
+// 2^14 .. 2^15, within what fp32 has.
+__device__ inline int scale_up(uint32_t top) { return min(max(127 + 14 + 127 - (int)(top >> 7), 1), 253); }
+
+// A workgroup computes some columns of all slots of one expert, `rows` of them
+// at a time; its four waves split the columns, K, or both. The workgroups find
+// the expert's slots themselves, so no order of slots has to be made before.
+//
+// Weights go from memory to registers, kDepth steps ahead, the first of them
+// before anything else is read but the expert's number. x is staged in shared
+// memory as f16. bf16 rows are scaled by a power of two for that, which
+// brings the largest element of a row so far to 2^14 .. 2^15: elements down to
+// 2^-32 of it keep their eight bits, and what smaller ones lose is below 2^-39
+// of it, far under the rounding of the fp32 sums. Sums over waves are formed in
+// wave order.
+template <class X, int U, bool SWIGLU>
+__global__ void __launch_bounds__(kThreads, kMinWaves) nvfp4_few_tokens_kernel(FewArgs a) {
+  constexpr int H = SWIGLU ? 2 : 1, SUB = U / H;
+  constexpr bool kScaled = X::kId == NVFP4_MOE_BF16;
+  extern __shared__ __attribute__((aligned(16))) uint8_t s_shared[];
+  __shared__ u32x4 s_codes[kWaves][U * 16 * kPieces];
+  __shared__ uint32_t s_top[kMaxRows];  // a row's largest element so far, without its sign
+
+  uint16_t* s_slots = (uint16_t*)(s_shared + a.slots_at);
+
+  const int which = blockIdx.x / a.tiles, tile = blockIdx.x % a.tiles;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x & 63;
+  const int k_wave = wave % a.k_waves;
+  // a wave's tile number -> its first weight row: runs of 16 rows, 32 apart, within 32 * SUB rows
+  const int wave_tile = tile * (kWaves / a.k_waves) + wave / a.k_waves;
+  const int row0 = wave_tile / 2 * (32 * SUB) + wave_tile % 2 * 16;
+  const int expert = a.by_expert ? which : a.ids[which];
+
+  // a slot without an expert gives zeros: from its own workgroups, or from those of expert 0
+  auto zero_slot = [&](int slot) {
+    for (int i = lane; i < 16 * SUB; i += 64) {
       const int col = row0 + i / 16 * 32 + i % 16;
-      if (col >= a.columns) continue;
-      const int64_t at = (int64_t)slot * a.columns + col;
-      if (a.out_dtype == NVFP4_MOE_F32) store1<F32>(a.out, at, 0.f);
-      else store1<F16>(a.out, at, 0.f);  // zero has the same bits in bf16
+      if (k_wave == 0 && col < a.columns) store_any(a.out, a.out_dtype, (int64_t)slot * a.columns + col, 0.f);
     }
+  };
+  if (!a.by_expert && (unsigned)expert >= (unsigned)a.experts) {
+    zero_slot(which);
     return;
   }
-  // the slots of this expert, in order
-  if (wave == 0) {
-    int count = 0;
-    for (int i0 = 0; i0 < a.slots; i0 += 64) {
-      const bool mine = i0 + lane < a.slots && a.ids[i0 + lane] == expert;
-      const uint64_t all = __ballot(mine);
-      if (mine) s_slots[count + __popcll(all & ((1ull << lane) - 1))] = (uint16_t)(i0 + lane);
-      count += __popcll(all);
-    }
-    if (lane == 0) s_count = count;
+
+  // Weights: rows past n are read from the last row, computed and dropped.
+  Operand<H, SUB> operand;
+  operand.last_code = a.k / 2 - 16;
+  operand.last_atom = ceil_div(a.k, kAtomK) - 1;
+  operand.lane = lane;
+  operand.apart = a.n / H % (32 * SUB) != 0;
+  const int kt = ceil_div(a.k, kAtomK);
+  operand.codes = a.b + (int64_t)expert * a.n * (a.k / 2);
+  operand.scales = a.sfb + (int64_t)expert * ceil_div(a.n, kAtomRows) * kt * kAtomBytes;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int run = (row0 < a.columns ? row0 : 0) + u % SUB * 32 + u / SUB * (a.n / H);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) operand.row_at[u][i] = (uint32_t)min(run + i * 8 + lane / 8, a.n - 1) * (a.k / 2);
+    // scales of runs that lie together are padded to whole atoms: their rows may pass n
+    const int row = H == 2 && operand.apart ? min(run + lane % 16, a.n - 1) : run + lane % 16;
+    operand.scale_at[u] = (uint32_t)(row / kAtomRows * kt) * kAtomBytes + atom_row(row % kAtomRows);
   }
-  __syncthreads();
-  const int count = s_count;
-  if (s_slots[0] != slot) return;
-
-  Operand<SUB> operand[kHalves];
+  // This wave's K-steps, and where its weights go ahead.
+  const int steps = ceil_div(a.k, kStep);
+  const int first = steps * k_wave / a.k_waves, last = steps * (k_wave + 1) / a.k_waves;
+  Weights<U> ahead[kDepth];
+  auto prefetch = [&] {
 #pragma unroll
-  for (int h = 0; h < kHalves; ++h) operand[h].at(a, expert, row0 + h * (a.n / 2), lane);
-  const int steps = ceil_div(a.k, kStep), first = steps * wave / kWaves, last = steps * (wave + 1) / kWaves;
-  _Float16* stage = (_Float16*)s_shared + wave * MT * kStageRow;
+    for (int d = 0; d < kDepth; ++d) ahead[d] = operand.load(min(first + d, steps - 1));
+  };
+  if (steps > 0) prefetch();
 
-  for (int from = 0; from < count; from += MT) {
-    const int rows = min(MT, count - from);
-    // this lane's pieces of a stage: piece p is 8 elements, kStageK / 8 pieces to a row
-    int64_t base[kStageItems];
-    int piece_k[kStageItems];
-#pragma unroll
-    for (int i = 0; i < kStageItems; ++i) {
-      const int p = i * 64 + lane, r = p / (kStageK / 8);
-      const int s = s_slots[from + min(r, rows - 1)];
-      base[i] = (int64_t)(a.per_slot ? s : s / a.topk) * a.x_stride;
-      piece_k[i] = p % (kStageK / 8) * 8;
+  // the slots of this expert, in order
+  int count = 0, first_slot = -1;
+  for (int i0 = 0; i0 < a.slots; i0 += 64) {
+    const int id = i0 + lane < a.slots ? a.ids[i0 + lane] : a.experts;
+    const bool mine = id == expert;
+    const uint64_t all = __ballot(mine);
+    if (a.by_expert && which == 0) {
+      uint64_t none = __ballot(i0 + lane < a.slots && (unsigned)id >= (unsigned)a.experts);
+      for (; none != 0; none &= none - 1) zero_slot(i0 + __builtin_ctzll(none));
     }
-    auto load_piece = [&](int i, int k0) {
-      const int k = k0 + piece_k[i];
-      u32x4 v = {0u, 0u, 0u, 0u};
-      if (k < a.k) {
-        const uint16_t* p = (const uint16_t*)a.x + base[i] + k;
-        if (a.x_vec) {
-          v = *(const u32x4*)p;
-        } else {
+    if (all == 0) continue;
+    if (first_slot < 0) {
+      first_slot = i0 + __builtin_ctzll(all);
+      // only the first slot's workgroups do the work
+      if (!a.by_expert && first_slot != which) return;
+    }
+    if (wave == 0 && mine) s_slots[count + __popcll(all & ((1ull << lane) - 1))] = (uint16_t)(i0 + lane);
+    count += __popcll(all);
+  }
+  if (count == 0) return;
+  if (threadIdx.x < kMaxRows) s_top[threadIdx.x] = 0;
+  __syncthreads();
+
+  // A stage holds the next `part` steps of every K-wave, for the slots of a pass.
+  int row_space = 1;
+  while (row_space < a.rows && row_space < count) row_space *= 2;
+  const int most = ceil_div(ceil_div(steps, a.k_waves), kDepth) * kDepth;
+  const int part = min(a.stage / (row_space * a.k_waves * kStep) / kDepth * kDepth, most);
+  const int pieces = a.k_waves * part * (kStep / 8), stage_row = pieces * 8 + kPad;
+  const int row_waves = row_space < kWaves ? kWaves / row_space : 1, turns = ceil_div(pieces, 64 * row_waves);
+  _Float16* stage = (_Float16*)s_shared;
+
+  for (int from = 0; from < count; from += a.rows) {
+    const int rows = min(a.rows, count - from);
+    f32x4 sum[U];
+    int up[4] = {253, 253, 253, 253};  // scales of this lane's rows so far
 #pragma unroll
-          for (int j = 0; j < 4; ++j) v[j] = p[2 * j] | (uint32_t)p[2 * j + 1] << 16;
-        }
-      }
-      return v;
-    };
-    const int k_end = last * kStep;
-    float scale[kStageItems];
-    if constexpr (X::kId == NVFP4_MOE_BF16) {
-      uint32_t top[kStageItems] = {};
-      for (int k0 = first * kStep; k0 < k_end; k0 += kStageK) {
+    for (int u = 0; u < U; ++u) sum[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+    int step = first;
+    for (int done = 0; done < most; done += part) {
+      // x, in pieces of 8 elements. A row's pieces go to `row_waves` waves, 64 at a time. bf16 rows are gone through
+      // twice: for their largest elements, and to be scaled. In between, a thread's pieces stay in registers if they
+      // are kHold or fewer; else they are read again (from a cache).
+      const int part_pieces = part * (kStep / 8);
+      const bool held = turns * ceil_div(rows * row_waves, kWaves) <= kHold;
+      u32x4 v[kHold];
+      auto each_piece = [&](bool load, auto&& use) {  // use(row, piece, its elements)
+        int row = wave / row_waves, turn = 0;
+        while (row < rows) {
+          const int row_before = row, turn_before = turn;
+          if (load) {
 #pragma unroll
-        for (int i = 0; i < kStageItems; ++i) {
-          const u32x4 v = k0 + piece_k[i] < k_end ? load_piece(i, k0) : u32x4{0u, 0u, 0u, 0u};
+            for (int h = 0; h < kHold; ++h) {
+              const int i = (turn * row_waves + wave % row_waves) * 64 + lane;
+              const int w = (i >= part_pieces) + (i >= 2 * part_pieces) + (i >= 3 * part_pieces);  // its K-wave
+              const int k = (steps * w / a.k_waves + done) * kStep + (i - w * part_pieces) * 8;
+              v[h] = u32x4{0u, 0u, 0u, 0u};
+              if (row < rows && i < pieces && k < a.k) {
+                const int slot = s_slots[from + row];
+                const uint16_t* x = (const uint16_t*)a.x + (int64_t)(a.per_slot ? slot : slot / a.topk) * a.x_stride;
+                if (a.x_vec) {
+                  v[h] = *(const u32x4*)(x + k);
+                } else {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t low = v[j] & 0x7FFFu, high = v[j] >> 16 & 0x7FFFu;
-            top[i] = max(top[i], max(low < 0x7F80u ? low : 0u, high < 0x7F80u ? high : 0u));
+                  for (int j = 0; j < 4; ++j) v[h][j] = x[k + 2 * j] | (uint32_t)x[k + 2 * j + 1] << 16;
+                }
+              }
+              if (++turn == turns) {
+                turn = 0;
+                row += kWaves / row_waves;
+              }
+            }
+          }
+          row = row_before;
+          turn = turn_before;
+#pragma unroll
+          for (int h = 0; h < kHold; ++h) {
+            if (row < rows) use(row, (turn * row_waves + wave % row_waves) * 64 + lane, v[h]);
+            if (++turn == turns) {
+              turn = 0;
+              row += kWaves / row_waves;
+            }
           }
         }
+      };
+      if constexpr (kScaled) {
+        each_piece(true, [&](int r, int, u32x4 v) {
+          uint32_t top = 0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t low = v[j] & 0x7FFFu, high = v[j] >> 16 & 0x7FFFu;  // infinities and NaNs do not count
+            top = max(top, max(low < 0x7F80u ? low : 0u, high < 0x7F80u ? high : 0u));
+          }
+          top = wave_max(top);
+          if (lane == 63) atomicMax(&s_top[r], top);
+        });
+        __syncthreads();
       }
-#pragma unroll
-      for (int i = 0; i < kStageItems; ++i) {
-        for (int d = 1; d < kStageK / 8 && d < 64; d *= 2) top[i] = max(top[i], (uint32_t)__shfl_xor((int)top[i], d));
-        // 2^(14 - exponent of the largest), within what fp32 has
-        const int up = min(max(127 + 14 + 127 - (int)(top[i] >> 7), 1), 253);
-        scale[i] = __builtin_bit_cast(float, (uint32_t)up << 23);
-        const int p = i * 64 + lane;
-        if (p % (kStageK / 8) == 0) s_unscale[wave][p / (kStageK / 8)] = __builtin_bit_cast(float, (uint32_t)(254 - up) << 23);
-      }
-    }
-
-    f32x4 sum[kHalves][SUB];
-#pragma unroll
-    for (int h = 0; h < kHalves; ++h)
-#pragma unroll
-      for (int s = 0; s < SUB; ++s) sum[h][s] = f32x4{0.f, 0.f, 0.f, 0.f};
-    Weights<SUB> next[kHalves];
-#pragma unroll
-    for (int h = 0; h < kHalves; ++h) next[h] = operand[h].load(a, first, lane);
-
-    for (int k0 = first * kStep; k0 < k_end; k0 += kStageK) {
-      // stage x as f16; the wave's reads of the stage before are done (they were waited for by their MFMAs)
-#pragma unroll
-      for (int i = 0; i < kStageItems; ++i) {
-        u32x4 v = load_piece(i, k0);
-        if constexpr (X::kId == NVFP4_MOE_BF16) {
+      each_piece(!kScaled || !held, [&](int r, int i, u32x4 v) {
+        if (i >= pieces) return;
+        if constexpr (kScaled) {
+          const float scale = __builtin_bit_cast(float, (uint32_t)scale_up(s_top[r]) << 23);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             float lo, hi;
             unpack2<BF16>(v[j], lo, hi);
-            v[j] = pack2<F16>(lo * scale[i], hi * scale[i]);
+            v[j] = pack2<F16>(lo * scale, hi * scale);
           }
         }
-        *(u32x4*)(stage + (i * 64 + lane) / (kStageK / 8) * kStageRow + piece_k[i]) = v;
-      }
-      wave_sync();
-      const int here = min(kStageK, k_end - k0) / kStep;
-      for (int t = 0; t < here; ++t) {
-        Weights<SUB> w[kHalves];
-        const int step = k0 / kStep + t;
-#pragma unroll
-        for (int h = 0; h < kHalves; ++h) {
-          w[h] = next[h];
-          if (step + 1 < last) next[h] = operand[h].load(a, step + 1, lane);
-        }
-        f16x8 xs[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          xs[j] = *(const f16x8*)(stage + lane % 16 % MT * kStageRow + t * kStep + lane / 16 * 32 + j * 8);
-#pragma unroll
-        for (int h = 0; h < kHalves; ++h)
-#pragma unroll
-          for (int s = 0; s < SUB; ++s) {
-            const f16x2 sc = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[h].scales[s] >> (lane / 16 % 2 * 16), 1.f, false);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              sum[h][s] = __builtin_amdgcn_mfma_f32_16x16x32_f16(xs[j], dequant8(w[h].codes[s][j], j < 2 ? sc.x : sc.y),
-                                                               sum[h][s], 0, 0, 0);
-          }
-      }
-      wave_sync();
-    }
-
-    // join the waves: lane has rows lane / 16 * 4 + i of column lane % 16
-    float total[kHalves][(MT * kTileN + kThreads - 1) / kThreads];
-    float* sums = (float*)s_shared;  // [wave][row][column]
-#pragma unroll
-    for (int h = 0; h < kHalves; ++h) {
+        *(u32x4*)(stage + r * stage_row + i * 8) = v;
+      });
       __syncthreads();
-#pragma unroll
-      for (int s = 0; s < SUB; ++s)
+      if constexpr (kScaled) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = lane / 16 * 4 + i;
-          if (r < MT) {
-            const float u = X::kId == NVFP4_MOE_BF16 ? s_unscale[wave][r] : 1.f;
-            sums[(wave * MT + r) * kTileN + s * 16 + lane % 16] = sum[h][s][i] * u;
+          if (r >= rows) continue;
+          const int now = scale_up(s_top[r]);
+          if (done > 0) {
+            const float down = __builtin_bit_cast(float, (uint32_t)max(127 + now - up[i], 0) << 23);
+#pragma unroll
+            for (int u = 0; u < U; ++u) sum[u][i] *= down;
+          }
+          up[i] = now;
+        }
+      }
+      // rows from `rows` on hold whatever was there: their sums are dropped
+      const _Float16* mine = stage + (lane % 16 & (row_space - 1)) * stage_row + (k_wave * part - first - done) * kStep +
+                             lane / 16 * 64;
+      u32x4* turn = s_codes[wave];
+      auto multiply = [&](int at, const Weights<U>& w) {
+        const uint32_t mask = operand.scale_mask(at);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) turn[u * 16 * kPieces + piece_at(i * 8 + lane / 8, lane % 8)] = w.codes[u][i];
+        wave_sync();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          f16x8 xs[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) xs[j] = *(const f16x8*)(mine + at * kStep + h * 32 + j * 8);
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const u32x4 c = turn[u * 16 * kPieces + piece_at(lane % 16, lane / 16 * 2 + h)];
+            const f16x2 sc = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((w.scales[u] & mask) >> (h * 16), 1.f, false);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              sum[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(xs[j], dequant8(c[j], j < 2 ? sc.x : sc.y), sum[u], 0, 0, 0);
           }
         }
-      __syncthreads();
+        wave_sync();
+      };
+      // whole rounds always load (the last step again at the end), so that what is waited for is known when compiled
+      const int end = min(first + done + part, last);
+      for (; step + kDepth <= end; step += kDepth) {
 #pragma unroll
-      for (int o = 0; o * kThreads < MT * kTileN; ++o) {
-        const int at = o * kThreads + threadIdx.x;
-        float t = 0.f;
-        if (at < MT * kTileN)
-          for (int w = 0; w < kWaves; ++w) t += sums[w * MT * kTileN + at];
-        total[h][o] = t;
+        for (int d = 0; d < kDepth; ++d) {
+          multiply(step + d, ahead[d]);
+          ahead[d] = operand.load(min(step + d + kDepth, last - 1));
+        }
       }
-    }
-    const float alpha = a.alpha == nullptr ? 1.f : a.alpha[expert];
+      if (end == last) {
 #pragma unroll
-    for (int o = 0; o * kThreads < MT * kTileN; ++o) {
-      const int at = o * kThreads + threadIdx.x, r = at / kTileN, c = at % kTileN;
-      const int col = row0 + c / 16 * 32 + c % 16;
-      if (at >= MT * kTileN || r >= rows || col >= a.columns) continue;
-      float y = total[0][o] * alpha;
-      if constexpr (SWIGLU) y = y / (1.f + exp_f32(-y)) * (total[kHalves - 1][o] * alpha);
-      const int64_t to = (int64_t)s_slots[from + r] * a.columns + col;
-      if (a.out_dtype == NVFP4_MOE_F32) store1<F32>(a.out, to, y);
-      else if (a.out_dtype == NVFP4_MOE_F16) store1<F16>(a.out, to, y);
-      else store1<BF16>(a.out, to, y);
+        for (int d = 0; d + 1 < kDepth; ++d)
+          if (step + d < last) multiply(step + d, ahead[d]);
+        step = last;
+      }
+      __syncthreads();  // the stage has been read
+    }
+    if (from + a.rows < count && steps > 0) prefetch();
+    if (kScaled && threadIdx.x < kMaxRows) s_top[threadIdx.x] = 0;  // read again after the next barrier only
+
+    // lane has rows lane / 16 * 4 + i of column lane % 16 of its runs
+    const float alpha = a.alpha == nullptr ? 1.f : a.alpha[expert];
+    float* sums = (float*)s_shared;  // [wave][run][row][column]
+    if (a.k_waves > 1) {
+      if (k_wave > 0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (lane / 16 * 4 + i < rows) sums[((wave * U + u) * kMaxRows + lane / 16 * 4 + i) * 16 + lane % 16] = sum[u][i];
+      }
+      __syncthreads();
+    }
+    if (k_wave == 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = lane / 16 * 4 + i;
+        if (r >= rows) continue;
+        float unscale = alpha;
+        if constexpr (kScaled) unscale *= __builtin_bit_cast(float, (uint32_t)(254 - up[i]) << 23);
+        float y[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          y[u] = sum[u][i];
+          for (int w = 1; w < a.k_waves; ++w) y[u] += sums[(((wave + w) * U + u) * kMaxRows + r) * 16 + lane % 16];
+          y[u] *= unscale;
+        }
+#pragma unroll
+        for (int u = 0; u < SUB; ++u) {
+          const int col = row0 + u * 32 + lane % 16;
+          float out = y[u];
+          if constexpr (SWIGLU) out = out / (1.f + exp_f32(-out)) * y[SUB + u];
+          if (col < a.columns) store_any(a.out, a.out_dtype, (int64_t)s_slots[from + r] * a.columns + col, out);
+        }
+      }
     }
     __syncthreads();
   }
 }
 
-template <class X, int SUB, bool SWIGLU> void launch_few(const FewArgs& a, int64_t tokens, hipStream_t st) {
-  const unsigned grid = (unsigned)a.slots * a.tiles;
-  if (tokens <= 4) nvfp4_few_tokens_kernel<X, SUB, SWIGLU, 4><<<grid, kThreads, 0, st>>>(a);
-  else nvfp4_few_tokens_kernel<X, SUB, SWIGLU, 16><<<grid, kThreads, 0, st>>>(a);
+template <class X, int U, bool SWIGLU> int launch_few(FewArgs& a, int64_t tokens, hipStream_t st) {
+  constexpr int SUB = SWIGLU ? U / 2 : U;
+  const int wave_tiles = ceil_div(a.columns, 32 * SUB) * 2, used = a.by_expert ? a.experts : a.slots;
+  const int steps = ceil_div(a.k, kStep);
+  // a token's experts differ as a rule: then an expert has at most a slot of each token (else it takes more passes)
+  a.rows = 1;
+  while (a.rows < kMaxRows && a.rows < tokens) a.rows *= 2;
+  // K is split over the waves until there are enough waves to fill the chip, or a wave's steps get few
+  a.k_waves = 1;
+  while (a.k_waves < kWaves && (int64_t)used * wave_tiles * a.k_waves < kEnoughWaves && steps >= 4 * a.k_waves &&
+         2 * a.rows * a.k_waves * kDepth * kStep <= kStageElements)
+    a.k_waves *= 2;
+  a.tiles = ceil_div(wave_tiles, kWaves / a.k_waves);
+  a.stage = a.rows * a.k_waves * ceil_div(ceil_div(steps, a.k_waves), kDepth) * kDepth * kStep;
+  if (a.stage > kStageElements) a.stage = kStageElements;
+  const size_t sums = (size_t)kWaves * U * kMaxRows * 16 * 4, staged = ((size_t)a.stage + kMaxRows * kPad) * 2;
+  a.slots_at = (int)(a.k_waves > 1 && sums > staged ? sums : staged);
+  const size_t shared = a.slots_at + ((size_t)a.slots * 2 + 15) / 16 * 16;
+  nvfp4_few_tokens_kernel<X, U, SWIGLU><<<(unsigned)(used * a.tiles), kThreads, shared, st>>>(a);
+  return launched();
 }
-template <class X, bool SWIGLU> void launch_few(FewArgs& a, int64_t tokens, hipStream_t st) {
-  // wide tiles where they still fill the chip
-  const int sub = (int64_t)a.slots * ceil_div(a.columns, 64) >= 256 ? 4 : (int64_t)a.slots * ceil_div(a.columns, 32) >= 256 ? 2 : 1;
-  a.tiles = ceil_div(a.columns, 32 * sub) * 2;
-  if (sub == 4) launch_few<X, 4, SWIGLU>(a, tokens, st);
-  else if (sub == 2) launch_few<X, 2, SWIGLU>(a, tokens, st);
-  else launch_few<X, 1, SWIGLU>(a, tokens, st);
-}
-template <class X> void launch_few(FewArgs& a, int64_t tokens, int swiglu, hipStream_t st) {
-  if (swiglu) launch_few<X, true>(a, tokens, st);
-  else launch_few<X, false>(a, tokens, st);
+template <class X> int launch_few(FewArgs& a, int64_t tokens, int swiglu, hipStream_t st) {
+  return swiglu ? launch_few<X, 2, true>(a, tokens, st) : launch_few<X, 2, false>(a, tokens, st);
 }
 
 }  // namespace
@@ -310,6 +452,7 @@ extern "C" int nvfp4_moe_few_tokens(const void* x, int dtype, int64_t x_stride, 
     return NVFP4_ERR_INVALID;
   if (experts < 1 || experts > NVFP4_MOE_MAX_EXPERTS) return NVFP4_ERR_INVALID;
   if (n < 0 || n % (swiglu ? 16 : 8) || n > 1 << 20 || k < 0 || k % 32 || k > 1 << 22) return NVFP4_ERR_INVALID;
+  if ((int64_t)n * (k / 2) >= (int64_t)1 << 31) return NVFP4_ERR_INVALID;
   if (x_stride < k || x_stride > (int64_t)1 << 40) return NVFP4_ERR_INVALID;
   const bool work = tokens > 0 && n > 0;
   if (work && (ids == nullptr || out == nullptr)) return NVFP4_ERR_INVALID;
@@ -335,7 +478,7 @@ extern "C" int nvfp4_moe_few_tokens(const void* x, int dtype, int64_t x_stride, 
   a.x_vec = wide_rows(x, dtype, x_stride);
   a.out_dtype = out_dtype;
   a.columns = swiglu ? n / 2 : n;
-  if (dtype == NVFP4_MOE_F16) launch_few<F16>(a, tokens, swiglu, (hipStream_t)stream);
-  else launch_few<BF16>(a, tokens, swiglu, (hipStream_t)stream);
-  return launched();
+  a.by_expert = a.experts < a.slots;
+  return dtype == NVFP4_MOE_F16 ? launch_few<F16>(a, tokens, swiglu, (hipStream_t)stream)
+                                : launch_few<BF16>(a, tokens, swiglu, (hipStream_t)stream);
 }
