@@ -20,57 +20,70 @@ struct CombineArgs {
   int topk, n, chunks, c_vec, out_vec, dy_vec;
 };
 
-// A slot's row (-1: none) and its expert's factor.
-__device__ inline int64_t slot_row(const CombineArgs& a, int64_t slot, float& factor) {
-  int64_t row = a.slot_rows == nullptr ? slot : a.slot_rows[slot];
-  factor = 1.f;
-  if (a.ids != nullptr) {
-    const int id = a.ids[slot];
-    if (id < 0) row = -1;
-    else if (a.alpha != nullptr && row >= 0) factor = a.alpha[id];
+// A token's slots, one to a lane: row (-1: none), weight and expert's factor
+// (both 0 without a row).
+struct Slot {
+  int64_t row;
+  float weight, factor;
+};
+__device__ inline Slot slot_of(const CombineArgs& a, int64_t token, int lane) {
+  Slot s = {-1, 0.f, 0.f};
+  if (lane < a.topk) {
+    const int64_t slot = token * a.topk + lane;
+    const int id = a.ids == nullptr ? 0 : a.ids[slot];
+    const int64_t row = a.slot_rows == nullptr ? slot : a.slot_rows[slot];
+    const float weight = a.weights == nullptr ? 1.f : a.weights[slot];
+    if (id >= 0 && row >= 0) s = {row, weight, a.alpha == nullptr ? 1.f : a.alpha[id]};
   }
-  return row;
+  return s;
+}
+// Slot j of a wave's token, for the whole wave. Called where all lanes are active:
+// what a lane holds is computed by that lane.
+__device__ inline int64_t row_of(const Slot& s, int j) {
+  const uint32_t low = __builtin_amdgcn_readlane((int)(uint32_t)s.row, j), high = __builtin_amdgcn_readlane((int)(s.row >> 32), j);
+  return (int64_t)((uint64_t)high << 32 | low);
+}
+__device__ inline float lane_value(float v, int j) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), j));
 }
 
-// Eight columns of a token to a thread; its rows are read at once and added in
-// slot order. Bound by memory: each row of c is read once, in 16-byte pieces.
+// A wave takes 512 columns of a token, eight to a lane; its rows are read at
+// once and added in slot order. Bound by memory: each row of c is read once, in
+// whole lines that are not kept.
 template <class C, class Out, int K>
 __global__ void __launch_bounds__(kThreads) nvfp4_moe_combine_kernel(CombineArgs a) {
-  const uint32_t index = blockIdx.x * kThreads + threadIdx.x;
-  const int64_t token = index / (uint32_t)a.chunks;
-  const int col = (int)(index % (uint32_t)a.chunks) * 8;
+  const uint32_t wave = blockIdx.x * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int64_t token = wave / (uint32_t)a.chunks;
+  const int lane = threadIdx.x & 63, col = (int)(wave % (uint32_t)a.chunks) * 512 + lane * 8;
   if (token >= a.tokens) return;
+  const Slot slot = slot_of(a, token, lane);
+  const float gain = slot.weight * slot.factor;
+  const bool mine = col < a.n;
   float sum[8];
-  if (a.residual != nullptr) {
+  if (a.residual != nullptr && mine) {
     load8<Out>(a.residual, token * a.out_stride + col, a.out_vec, sum);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) sum[i] = 0.f;
   }
   for (int from = 0; from < a.topk; from += K) {
-    float w[K], v[K][8];
+    Raw8<C> v[K];
 #pragma unroll
     for (int j = 0; j < K; ++j) {
-      w[j] = 0.f;
-      if (from + j < a.topk) {
-        const int64_t slot = token * a.topk + from + j;
-        float factor;
-        const int64_t row = slot_row(a, slot, factor);
-        if (row >= 0) {
-          w[j] = (a.weights == nullptr ? 1.f : a.weights[slot]) * factor;
-          load8<C>(a.c, row * a.c_stride + col, a.c_vec, v[j]);
-          continue;
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[j][i] = 0.f;
+      const int64_t row = row_of(slot, from + j);  // -1 from topk on
+      v[j] = Raw8<C>{};
+      if (row >= 0 && mine) v[j].load(a.c, row * a.c_stride + col, a.c_vec);
     }
 #pragma unroll
-    for (int j = 0; j < K; ++j)
+    for (int j = 0; j < K; ++j) {
+      const float w = lane_value(gain, from + j);
+      float x[8];
+      v[j].values(x);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum[i] = fmaf(w[j], v[j][i], sum[i]);
+      for (int i = 0; i < 8; ++i) sum[i] = fmaf(w, x[i], sum[i]);
+    }
   }
-  store8<Out>(a.out, token * a.out_stride + col, a.out_vec, sum);
+  if (mine) store8<Out>(a.out, token * a.out_stride + col, a.out_vec, sum);
 }
 
 // A workgroup per token: dy is read once, its rows of c once, dc written once.
@@ -80,29 +93,34 @@ template <class C, class Dy, int K>
 __global__ void __launch_bounds__(kThreads) nvfp4_moe_combine_backward_kernel(CombineArgs a) {
   __shared__ float s_sum[K][kThreads / 64];
   const int64_t token = blockIdx.x;
+  const int lane = threadIdx.x & 63;
+  const Slot slot = slot_of(a, token, lane);
+  const float gain = slot.weight * slot.factor;
   int64_t row[K];
-  float w[K], factor[K], sum[K];
+  float w[K], sum[K];
 #pragma unroll
   for (int j = 0; j < K; ++j) {
-    row[j] = -1;
-    w[j] = factor[j] = sum[j] = 0.f;
-    if (j < a.topk) {
-      const int64_t slot = token * a.topk + j;
-      row[j] = slot_row(a, slot, factor[j]);
-      if (row[j] >= 0) w[j] = (a.weights == nullptr ? 1.f : a.weights[slot]) * factor[j];
-    }
+    row[j] = row_of(slot, j);  // -1 from topk on
+    w[j] = lane_value(gain, j);
+    sum[j] = 0.f;
   }
   for (int col = threadIdx.x * 8; col < a.n; col += kThreads * 8) {
+    Raw8<Dy> raw;
+    Raw8<C> v[K];
+    raw.load(a.dy, token * a.dy_stride + col, a.dy_vec);
+#pragma unroll
+    for (int j = 0; j < K; ++j)
+      if (row[j] >= 0) v[j].load(a.c, row[j] * a.c_stride + col, a.c_vec);
     float dy[8];
-    load8<Dy>(a.dy, token * a.dy_stride + col, a.dy_vec, dy);
+    raw.values(dy);
 #pragma unroll
     for (int j = 0; j < K; ++j) {
       if (row[j] < 0) continue;
-      float v[8], d[8];
-      load8<C>(a.c, row[j] * a.c_stride + col, a.c_vec, v);
+      float x[8], d[8];
+      v[j].values(x);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        sum[j] = fmaf(dy[i], v[i], sum[j]);
+        sum[j] = fmaf(dy[i], x[i], sum[j]);
         d[i] = w[j] * dy[i];
       }
       store8<C>(a.dc, row[j] * a.c_stride + col, a.c_vec, d);
@@ -112,16 +130,13 @@ __global__ void __launch_bounds__(kThreads) nvfp4_moe_combine_backward_kernel(Co
   for (int j = 0; j < K; ++j) {
     float s = sum[j];
     for (int d = 1; d < 64; d *= 2) s += __shfl_xor(s, d);
-    if (threadIdx.x % 64 == 0) s_sum[j][threadIdx.x / 64] = s;
+    if (lane == 0) s_sum[j][threadIdx.x / 64] = s;
   }
   __syncthreads();
   if ((int)threadIdx.x < a.topk) {
     float s = 0.f;
     for (int i = 0; i < kThreads / 64; ++i) s += s_sum[threadIdx.x][i];
-    const int64_t slot = token * a.topk + threadIdx.x;
-    float f;
-    const int64_t r = slot_row(a, slot, f);
-    a.dweights[slot] = r >= 0 ? s * f : 0.f;
+    a.dweights[token * a.topk + threadIdx.x] = slot.row >= 0 ? s * slot.factor : 0.f;
   }
 }
 
@@ -164,10 +179,10 @@ int nvfp4_moe_combine(const void* c, int c_dtype, int64_t c_stride, int64_t toke
   if (int rc = check_combine(a, c_dtype, out_dtype, out_stride, out, out)) return rc;
   if (!aligned(residual, element_bytes(out_dtype))) return NVFP4_ERR_MISALIGNED;
   if (tokens == 0 || n == 0) return NVFP4_OK;
-  a.chunks = n / 8;
+  a.chunks = ceil_div(n, 512);
   a.c_vec = wide_rows(c, c_dtype, c_stride);
   a.out_vec = wide_rows(out, out_dtype, out_stride) && aligned(residual, 16);
-  const int64_t blocks = ceil_div64(tokens * a.chunks, kThreads);
+  const int64_t blocks = ceil_div64(tokens * a.chunks, kThreads / 64);
   if (blocks >= (int64_t)1 << 24) return NVFP4_ERR_INVALID;
   const hipStream_t st = (hipStream_t)stream;
   return with_type(c_dtype, [&](auto t) {

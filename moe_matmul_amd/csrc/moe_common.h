@@ -107,6 +107,38 @@ template <class T> __device__ inline void store8(void* p, int64_t i, bool vec, c
   }
 }
 
+// Eight elements as they lie in memory, for loads that are used later. They are
+// read once, so the lines are not kept where one load of a wave takes whole lines;
+// the two halves of eight fp32 elements share theirs.
+template <class T> struct Raw8 {
+  u32x4 w[T::kBytes / 2];
+
+  __device__ inline void load(const void* p, int64_t i, bool vec) {
+    const uint8_t* at = (const uint8_t*)p + i * T::kBytes;
+    if (vec) {
+#pragma unroll
+      for (int j = 0; j < T::kBytes / 2; ++j) w[j] = T::kBytes == 2 ? __builtin_nontemporal_load((const u32x4*)at + j) : ((const u32x4*)at)[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < 2 * T::kBytes; ++j)
+        w[j / 4][j % 4] = T::kBytes == 4 ? ((const uint32_t*)at)[j]
+                                         : ((const uint16_t*)at)[2 * j] | (uint32_t)((const uint16_t*)at)[2 * j + 1] << 16;
+    }
+  }
+  __device__ inline void values(float* v) const {
+    if constexpr (T::kBytes == 4) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t u = w[j / 4][j % 4];  // bit_cast of a vector's element itself takes the first one
+        v[j] = __builtin_bit_cast(float, u);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) unpack2<T>(w[0][j], v[2 * j], v[2 * j + 1]);
+    }
+  }
+};
+
 // exp in fp32: 2^(x log2 e) with the product's rounding error taken back, so
 // that the result is within about 2 ulp for every x (the plain product loses
 // |x| * 2^-24). -inf gives 0, NaN gives NaN.

@@ -2,6 +2,8 @@
 // gradient of the weights with respect to the logits.
 #include "moe_common.h"
 
+#include <type_traits>
+
 namespace moe {
 
 thread_local int t_last_hip_error = 0;
@@ -9,29 +11,71 @@ thread_local int t_last_hip_error = 0;
 namespace {
 
 constexpr int kThreads = 256;
-constexpr double kLargest = 1e300;  // choice values are held within +-this, so that a key stays finite
+constexpr double kLargest = 0x1p+1000;  // choice values are held within +-this, so that a key stays finite
 constexpr int kIndexMask = NVFP4_MOE_MAX_EXPERTS - 1;
+constexpr int kLeastLanes = 4;  // of a token
+constexpr int64_t kEnoughLanes = 256 * 1024;
 
-// ---- keys: a choice value and its expert in one fp64 ------------------------
-// The nine low mantissa bits of the value hold the index such that of two equal
-// values the lower index has the larger key. So one max and one min order two
-// candidates with their indices, and no two keys of a token are equal.
-__device__ inline double make_key(double v, int e) {
-  v = fmin(fmax(v, -kLargest), kLargest) + 0.0;  // -0 counts as 0
-  uint64_t u = __builtin_bit_cast(uint64_t, v) & ~(uint64_t)kIndexMask;
-  u |= (int64_t)u < 0 ? (uint64_t)e : (uint64_t)(kIndexMask - e);
-  return __builtin_bit_cast(double, u);
-}
-__device__ inline double no_key() { return -__builtin_inf(); }
-__device__ inline int key_index(double key) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, key);
-  const int low = (int)(u & kIndexMask);
-  return key == no_key() ? -1 : (int64_t)u < 0 ? low : kIndexMask - low;
-}
-__device__ inline double key_value(double key) {
-  return key == no_key() ? key
-                         : __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, key) & ~(uint64_t)kIndexMask);
-}
+// ---- keys: a choice value and its expert in one number ------------------------
+// The low bits hold the index such that of two equal values the lower index has
+// the larger key. So one max and one min order two candidates with their
+// indices, and no two keys of a token are equal.
+
+// fp64 values in fp64, the index in the nine low mantissa bits. Values lie within
+// +-kLargest (whose low bits are 0), which is also the key of no candidate: fp32
+// logits keep their order exactly, scores to 2^-43.
+struct Wide {
+  typedef double Key;
+  static __device__ inline Key none() { return -kLargest; }
+  static __device__ inline Key make(double v, int e) {  // NaN and -inf: none
+    v = fmin(fmax(v, -kLargest), kLargest) + 0.0;       // -0 counts as 0
+    uint64_t u = __builtin_bit_cast(uint64_t, v) & ~(uint64_t)kIndexMask;
+    u |= (int64_t)u < 0 ? (uint64_t)e : (uint64_t)(kIndexMask - e);
+    return __builtin_bit_cast(double, u);
+  }
+  // fp32 logits have no low bits to clear
+  static __device__ inline Key of_logit(float x, int e) {
+    const double v = fmin(fmax((double)(x + 0.f), -kLargest), kLargest);
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    return __builtin_bit_cast(double, u | ((int64_t)u < 0 ? (uint64_t)e : (uint64_t)(kIndexMask - e)));
+  }
+  static __device__ inline int index(Key key) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, key);
+    const int low = (int)(u & kIndexMask);
+    return !there(key) ? -1 : (int64_t)u < 0 ? low : kIndexMask - low;
+  }
+  static __device__ inline bool there(Key key) { return key > -0.9 * kLargest; }
+  static __device__ inline double value(Key key) {
+    return __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, key) & ~(uint64_t)kIndexMask);
+  }
+  static __device__ inline Key larger(Key a, Key b) { return fmax(a, b); }
+  static __device__ inline Key smaller(Key a, Key b) { return fmin(a, b); }
+  template <int kCtrl> static __device__ inline Key from_lane(Key v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t low = __builtin_amdgcn_mov_dpp((int)(uint32_t)u, kCtrl, 0xF, 0xF, false);
+    const uint32_t high = __builtin_amdgcn_mov_dpp((int)(uint32_t)(u >> 32), kCtrl, 0xF, 0xF, false);
+    return __builtin_bit_cast(double, (uint64_t)high << 32 | low);
+  }
+};
+
+// 16-bit logits: their bits, mapped so that they order as whole numbers, over the index.
+struct Narrow {
+  typedef uint32_t Key;
+  static __device__ inline Key none() { return 0u; }
+  // `bits`: of the logit, fp16 or bf16; `infinity`: of +inf in that type
+  static __device__ inline Key of_bits(uint32_t bits, uint32_t infinity, int e) {
+    if (bits == 0x8000u) bits = 0;  // -0 counts as 0
+    const uint32_t order = bits & 0x8000u ? ~bits & 0xFFFFu : bits | 0x8000u;
+    const bool candidate = (bits & 0x7FFFu) <= infinity && bits != (0x8000u | infinity);  // neither NaN nor -inf
+    return candidate ? order << 16 | (uint32_t)(kIndexMask - e) : 0u;
+  }
+  static __device__ inline int index(Key key) { return key == 0 ? -1 : kIndexMask - (int)(key & 0xFFFFu); }
+  static __device__ inline Key larger(Key a, Key b) { return max(a, b); }
+  static __device__ inline Key smaller(Key a, Key b) { return min(a, b); }
+  template <int kCtrl> static __device__ inline Key from_lane(Key v) {
+    return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, kCtrl, 0xF, 0xF, false);
+  }
+};
 
 // ---- exp and sigmoid in fp64 -------------------------------------------------
 // 2^n times the Taylor series of e^r, |r| <= ln 2 / 2: 13 terms leave 2^-53 / 4.
@@ -62,13 +106,13 @@ __device__ inline double inverse_f64(double d) {
 }
 
 // ---- sorted lists in registers -------------------------------------------------
-__device__ inline void order(double& a, double& b) {  // a the larger
-  const double x = fmax(a, b), y = fmin(a, b);
+template <class W> __device__ inline void order(typename W::Key& a, typename W::Key& b) {  // a the larger
+  const typename W::Key x = W::larger(a, b), y = W::smaller(a, b);
   a = x;
   b = y;
 }
 // Odd-even merge sort, falling.
-template <int N> __device__ inline void sort_falling(double (&v)[N]) {
+template <class W, int N> __device__ inline void sort_falling(typename W::Key (&v)[N]) {
 #pragma unroll
   for (int p = 1; p < N; p *= 2) {
 #pragma unroll
@@ -77,53 +121,65 @@ template <int N> __device__ inline void sort_falling(double (&v)[N]) {
       for (int j = k % p; j <= N - 1 - k; j += 2 * k) {
 #pragma unroll
         for (int i = 0; i < k; ++i)
-          if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) order(v[i + j], v[i + j + k]);
+          if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) order<W>(v[i + j], v[i + j + k]);
       }
     }
   }
 }
 // The K largest of two falling lists, falling: the larger of each pair of one
 // list and the other reversed form a bitonic sequence.
-template <int K> __device__ inline void merge_falling(double (&list)[K], const double (&other)[K]) {
+template <class W, int K>
+__device__ inline void merge_falling(typename W::Key (&list)[K], const typename W::Key (&other)[K]) {
 #pragma unroll
-  for (int i = 0; i < K; ++i) list[i] = fmax(list[i], other[K - 1 - i]);
+  for (int i = 0; i < K; ++i) list[i] = W::larger(list[i], other[K - 1 - i]);
 #pragma unroll
   for (int k = K / 2; k >= 1; k /= 2) {
 #pragma unroll
     for (int i = 0; i < K; ++i)
-      if ((i & k) == 0) order(list[i], list[i + k]);
+      if ((i & k) == 0) order<W>(list[i], list[i + k]);
+  }
+}
+// The K largest of N keys, falling.
+template <class W, int K, int N>
+__device__ inline void keep_largest(const typename W::Key (&v)[N], typename W::Key (&list)[K]) {
+#pragma unroll
+  for (int at = 0; at < N; at += K) {
+    typename W::Key part[K];
+#pragma unroll
+    for (int i = 0; i < K; ++i) part[i] = at + i < N ? v[at + i < N ? at + i : 0] : W::none();
+    sort_falling<W, K>(part);
+    if (at == 0) {
+#pragma unroll
+      for (int i = 0; i < K; ++i) list[i] = part[i];
+    } else {
+      merge_falling<W, K>(list, part);
+    }
   }
 }
 
-template <int kCtrl> __device__ inline double from_lane(double v) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, v);
-  const uint32_t low = __builtin_amdgcn_mov_dpp((int)(uint32_t)u, kCtrl, 0xF, 0xF, false);
-  const uint32_t high = __builtin_amdgcn_mov_dpp((int)(uint32_t)(u >> 32), kCtrl, 0xF, 0xF, false);
-  return __builtin_bit_cast(double, (uint64_t)high << 32 | low);
-}
 constexpr int kXor1 = 0xB1, kXor2 = 0x4E;           // quad permutations
 constexpr int kMirror8 = 0x141, kMirror16 = 0x140;  // lane i <-> 7 - i, 15 - i
 
-template <int K, int kCtrl> __device__ inline void merge_with(double (&list)[K]) {
-  double other[K];
+template <class W, int K, int kCtrl> __device__ inline void merge_with(typename W::Key (&list)[K]) {
+  typename W::Key other[K];
 #pragma unroll
-  for (int i = 0; i < K; ++i) other[i] = from_lane<kCtrl>(list[i]);
-  merge_falling(list, other);
+  for (int i = 0; i < K; ++i) other[i] = W::template from_lane<kCtrl>(list[i]);
+  merge_falling<W, K>(list, other);
 }
-template <int K> __device__ inline void merge_across(double (&list)[K], int distance) {
-  double other[K];
+template <class W, int K> __device__ inline void merge_across(typename W::Key (&list)[K], int distance) {
+  typename W::Key other[K];
 #pragma unroll
   for (int i = 0; i < K; ++i) other[i] = __shfl_xor(list[i], distance);
-  merge_falling(list, other);
+  merge_falling<W, K>(list, other);
 }
 // Every lane of a token's `lanes` gets the K largest of all of them.
-template <int K> __device__ inline void merge_lanes(double (&list)[K], int lanes) {
-  if (lanes > 1) merge_with<K, kXor1>(list);
-  if (lanes > 2) merge_with<K, kXor2>(list);
-  if (lanes > 4) merge_with<K, kMirror8>(list);
-  if (lanes > 8) merge_with<K, kMirror16>(list);
-  if (lanes > 16) merge_across<K>(list, 16);
-  if (lanes > 32) merge_across<K>(list, 32);
+template <class W, int K> __device__ inline void merge_lanes(typename W::Key (&list)[K], int lanes) {
+  if (lanes > 1) merge_with<W, K, kXor1>(list);
+  if (lanes > 2) merge_with<W, K, kXor2>(list);
+  if (lanes > 4) merge_with<W, K, kMirror8>(list);
+  if (lanes > 8) merge_with<W, K, kMirror16>(list);
+  if (lanes > 16) merge_across<W, K>(list, 16);
+  if (lanes > 32) merge_across<W, K>(list, 32);
 }
 
 template <class V, class Op> __device__ inline V across(V v, int lanes, Op op) {
@@ -211,15 +267,20 @@ __device__ inline bool poisons(float x, int score) {
   return x != x || (score == NVFP4_MOE_SOFTMAX && x == __builtin_inff());
 }
 
+// Whether the choice goes by the logits (as 32-bit keys where they have 16 bits)
+// or by scores (a bias, or groups), which are then computed in fp64.
+enum Mode { kLogits16, kLogits32, kScores };
+
 // Routing. A token's logits are read once into the registers of `lanes` lanes;
-// each lane keeps the K largest keys of its experts in a sorted list (sort a
-// chunk, merge it in: two instructions for each comparison), and the lanes'
-// lists are merged in log2(lanes) steps. kScores: the choice goes by scores
-// (a bias or groups), which are then computed in fp64; else by the logits.
-template <int K, int NC, bool kScores>
+// each lane keeps the K largest keys of its experts in a sorted list (sort K,
+// merge them in: two instructions for each comparison), and the lanes' lists are
+// merged in log2(lanes) steps. Bound by these instructions, not by the logits.
+template <int K, int NC, Mode kMode>
 __global__ void __launch_bounds__(kThreads) nvfp4_moe_route_kernel(RouteArgs a) {
-  __shared__ double s_best[kScores ? kThreads : 1][2];
-  __shared__ double s_group[kScores ? kThreads / 4 : 1][kScores ? NVFP4_MOE_MAX_GROUPS : 1];
+  typedef typename std::conditional<kMode == kLogits16, Narrow, Wide>::type W;
+  typedef typename W::Key Key;
+  extern __shared__ double s_group[];  // [tokens][groups]
+  __shared__ double s_best[kMode == kScores ? kThreads : 1][2];
   const int lane = threadIdx.x & (a.lanes - 1), local = threadIdx.x / a.lanes;
   const int64_t mine = (int64_t)blockIdx.x * (kThreads / a.lanes) + local;
   const int64_t token = mine < a.tokens ? mine : a.tokens - 1;  // lanes past the end repeat the last token
@@ -239,32 +300,29 @@ __global__ void __launch_bounds__(kThreads) nvfp4_moe_route_kernel(RouteArgs a) 
 
   const bool softmax = a.how.score == NVFP4_MOE_SOFTMAX;
   float total = 1.f;  // of e^(x - top) over all experts
-  double list[K];
-  if constexpr (!kScores) {
+  Key v[NC * 8];
+  if constexpr (kMode != kScores) {
     if (softmax && !a.how.renormalize) {
       top = max_across(top, a.lanes);
       const float from = top == -__builtin_inff() ? 0.f : top;
       total = 0.f;
+      // the plain product's error, |x - top| 2^-24 of a term, is small where the term is not
 #pragma unroll
-      for (int i = 0; i < NC * 8; ++i) total += exp_f32(x[i] - from);
+      for (int i = 0; i < NC * 8; ++i) total += __builtin_amdgcn_exp2f((x[i] - from) * 1.44269502f);
       total = sum_across(total, a.lanes);
     }
+    const bool half = a.dtype == NVFP4_MOE_F16;
 #pragma unroll
-    for (int i = 0; i < K; ++i) list[i] = no_key();
-#pragma unroll
-    for (int at = 0; at < NC * 8; at += K) {
-      double part[K];
-#pragma unroll
-      for (int i = 0; i < K; ++i) {
-        const int n = at + i;
-        const bool there = n < NC * 8 && x[n < NC * 8 ? n : 0] > -__builtin_inff();  // not for NaN
-        part[i] = there ? make_key((double)x[n < NC * 8 ? n : 0], s.base + n / 8 * s.step + n % 8) : no_key();
+    for (int i = 0; i < NC * 8; ++i) {
+      const int e = s.base + i / 8 * s.step + i % 8;
+      if constexpr (kMode == kLogits16) {
+        const uint32_t bits = half ? (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)x[i]) : __builtin_bit_cast(uint32_t, x[i]) >> 16;
+        v[i] = Narrow::of_bits(bits, half ? 0x7C00u : 0x7F80u, e);
+      } else {
+        v[i] = Wide::of_logit(x[i], e);
       }
-      sort_falling(part);
-      merge_falling(list, part);
     }
   } else {
-    double v[NC * 8];
     if (softmax) {
       top = max_across(top, a.lanes);
       const double from = top == -__builtin_inff() ? 0.0 : (double)fminf(top, 3.4e38f);
@@ -287,18 +345,17 @@ __global__ void __launch_bounds__(kThreads) nvfp4_moe_route_kernel(RouteArgs a) 
     for (int i = 0; i < NC * 8; ++i) {
       const int e = s.base + i / 8 * s.step + i % 8;
       if (a.bias != nullptr) v[i] += e < s.end ? (double)a.bias[e] : 0.0;
-      const bool there = x[i] > -__builtin_inff() && v[i] > -__builtin_inf();  // neither for NaN
-      v[i] = there ? make_key(v[i], e) : no_key();
+      v[i] = x[i] > -__builtin_inff() ? Wide::make(v[i], e) : Wide::none();  // none for a NaN logit, too
     }
     if (a.how.groups > 1) {
       // The best two of each lane, or the values of each lane's groups, then a
       // group's rank: how many groups are better.
       auto worth = [&](double first, double second) {
-        const double f = key_value(first), g = key_value(second);
-        return a.how.group_best == 1 || g == no_key() ? f : f + g;
+        const double f = Wide::value(first), g = Wide::value(second);
+        return a.how.group_best == 1 || !Wide::there(second) ? f : f + g;
       };
       if (a.groups_of == 1) {
-        double one = no_key(), two = no_key();
+        double one = Wide::none(), two = Wide::none();
 #pragma unroll
         for (int i = 0; i < NC * 8; ++i) {
           two = fmax(two, fmin(one, v[i]));
@@ -308,79 +365,87 @@ __global__ void __launch_bounds__(kThreads) nvfp4_moe_route_kernel(RouteArgs a) 
         s_best[threadIdx.x][1] = two;
         __syncthreads();
         for (int g = lane; g < a.how.groups; g += a.lanes) {
-          double first = no_key(), second = no_key();
+          double first = Wide::none(), second = Wide::none();
           for (int q = 0; q < a.lanes_of; ++q) {
             const int from = threadIdx.x - lane + g * a.lanes_of + q;
             const double p = s_best[from][0], r = s_best[from][1];
             second = fmax(fmax(second, r), fmin(first, p));
             first = fmax(first, p);
           }
-          s_group[local][g] = worth(first, second);
+          s_group[local * a.how.groups + g] = worth(first, second);
         }
       } else {
         for (int q = 0; q < a.groups_of; ++q) {
           const int g = lane * a.groups_of + q;
           if (g >= a.how.groups) break;
-          double one = no_key(), two = no_key();
+          double one = Wide::none(), two = Wide::none();
 #pragma unroll
           for (int i = 0; i < NC * 8; ++i) {
-            const double w = i / a.per == q ? v[i] : no_key();
+            const double w = i / a.per == q ? v[i] : Wide::none();
             two = fmax(two, fmin(one, w));
             one = fmax(one, w);
           }
-          s_group[local][g] = worth(one, two);
+          s_group[local * a.how.groups + g] = worth(one, two);
         }
       }
       __syncthreads();
       for (int q = 0; q < a.groups_of; ++q) {
         const int g = a.groups_of == 1 ? lane / a.lanes_of : lane * a.groups_of + q;
-        const double w = g < a.how.groups ? s_group[local][g] : no_key();
+        const double w = g < a.how.groups ? s_group[local * a.how.groups + g] : Wide::none();
         int better = 0;
         for (int o = 0; o < a.how.groups; ++o) {
-          const double u = s_group[local][o];
+          const double u = s_group[local * a.how.groups + o];
           better += u > w || (u == w && o < g);
         }
 #pragma unroll
         for (int i = 0; i < NC * 8; ++i) {
           const bool of = a.groups_of == 1 || i / a.per == q;
-          if (of && better >= a.how.topk_groups) v[i] = no_key();
+          if (of && better >= a.how.topk_groups) v[i] = Wide::none();
         }
       }
     }
-#pragma unroll
-    for (int i = 0; i < K; ++i) list[i] = no_key();
-#pragma unroll
-    for (int at = 0; at < NC * 8; at += K) {
-      double part[K];
-#pragma unroll
-      for (int i = 0; i < K; ++i) part[i] = at + i < NC * 8 ? v[at + i < NC * 8 ? at + i : 0] : no_key();
-      sort_falling(part);
-      merge_falling(list, part);
-    }
   }
-  merge_lanes(list, a.lanes);
+  Key list[K];
+  keep_largest<W, K, NC * 8>(v, list);
+  merge_lanes<W, K>(list, a.lanes);
 
-  // lane j < topk has slot j
-  double key = no_key();
+  // slot j belongs to lane j % lanes: slots of a lane are K / lanes at most
+  constexpr int kLaneSlots = K > kLeastLanes ? K / kLeastLanes : 1;
+  int ids[kLaneSlots];
+  float chosen[kLaneSlots], w[kLaneSlots], largest = -__builtin_inff();
 #pragma unroll
-  for (int i = 0; i < K; ++i) key = i == lane ? list[i] : key;
-  const int id = lane < a.how.topk ? key_index(key) : -1;
-  const float chosen = id >= 0 ? load_logit(a.logits, a.dtype, token * a.row_stride + id) : -__builtin_inff();
-  float w;
-  if (softmax) {
-    const float from = a.how.renormalize ? max_across(chosen, a.lanes) : top;
-    w = exp_f32(chosen - (from == -__builtin_inff() ? 0.f : from));
-  } else {
-    w = id >= 0 ? 1.f / (1.f + exp_f32(-chosen)) : 0.f;
+  for (int q = 0; q < kLaneSlots; ++q) {
+    const int slot = q * a.lanes + lane;
+    Key key = W::none();
+#pragma unroll
+    for (int i = 0; i < K; ++i) key = i == slot ? list[i] : key;
+    ids[q] = slot < a.how.topk ? W::index(key) : -1;
+    chosen[q] = ids[q] >= 0 ? load_logit(a.logits, a.dtype, token * a.row_stride + ids[q]) : -__builtin_inff();
+    largest = fmaxf(largest, chosen[q]);
   }
-  if (a.how.renormalize) total = sum_across(w, a.lanes);
+  const int share = a.lanes < K ? a.lanes : K;  // lanes that have a slot
+  if (softmax && a.how.renormalize) top = max_across(largest, share);
+  const float from = top == -__builtin_inff() ? 0.f : top;
+  float sum = 0.f;
+#pragma unroll
+  for (int q = 0; q < kLaneSlots; ++q) {
+    if (softmax) w[q] = exp_f32(chosen[q] - from);
+    else w[q] = ids[q] >= 0 ? 1.f / (1.f + exp_f32(-chosen[q])) : 0.f;
+    sum += w[q];
+  }
+  if (a.how.renormalize) total = sum_across(sum, share);
   else if (!softmax) total = 1.f;
-  w = w / (total == 0.f ? 1.f : total) * a.how.scale;
-  if (id < 0) w = 0.f;
-  else if (bad) w = __builtin_nanf("");
-  if (lane < a.how.topk && mine < a.tokens) {
-    a.ids[token * a.how.topk + lane] = id;
-    a.weights[token * a.how.topk + lane] = w;
+  if (total == 0.f) total = 1.f;
+#pragma unroll
+  for (int q = 0; q < kLaneSlots; ++q) {
+    const int slot = q * a.lanes + lane;
+    float y = w[q] / total * a.how.scale;
+    if (ids[q] < 0) y = 0.f;
+    else if (bad) y = __builtin_nanf("");
+    if (slot < a.how.topk && mine < a.tokens) {
+      a.ids[token * a.how.topk + slot] = ids[q];
+      a.weights[token * a.how.topk + slot] = y;
+    }
   }
 }
 
@@ -519,10 +584,10 @@ int at_least_pow2(int v) {
   return p;
 }
 
-// Lanes of a token: enough that every slot has one and none holds more than 32
-// experts, and more where there are too few tokens to fill the chip.
+// Lanes of a token: few, as the lanes' merged lists are the same work in each of
+// them, but more where there are too few tokens to fill the chip.
 int widen(int lanes, int64_t tokens, int experts) {
-  while (lanes < 64 && tokens * lanes < 256 * 1024 && lanes * 8 < experts) lanes *= 2;
+  while (lanes < 64 && tokens * lanes < kEnoughLanes && lanes * 8 < experts) lanes *= 2;
   return lanes;
 }
 
@@ -537,14 +602,17 @@ int lay_out(RouteArgs& a) {
   return ceil_div(a.groups_of > 1 ? a.groups_of * a.per : ceil_div(a.per, a.lanes_of), 8);
 }
 
-template <int K, int NC> void launch_route(const RouteArgs& a, bool scores, int64_t blocks, hipStream_t stream) {
-  if (scores) nvfp4_moe_route_kernel<K, NC, true><<<dim3((unsigned)blocks), kThreads, 0, stream>>>(a);
-  else nvfp4_moe_route_kernel<K, NC, false><<<dim3((unsigned)blocks), kThreads, 0, stream>>>(a);
+template <int K, int NC> void launch_route(const RouteArgs& a, Mode mode, int64_t blocks, hipStream_t stream) {
+  const dim3 grid((unsigned)blocks);
+  const size_t shared = a.how.groups > 1 ? sizeof(double) * (kThreads / a.lanes) * a.how.groups : 0;
+  if (mode == kScores) nvfp4_moe_route_kernel<K, NC, kScores><<<grid, kThreads, shared, stream>>>(a);
+  else if (mode == kLogits16) nvfp4_moe_route_kernel<K, NC, kLogits16><<<grid, kThreads, 0, stream>>>(a);
+  else nvfp4_moe_route_kernel<K, NC, kLogits32><<<grid, kThreads, 0, stream>>>(a);
 }
-template <int K> void launch_route(const RouteArgs& a, int chunks, bool scores, int64_t blocks, hipStream_t stream) {
-  if (chunks <= 1) launch_route<K, 1>(a, scores, blocks, stream);
-  else if (chunks <= 2) launch_route<K, 2>(a, scores, blocks, stream);
-  else launch_route<K, 4>(a, scores, blocks, stream);
+template <int K> void launch_route(const RouteArgs& a, int chunks, Mode mode, int64_t blocks, hipStream_t stream) {
+  if (chunks <= 1) launch_route<K, 1>(a, mode, blocks, stream);
+  else if (chunks <= 2) launch_route<K, 2>(a, mode, blocks, stream);
+  else launch_route<K, 4>(a, mode, blocks, stream);
 }
 
 }  // namespace
@@ -575,19 +643,19 @@ int nvfp4_moe_route(const void* logits, int dtype, int64_t tokens, int experts, 
   a.dtype = dtype;
   a.vec = wide_rows(logits, dtype, row_stride);
   a.how = *choice;
-  a.lanes = widen(at_least_pow2(choice->topk < 4 ? 4 : choice->topk), tokens, experts);
+  a.lanes = widen(kLeastLanes, tokens, experts);
   int chunks = lay_out(a);
   while (chunks > 4) {
     a.lanes *= 2;
     chunks = lay_out(a);
   }
-  const bool scores = bias != nullptr || choice->groups > 1;
+  const Mode mode = bias != nullptr || choice->groups > 1 ? kScores : dtype == NVFP4_MOE_F32 ? kLogits32 : kLogits16;
   const int64_t blocks = ceil_div64(tokens, kThreads / a.lanes);
   const hipStream_t st = (hipStream_t)stream;
-  if (choice->topk <= 2) launch_route<2>(a, chunks, scores, blocks, st);
-  else if (choice->topk <= 4) launch_route<4>(a, chunks, scores, blocks, st);
-  else if (choice->topk <= 8) launch_route<8>(a, chunks, scores, blocks, st);
-  else launch_route<16>(a, chunks, scores, blocks, st);
+  if (choice->topk <= 2) launch_route<2>(a, chunks, mode, blocks, st);
+  else if (choice->topk <= 4) launch_route<4>(a, chunks, mode, blocks, st);
+  else if (choice->topk <= 8) launch_route<8>(a, chunks, mode, blocks, st);
+  else launch_route<16>(a, chunks, mode, blocks, st);
   return launched();
 }
 

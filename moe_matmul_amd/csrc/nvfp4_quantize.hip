@@ -92,9 +92,12 @@ template <class T> struct RowSource {
 
   __device__ inline Block block(int64_t row, int, int kb) const {
     const int64_t at = (m > 0 ? row / m * batch_stride + row % m * row_stride : row * row_stride) + kb * 16;
+    Raw8<T> raw[2];
+    raw[0].load(x, at, vec);
+    raw[1].load(x, at + 8, vec);
     float v[16];
-    load8<T>(x, at, vec, v);
-    load8<T>(x, at + 8, vec, v + 8);
+    raw[0].values(v);
+    raw[1].values(v + 8);
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] *= scale;
     return encode(v);
@@ -136,11 +139,14 @@ template <class T> struct SwigluSource {
 
   __device__ inline Block block(int64_t row, int expert, int kb) const {
     const int64_t at = row * row_stride + kb * 16;
+    Raw8<T> raw[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) raw[i].load(c, at + i / 2 * k + i % 2 * 8, vec);
     float g[16], u[16], v[16];
-    load8<T>(c, at, vec, g);
-    load8<T>(c, at + 8, vec, g + 8);
-    load8<T>(c, at + k, vec, u);
-    load8<T>(c, at + k + 8, vec, u + 8);
+    raw[0].values(g);
+    raw[1].values(g + 8);
+    raw[2].values(u);
+    raw[3].values(u + 8);
     const float al = alpha == nullptr ? 1.f : alpha[expert];
     uint32_t top = 0;
 #pragma unroll
@@ -301,7 +307,7 @@ __global__ void __launch_bounds__(kTileThreads)
 
 // Dispatch: a token's row is quantised once and its codes stored to the rows of
 // all its slots. kDirect: so are its scales, a word at a time; else they go to
-// token_scales [tokens][padded] and nvfp4_dispatch_scales_kernel lays them out.
+// token_scales [tokens][atoms along k, padded to fours] and nvfp4_dispatch_scales_kernel lays them out.
 struct Slots {
   const int32_t *ids, *slot_rows, *offsets, *atoms;
   int topk, experts;
@@ -327,93 +333,101 @@ __global__ void __launch_bounds__(kRowThreads)
       *(uint32_t*)(sfa + (atom * (padded / 4) + p.kb / 4) * kAtomBytes + atom_row(at % kAtomRows)) = word;
     }
   }
-  if (!kDirect && p.kb % 4 == 0) token_scales[p.row * (padded / 4) + p.kb / 4] = word;
+  if (!kDirect && p.kb % 4 == 0) token_scales[p.row * (ceil_div(padded, 16) * 4) + p.kb / 4] = word;
 }
 
 // Scales of the rows sorted by expert, whole atoms at a time: thread = row of
-// the atom row, in the order in which its words lie.
+// the atom row, in the order in which its words lie. A token's words are padded
+// to a multiple of four, so that they are read four atoms at a time.
 constexpr int kScaleThreads = 128;
 constexpr int kScaleAtoms = 16;  // along K, of a workgroup
 __global__ void __launch_bounds__(kScaleThreads)
     nvfp4_dispatch_scales_kernel(const uint32_t* token_scales, const int32_t* row_slots, int topk, Rows rows,
                                  int along, uint8_t* sfa) {
-  const int chunks = ceil_div(along, kScaleAtoms);
+  const int chunks = ceil_div(along, kScaleAtoms), stride = ceil_div(along, 4) * 4;
   const int64_t atom = blockIdx.x / chunks;
-  const int from = blockIdx.x % chunks * kScaleAtoms, to = min(along, from + kScaleAtoms);
+  const int from = blockIdx.x % chunks * kScaleAtoms;
   int count, expert;
   const int64_t first = rows.first_row(atom, count, expert);
   if (count == 0) return;
   const int r = threadIdx.x / 4 + threadIdx.x % 4 * 32;
   const int64_t token = r < count ? row_slots[first + r] / topk : -1;
+  const uint32_t* in = token_scales + token * stride;
   uint32_t* out = (uint32_t*)(sfa + atom * along * kAtomBytes) + threadIdx.x;
-#pragma unroll 4
-  for (int k = from; k < to; ++k) out[k * (kAtomBytes / 4)] = token >= 0 ? token_scales[token * along + k] : 0u;
+  u32x4 word[kScaleAtoms / 4];
+#pragma unroll
+  for (int i = 0; i < kScaleAtoms / 4; ++i)
+    word[i] = token >= 0 && from + i * 4 < along ? *(const u32x4*)(in + from + i * 4) : u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int i = 0; i < kScaleAtoms; ++i)
+    if (from + i < along) out[(from + i) * (kAtomBytes / 4)] = word[i / 4][i % 4];
 }
 
 // ---- back to values ---------------------------------------------------------------
-__device__ inline void decode(u32x2 codes, uint32_t scale, float (&v)[16]) {
+// Eight values to a thread: a wave's stores then fill whole lines at once.
+__device__ inline void decode(uint32_t codes, uint32_t scale, float (&v)[8]) {
   const float s = e4m3_value(scale);
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint32_t w = h ? codes.y : codes.x;
-    const f32x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.f, 0);
-    const f32x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.f, 1);
-    const f32x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.f, 2);
-    const f32x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.f, 3);
-    v[h * 8 + 0] = p0.x * s;
-    v[h * 8 + 1] = p0.y * s;
-    v[h * 8 + 2] = p1.x * s;
-    v[h * 8 + 3] = p1.y * s;
-    v[h * 8 + 4] = p2.x * s;
-    v[h * 8 + 5] = p2.y * s;
-    v[h * 8 + 6] = p3.x * s;
-    v[h * 8 + 7] = p3.y * s;
-  }
+  const f32x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.f, 0);
+  const f32x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.f, 1);
+  const f32x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.f, 2);
+  const f32x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.f, 3);
+  v[0] = p0.x * s;
+  v[1] = p0.y * s;
+  v[2] = p1.x * s;
+  v[3] = p1.y * s;
+  v[4] = p2.x * s;
+  v[5] = p2.y * s;
+  v[6] = p3.x * s;
+  v[7] = p3.y * s;
 }
 
 template <class T>
 __global__ void __launch_bounds__(kRowThreads)
-    nvfp4_dequantize_rows_kernel(const uint8_t* a, const uint8_t* sfa, Rows rows, int blocks, void* out,
+    nvfp4_dequantize_rows_kernel(const uint32_t* a, const uint8_t* sfa, Rows rows, int blocks, void* out,
                                  int64_t row_stride, int vec) {
-  const Place p = place_of(blockIdx.x * kRowThreads + threadIdx.x, blocks);
+  const Place p = place_of(blockIdx.x * kRowThreads + threadIdx.x, 2 * blocks);  // halves of blocks
   const int64_t end = rows.offsets == nullptr ? rows.rows : rows.offsets[rows.experts];
   if (p.row >= end) return;
   int expert, r;
   int64_t atom;
   rows.find(p.row, expert, atom, r);
-  float v[16];
-  decode(*(const u32x2*)(a + (p.row * blocks + p.kb) * 8),
-         sfa[(atom * ceil_div(blocks, 4) + p.kb / 4) * kAtomBytes + atom_row(r) + p.kb % 4], v);
-  store8<T>(out, p.row * row_stride + p.kb * 16, vec, v);
-  store8<T>(out, p.row * row_stride + p.kb * 16 + 8, vec, v + 8);
+  const int kb = p.kb / 2;
+  float v[8];
+  decode(a[p.row * 2 * blocks + p.kb], sfa[(atom * ceil_div(blocks, 4) + kb / 4) * kAtomBytes + atom_row(r) + kb % 4], v);
+  store8<T>(out, p.row * row_stride + p.kb * 8, vec, v);
 }
 
 template <class T>
 __global__ void __launch_bounds__(kTileThreads)
-    nvfp4_dequantize_tiles_kernel(const uint8_t* a, const uint8_t* sfa, Rows rows, int blocks, void* out,
+    nvfp4_dequantize_tiles_kernel(const uint32_t* a, const uint8_t* sfa, Rows rows, int blocks, void* out,
                                   int64_t row_stride, int vec) {
   __shared__ uint32_t s_sf[kTileAtoms * kAtomBytes / 4];
+  constexpr int kHalves = 2 * kTileBlocks, kPassRows = kTileThreads / kHalves;
   const int along = ceil_div(blocks, 4), chunks = ceil_div(along, kTileAtoms);
   const int64_t atom = blockIdx.x / chunks;
   const int first_atom = blockIdx.x % chunks * kTileAtoms;
   int count, expert;
   const int64_t first = rows.first_row(atom, count, expert);
   if (count == 0) return;
+  const int half = threadIdx.x % kHalves, kh = first_atom * 8 + half;
+  uint32_t codes[kAtomRows / kPassRows];
+#pragma unroll
+  for (int pass = 0; pass < kAtomRows / kPassRows; ++pass) {
+    const int r = pass * kPassRows + threadIdx.x / kHalves;
+    codes[pass] = r < count && kh < 2 * blocks ? __builtin_nontemporal_load(a + (first + r) * 2 * blocks + kh) : 0u;
+  }
   const int words = min(kTileAtoms, along - first_atom) * (kAtomBytes / 4);
   const uint32_t* from = (const uint32_t*)(sfa + (atom * along + first_atom) * kAtomBytes);
   for (int i = threadIdx.x; i < words; i += kTileThreads) s_sf[i] = from[i];
   __syncthreads();
-  const int kt = threadIdx.x % kTileBlocks, kb = first_atom * 4 + kt;
-  if (kb >= blocks) return;
+  if (kh >= 2 * blocks) return;
 #pragma unroll
-  for (int pass = 0; pass < kAtomRows / (kTileThreads / kTileBlocks); ++pass) {
-    const int r = pass * (kTileThreads / kTileBlocks) + threadIdx.x / kTileBlocks;
+  for (int pass = 0; pass < kAtomRows / kPassRows; ++pass) {
+    const int r = pass * kPassRows + threadIdx.x / kHalves;
     if (r >= count) break;
-    float v[16];
-    decode(*(const u32x2*)(a + ((first + r) * blocks + kb) * 8),
-           ((const uint8_t*)s_sf)[kt / 4 * kAtomBytes + atom_row(r) + kt % 4], v);
-    store8<T>(out, (first + r) * row_stride + kb * 16, vec, v);
-    store8<T>(out, (first + r) * row_stride + kb * 16 + 8, vec, v + 8);
+    float v[8];
+    decode(codes[pass], ((const uint8_t*)s_sf)[half / 8 * kAtomBytes + atom_row(r) + half / 2 % 4], v);
+    store8<T>(out, (first + r) * row_stride + kh * 8, vec, v);
   }
 }
 
@@ -488,7 +502,7 @@ int nvfp4_moe_quantize(const void* x, int dtype, int l, int64_t m, int k, int64_
 
 size_t nvfp4_moe_dispatch_workspace_bytes(int64_t tokens, int topk, int k, int experts) {
   if (tokens <= 0 || topk < 1 || k <= 0 || direct_scales(tokens, topk, experts)) return 0;
-  return (size_t)tokens * ceil_div(k, kAtomK) * 4;
+  return (size_t)tokens * ceil_div(k, 4 * kAtomK) * 16;
 }
 
 int nvfp4_moe_dispatch(const void* x, int dtype, int64_t tokens, int topk, int k, int64_t row_stride, float scale,
@@ -556,17 +570,17 @@ int nvfp4_moe_dequantize(const void* a, const void* sfa, int l, int64_t m, int k
   const int blocks = k / 16;
   const bool tiles = tiles_pay(rows);
   const int64_t grid = tiles ? atom_rows(rows, l) * ceil_div(ceil_div(blocks, 4), kTileAtoms)
-                             : ceil_div64(rows.rows * blocks, kRowThreads);
+                             : ceil_div64(rows.rows * 2 * blocks, kRowThreads);
   if (grid > kMaxGrid) return NVFP4_ERR_INVALID;
   const hipStream_t st = (hipStream_t)stream;
   return with_type(dtype, [&](auto t) {
     using T = decltype(t);
     const int vec = wide_rows(out, dtype, row_stride);
     if (tiles)
-      nvfp4_dequantize_tiles_kernel<T><<<(unsigned)grid, kTileThreads, 0, st>>>((const uint8_t*)a, (const uint8_t*)sfa, rows,
+      nvfp4_dequantize_tiles_kernel<T><<<(unsigned)grid, kTileThreads, 0, st>>>((const uint32_t*)a, (const uint8_t*)sfa, rows,
                                                                                 blocks, out, row_stride, vec);
     else
-      nvfp4_dequantize_rows_kernel<T><<<(unsigned)grid, kRowThreads, 0, st>>>((const uint8_t*)a, (const uint8_t*)sfa, rows,
+      nvfp4_dequantize_rows_kernel<T><<<(unsigned)grid, kRowThreads, 0, st>>>((const uint32_t*)a, (const uint8_t*)sfa, rows,
                                                                               blocks, out, row_stride, vec);
     return launched();
   });
