@@ -80,8 +80,9 @@ typedef struct nvfp4_moe_choice {
  *   part in it.
  * A logit of -inf masks its expert: score 0 and never chosen. A token with
  * fewer eligible experts than topk gets id -1 and weight 0 in the other slots.
- * A NaN logit is never chosen. It, and with softmax a logit of +inf, makes the
- * weights of its token's chosen experts NaN. A choice value of NaN or -inf
+ * For the choice, a NaN logit counts as -inf and +inf as the largest fp32. A NaN
+ * logit, and with softmax one of +inf, makes the weights of its token's chosen
+ * experts NaN. A choice value of NaN or -inf
  * (through the bias) is never chosen either. A sum of scores that is 0 counts
  * as 1.
  *
@@ -170,7 +171,7 @@ size_t nvfp4_moe_dispatch_workspace_bytes(int64_t tokens, int topk, int k, int e
  * nvfp4_moe_swiglu - as nvfp4_moe_quantize for v = silu(g * alpha) * (u * alpha)
  * * scale of rows sorted by expert, c [rows][2k] with g in columns 0 .. k-1 and
  * u in k .. 2k-1; codes and scales are those of the exact v (evaluated in fp64
- * where fp32 cannot tell).
+ * where fp32 cannot tell; a v beyond fp32 counts as infinite).
  *   alpha    device fp32 [experts], or NULL for 1
  *   offsets, atoms  of the plan, or both NULL with experts == 1: `rows` rows of one group
  * rows is the size of c; rows from offsets[experts] on are not touched.

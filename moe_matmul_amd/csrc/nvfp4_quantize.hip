@@ -149,17 +149,20 @@ template <class T> struct SwigluSource {
     raw[3].values(u + 8);
     const float al = alpha == nullptr ? 1.f : alpha[expert];
     uint32_t top = 0;
+    float factor = 0.f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const float ga = g[i] * al;
+      const float ga = g[i] * al, ua = u[i] * al * scale;
       const float sigmoid = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(ga * -1.44269502f));
-      v[i] = ga * sigmoid * (u[i] * al) * scale;
+      v[i] = ga * sigmoid * ua;
+      factor = fmaxf(factor, fabsf(ua));
       top = max(top, __builtin_bit_cast(uint32_t, v[i]) & 0x7FFFFFFFu);
     }
     Block b;
     const float sixth = __builtin_bit_cast(float, top) * (1.f / 6.f);
     b.scale = e4m3_of(sixth * (1.f - kUnsure));
-    bool unsure = b.scale != e4m3_of(sixth * (1.f + kUnsure));
+    // a sigmoid below 2^-126 is 0 here: g times it would count with a factor this large only
+    bool unsure = factor > 0x1p+90f || b.scale != e4m3_of(sixth * (1.f + kUnsure));
     const float s = e4m3_value(b.scale), inverse = s == 0.f ? 0.f : __builtin_amdgcn_rcpf(s);
     const float low = inverse * (1.f - kUnsure), high = inverse * (1.f + kUnsure);
     float q[16], r[16];
