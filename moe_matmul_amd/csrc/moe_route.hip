@@ -14,7 +14,7 @@ constexpr int kThreads = 256;
 constexpr double kLargest = 0x1p+1000;  // choice values are held within +-this, so that a key stays finite
 constexpr int kIndexMask = NVFP4_MOE_MAX_EXPERTS - 1;
 constexpr int kLeastLanes = 4;  // of a token
-constexpr int64_t kEnoughLanes = 256 * 1024;
+constexpr int64_t kLogitLanes = 64 * 1024, kScoreLanes = 256 * 1024;  // in all, that fill the chip
 
 // ---- keys: a choice value and its expert in one number ------------------------
 // The low bits hold the index such that of two equal values the lower index has
@@ -182,8 +182,25 @@ template <class W, int K> __device__ inline void merge_lanes(typename W::Key (&l
   if (lanes > 32) merge_across<W, K>(list, 32);
 }
 
+template <int kCtrl> __device__ inline uint32_t lane_bits(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, kCtrl, 0xF, 0xF, false);
+}
+template <int kCtrl, class V> __device__ inline V from_lane(V v) {
+  if constexpr (sizeof(V) == 8) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    return __builtin_bit_cast(V, (uint64_t)lane_bits<kCtrl>((uint32_t)(u >> 32)) << 32 | lane_bits<kCtrl>((uint32_t)u));
+  } else {
+    return __builtin_bit_cast(V, lane_bits<kCtrl>(__builtin_bit_cast(uint32_t, v)));
+  }
+}
+// op over the values of a token's `lanes` (a power of two), in all of them; in a fixed order.
 template <class V, class Op> __device__ inline V across(V v, int lanes, Op op) {
-  for (int d = 1; d < lanes; d *= 2) v = op(v, __shfl_xor(v, d));
+  if (lanes > 1) v = op(v, from_lane<kXor1>(v));
+  if (lanes > 2) v = op(v, from_lane<kXor2>(v));
+  if (lanes > 4) v = op(v, from_lane<kMirror8>(v));
+  if (lanes > 8) v = op(v, from_lane<kMirror16>(v));
+  if (lanes > 16) v = op(v, __shfl_xor(v, 16));
+  if (lanes > 32) v = op(v, __shfl_xor(v, 32));
   return v;
 }
 __device__ inline float max_across(float v, int lanes) {
@@ -206,13 +223,18 @@ struct RouteArgs {
   const float* bias;
   int32_t* ids;
   float* weights;
-  int experts, dtype, vec;
-  int lanes;      // per token
-  int per;        // experts of a group
-  int lanes_of;   // lanes that share a group (1 where a lane has whole groups)
-  int groups_of;  // groups that a lane has (1 where lanes share one)
+  int experts, dtype, vec, bias_vec;
+  int lanes, lane_bits;  // per token, and their logarithm
+  int per;               // experts of a group
+  int part;              // of these, a lane's where lanes share one
+  int lanes_of;          // lanes that share a group (1 where a lane has whole groups)
+  int inverse_of;        // 2^16 / lanes_of, rounded up
+  int groups_of;         // groups that a lane has (1 where lanes share one)
   nvfp4_moe_choice how;
 };
+
+// The group that a lane has a part of: lane / lanes_of, for lanes below 64.
+__device__ inline int group_of(const RouteArgs& a, int lane) { return (lane * a.inverse_of) >> 16; }
 
 __device__ inline Share share_of(const RouteArgs& a, int lane) {
   Share s;
@@ -221,10 +243,10 @@ __device__ inline Share share_of(const RouteArgs& a, int lane) {
     s.step = a.lanes * 8;
     s.end = a.experts;
   } else if (a.lanes_of > 1) {
-    const int g = lane / a.lanes_of, part = (a.per + a.lanes_of - 1) / a.lanes_of, at = lane % a.lanes_of * part;
+    const int g = group_of(a, lane), at = (lane - g * a.lanes_of) * a.part;
     s.base = g * a.per + at;
     s.step = 8;
-    s.end = g < a.how.groups ? g * a.per + min(a.per, at + part) : 0;
+    s.end = g < a.how.groups ? g * a.per + min(a.per, at + a.part) : 0;
   } else {
     s.base = lane * a.groups_of * a.per;
     s.step = 8;
@@ -263,26 +285,205 @@ __device__ inline float load_logit(const void* logits, int dtype, int64_t at) {
                                   : load1<BF16>(logits, at);
 }
 
-__device__ inline bool poisons(float x, int score) {
-  return x != x || (score == NVFP4_MOE_SOFTMAX && x == __builtin_inff());
+// Whether the choice goes by the logits (as 32-bit keys where they have 16 bits)
+// or by scores (a bias, or groups).
+enum Mode { kLogits16, kLogits32, kScores };
+
+// How many groups precede group g of a token, by worth and then by index:
+// certainly, and possibly, where worths within 2 * margin of each other may be equal.
+template <class V> __device__ inline void rank_of(const V* worth, int groups, int g, V margin, int& least, int& most) {
+  const V w = worth[g];
+  least = most = 0;
+  for (int o = 0; o < groups; ++o) {
+    const V u = worth[o];
+    const bool before = u > w || (u == w && o < g);
+    least += margin == V(0) ? before : u > w + 2 * margin;
+    most += margin == V(0) ? before : o != g && u + 2 * margin >= w;
+  }
 }
 
-// Whether the choice goes by the logits (as 32-bit keys where they have 16 bits)
-// or by scores (a bias, or groups), which are then computed in fp64.
-enum Mode { kLogits16, kLogits32, kScores };
+template <class Key> __device__ inline void best_two(Key v, Key& one, Key& two) {
+  two = max(two, min(one, v));
+  one = max(one, v);
+}
+
+// The choice by scores in fp32, as 23-bit fixed-point numbers below the token's
+// largest choice value (0 for one that is 1 or more below it, and for none) over
+// the index: half the instructions of the
+// fp64 choice, and cheaper ones. In units of 2^-22 a number is off the exact
+// value by 1 for the score (e^-x within (|x| + 2) 2^-24, times s (1 - s); its sum
+// and reciprocal), 1 for the sum with a bias (values up to 5), 1.75 for the
+// difference and its truncation; with softmax by as much for the
+// score, and 11 more for the sum of up to 512 terms (a factor that all scores
+// share). Returns whether the list is that of the exact values: no two
+// neighbours in it, no candidate next to its end and no groups at the cut are
+// as near to each other as two such errors.
+constexpr uint32_t kSigmoidMargin = 8, kSoftmaxMargin = 32;
+template <int K, int NC>
+__device__ inline bool choose_fp32(const RouteArgs& a, const Share& s, int lane, const float (&x)[NC * 8],
+                                   const float (&bias)[NC * 8], float from, float inverse, uint32_t (*s_best)[4],
+                                   uint32_t* s_worth, uint32_t (&list)[K]) {
+  const bool softmax = a.how.score == NVFP4_MOE_SOFTMAX;
+  const uint32_t margin = softmax ? kSoftmaxMargin : kSigmoidMargin;
+  float value[NC * 8], top = -__builtin_inff();
+#pragma unroll
+  for (int i = 0; i < NC * 8; ++i) {
+    const float e = __builtin_amdgcn_exp2f((softmax ? x[i] - from : -x[i]) * 1.44269502f);
+    value[i] = (softmax ? e * inverse : __builtin_amdgcn_rcpf(1.f + e)) + bias[i];
+    value[i] = x[i] > -__builtin_inff() ? value[i] : -__builtin_inff();  // not for NaN
+    top = fmaxf(top, value[i]);
+  }
+  top = max_across(top, a.lanes);
+  bool sure = fabsf(top) <= 4.f;  // not for a token without candidates
+  uint32_t v[NC * 8];
+#pragma unroll
+  for (int i = 0; i < NC * 8; ++i) {
+    const int e = s.base + i / 8 * s.step + i % 8;
+    const float fixed = fmaxf(fmaf(value[i], 0x1p22f, 0x1p22f - top * 0x1p22f), 0.f);  // 0 for NaN
+    v[i] = (uint32_t)fminf(fixed, 0x1p22f) << 9 | (uint32_t)(kIndexMask - e);
+  }
+  if (a.how.groups > 1) {
+    auto worth = [&](uint32_t one, uint32_t two) {
+      if (a.how.group_best == 1) return one >> 9;
+      sure &= two >> 9 > 0;  // without a second candidate, or with a far one, sums cannot be compared
+      return (one >> 9) + (two >> 9);
+    };
+    if (a.groups_of == 1) {
+      uint32_t one = 0, two = 0;
+#pragma unroll
+      for (int i = 0; i < NC * 8; ++i) best_two(v[i], one, two);
+      s_best[threadIdx.x][0] = one;
+      s_best[threadIdx.x][1] = two;
+      wave_sync();
+      for (int g = lane; g < a.how.groups; g += a.lanes) {
+        one = two = 0;
+        for (int q = 0; q < a.lanes_of; ++q) {
+          const int at = threadIdx.x - lane + g * a.lanes_of + q;
+          two = max(s_best[at][1], two);
+          best_two(s_best[at][0], one, two);
+        }
+        s_worth[g] = worth(one, two);
+      }
+    } else {
+      for (int q = 0; q < a.groups_of; ++q) {
+        const int g = lane * a.groups_of + q;
+        if (g >= a.how.groups) break;
+        uint32_t one = 0, two = 0;
+#pragma unroll
+        for (int i = 0; i < NC * 8; ++i) best_two(i / a.per == q ? v[i] : 0u, one, two);
+        s_worth[g] = worth(one, two);
+      }
+    }
+    wave_sync();
+    for (int q = 0; q < a.groups_of; ++q) {
+      const int g = a.groups_of == 1 ? group_of(a, lane) : lane * a.groups_of + q;
+      int least = a.how.groups, most = a.how.groups;
+      if (g < a.how.groups) rank_of(s_worth, a.how.groups, g, margin, least, most);
+      sure &= least >= a.how.topk_groups || most < a.how.topk_groups;
+#pragma unroll
+      for (int i = 0; i < NC * 8; ++i)
+        if ((a.groups_of == 1 || i / a.per == q) && least >= a.how.topk_groups) v[i] = 0u;
+    }
+  }
+  keep_largest<Narrow, K, NC * 8>(v, list);
+  merge_lanes<Narrow, K>(list, a.lanes);
+  uint32_t last = 0;  // the last chosen
+#pragma unroll
+  for (int i = 0; i < K; ++i) {
+    last = i < a.how.topk ? list[i] : last;
+    if (i + 1 < K) sure &= i + 1 >= a.how.topk || list[i] - list[i + 1 < K ? i + 1 : i] > (margin + 1) << 9;
+  }
+  sure &= last >> 9 > margin;
+  const uint32_t near = last - (margin << 9);
+  int count = 0;
+#pragma unroll
+  for (int i = 0; i < NC * 8; ++i) count += (v[i] | kIndexMask) >= near;
+  return sure && sum_across(count, a.lanes) == a.how.topk;
+}
+
+// The same in fp64, for any values.
+template <int K, int NC>
+__device__ inline void choose_fp64(const RouteArgs& a, const Share& s, int lane, const float (&x)[NC * 8],
+                                   const float (&bias)[NC * 8], float top, double (*s_best)[2], double* s_worth,
+                                   double (&list)[K]) {
+  double v[NC * 8];
+  if (a.how.score == NVFP4_MOE_SOFTMAX) {
+    const double from = top == -__builtin_inff() ? 0.0 : (double)fminf(top, 3.4e38f);
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < NC * 8; ++i) {
+      v[i] = exp_f64((double)x[i] - from);
+      sum += x[i] > -__builtin_inff() ? v[i] : 0.0;
+    }
+    sum = sum_across(sum, a.lanes);
+    const double inverse = inverse_f64(sum > 0.0 ? sum : 1.0);
+#pragma unroll
+    for (int i = 0; i < NC * 8; ++i) v[i] *= inverse;
+  } else {
+#pragma unroll
+    for (int i = 0; i < NC * 8; ++i) v[i] = inverse_f64(1.0 + exp_f64(-(double)x[i]));
+  }
+#pragma unroll
+  for (int i = 0; i < NC * 8; ++i) {
+    const int e = s.base + i / 8 * s.step + i % 8;
+    v[i] = x[i] > -__builtin_inff() ? Wide::make(v[i] + bias[i], e) : Wide::none();  // none for a NaN logit, too
+  }
+  if (a.how.groups > 1) {
+    auto worth = [&](double one, double two) {
+      return a.how.group_best == 1 || !Wide::there(two) ? Wide::value(one) : Wide::value(one) + Wide::value(two);
+    };
+    if (a.groups_of == 1) {
+      double one = Wide::none(), two = Wide::none();
+#pragma unroll
+      for (int i = 0; i < NC * 8; ++i) best_two(v[i], one, two);
+      s_best[threadIdx.x][0] = one;
+      s_best[threadIdx.x][1] = two;
+      wave_sync();
+      for (int g = lane; g < a.how.groups; g += a.lanes) {
+        one = two = Wide::none();
+        for (int q = 0; q < a.lanes_of; ++q) {
+          const int at = threadIdx.x - lane + g * a.lanes_of + q;
+          two = fmax(s_best[at][1], two);
+          best_two(s_best[at][0], one, two);
+        }
+        s_worth[g] = worth(one, two);
+      }
+    } else {
+      for (int q = 0; q < a.groups_of; ++q) {
+        const int g = lane * a.groups_of + q;
+        if (g >= a.how.groups) break;
+        double one = Wide::none(), two = Wide::none();
+#pragma unroll
+        for (int i = 0; i < NC * 8; ++i) best_two(i / a.per == q ? v[i] : Wide::none(), one, two);
+        s_worth[g] = worth(one, two);
+      }
+    }
+    wave_sync();
+    for (int q = 0; q < a.groups_of; ++q) {
+      const int g = a.groups_of == 1 ? group_of(a, lane) : lane * a.groups_of + q;
+      int before = a.how.groups, most;
+      if (g < a.how.groups) rank_of(s_worth, a.how.groups, g, 0.0, before, most);
+#pragma unroll
+      for (int i = 0; i < NC * 8; ++i)
+        if ((a.groups_of == 1 || i / a.per == q) && before >= a.how.topk_groups) v[i] = Wide::none();
+    }
+  }
+  keep_largest<Wide, K, NC * 8>(v, list);
+  merge_lanes<Wide, K>(list, a.lanes);
+}
 
 // Routing. A token's logits are read once into the registers of `lanes` lanes;
 // each lane keeps the K largest keys of its experts in a sorted list (sort K,
 // merge them in: two instructions for each comparison), and the lanes' lists are
 // merged in log2(lanes) steps. Bound by these instructions, not by the logits.
+// A choice by scores is made in fp32, and again in fp64 by a wave that holds a
+// token for which fp32 cannot tell.
 template <int K, int NC, Mode kMode>
-__global__ void __launch_bounds__(kThreads) nvfp4_moe_route_kernel(RouteArgs a) {
-  typedef typename std::conditional<kMode == kLogits16, Narrow, Wide>::type W;
-  typedef typename W::Key Key;
-  extern __shared__ double s_group[];  // [tokens][groups]
+__global__ void __launch_bounds__(kThreads, NC > 2 ? 2 : 4) nvfp4_moe_route_kernel(RouteArgs a) {
+  extern __shared__ double s_worth[];  // [tokens][groups]
   __shared__ double s_best[kMode == kScores ? kThreads : 1][2];
-  const int lane = threadIdx.x & (a.lanes - 1), local = threadIdx.x / a.lanes;
-  const int64_t mine = (int64_t)blockIdx.x * (kThreads / a.lanes) + local;
+  const int lane = threadIdx.x & (a.lanes - 1), local = threadIdx.x >> a.lane_bits;
+  const int64_t mine = (int64_t)blockIdx.x * (kThreads >> a.lane_bits) + local;
   const int64_t token = mine < a.tokens ? mine : a.tokens - 1;  // lanes past the end repeat the last token
   const Share s = share_of(a, lane);
   float x[NC * 8];
@@ -292,25 +493,61 @@ __global__ void __launch_bounds__(kThreads) nvfp4_moe_route_kernel(RouteArgs a) 
   float top = -__builtin_inff();
 #pragma unroll
   for (int i = 0; i < NC * 8; ++i) {
-    bad |= poisons(x[i], a.how.score);
+    bad |= x[i] != x[i];
     top = fmaxf(top, x[i]);  // passes over NaN
   }
+  bad |= a.how.score == NVFP4_MOE_SOFTMAX && top == __builtin_inff();
   const uint64_t lanes_mask = (a.lanes == 64 ? ~0ull : (1ull << a.lanes) - 1) << (threadIdx.x & 63 & ~(a.lanes - 1));
   bad = (__ballot(bad) & lanes_mask) != 0;
 
   const bool softmax = a.how.score == NVFP4_MOE_SOFTMAX;
   float total = 1.f;  // of e^(x - top) over all experts
-  Key v[NC * 8];
-  if constexpr (kMode != kScores) {
-    if (softmax && !a.how.renormalize) {
-      top = max_across(top, a.lanes);
-      const float from = top == -__builtin_inff() ? 0.f : top;
-      total = 0.f;
-      // the plain product's error, |x - top| 2^-24 of a term, is small where the term is not
+  if (softmax && (kMode == kScores || !a.how.renormalize)) {
+    top = max_across(top, a.lanes);
+    const float from = top == -__builtin_inff() ? 0.f : top;
+    total = 0.f;
+    // the plain product's error, |x - top| 2^-24 of a term, is small where the term is not
 #pragma unroll
-      for (int i = 0; i < NC * 8; ++i) total += __builtin_amdgcn_exp2f((x[i] - from) * 1.44269502f);
-      total = sum_across(total, a.lanes);
+    for (int i = 0; i < NC * 8; ++i) {
+      const float e = __builtin_amdgcn_exp2f((x[i] - from) * 1.44269502f);
+      total += kMode == kScores && x[i] != x[i] ? 0.f : e;
     }
+    total = sum_across(total, a.lanes);
+  }
+  int chosen_ids[K];
+  if constexpr (kMode == kScores) {
+    float bias[NC * 8];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int e = s.base + c * s.step;
+      float b[8] = {};
+      if (a.bias != nullptr) {
+        if (e + 8 <= s.end) {
+          load8<F32>(a.bias, e, a.bias_vec && e % 4 == 0, b);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) b[j] = e + j < s.end ? a.bias[e + j] : 0.f;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) bias[c * 8 + j] = b[j];
+    }
+    // both forms of the choice use a wave's own parts of s_best and s_worth
+    uint32_t list[K];
+    const bool sure = choose_fp32<K, NC>(a, s, lane, x, bias, top, 1.f / total, (uint32_t(*)[4])s_best,
+                                         (uint32_t*)(s_worth + local * a.how.groups), list);
+#pragma unroll
+    for (int i = 0; i < K; ++i) chosen_ids[i] = kIndexMask - (int)(list[i] & kIndexMask);
+    if (__any(!sure)) {
+      double exact[K];
+      wave_sync();
+      choose_fp64<K, NC>(a, s, lane, x, bias, top, s_best, s_worth + local * a.how.groups, exact);
+#pragma unroll
+      for (int i = 0; i < K; ++i) chosen_ids[i] = Wide::index(exact[i]);
+    }
+  } else {
+    typedef typename std::conditional<kMode == kLogits16, Narrow, Wide>::type W;
+    typename W::Key v[NC * 8], list[K];
     const bool half = a.dtype == NVFP4_MOE_F16;
 #pragma unroll
     for (int i = 0; i < NC * 8; ++i) {
@@ -322,92 +559,11 @@ __global__ void __launch_bounds__(kThreads) nvfp4_moe_route_kernel(RouteArgs a) 
         v[i] = Wide::of_logit(x[i], e);
       }
     }
-  } else {
-    if (softmax) {
-      top = max_across(top, a.lanes);
-      const double from = top == -__builtin_inff() ? 0.0 : (double)fminf(top, 3.4e38f);
-      double sum = 0.0;
+    keep_largest<W, K, NC * 8>(v, list);
+    merge_lanes<W, K>(list, a.lanes);
 #pragma unroll
-      for (int i = 0; i < NC * 8; ++i) {
-        v[i] = exp_f64((double)x[i] - from);
-        sum += x[i] > -__builtin_inff() ? v[i] : 0.0;
-      }
-      sum = sum_across(sum, a.lanes);
-      total = (float)sum;
-      const double inverse = inverse_f64(sum > 0.0 ? sum : 1.0);
-#pragma unroll
-      for (int i = 0; i < NC * 8; ++i) v[i] *= inverse;
-    } else {
-#pragma unroll
-      for (int i = 0; i < NC * 8; ++i) v[i] = inverse_f64(1.0 + exp_f64(-(double)x[i]));
-    }
-#pragma unroll
-    for (int i = 0; i < NC * 8; ++i) {
-      const int e = s.base + i / 8 * s.step + i % 8;
-      if (a.bias != nullptr) v[i] += e < s.end ? (double)a.bias[e] : 0.0;
-      v[i] = x[i] > -__builtin_inff() ? Wide::make(v[i], e) : Wide::none();  // none for a NaN logit, too
-    }
-    if (a.how.groups > 1) {
-      // The best two of each lane, or the values of each lane's groups, then a
-      // group's rank: how many groups are better.
-      auto worth = [&](double first, double second) {
-        const double f = Wide::value(first), g = Wide::value(second);
-        return a.how.group_best == 1 || !Wide::there(second) ? f : f + g;
-      };
-      if (a.groups_of == 1) {
-        double one = Wide::none(), two = Wide::none();
-#pragma unroll
-        for (int i = 0; i < NC * 8; ++i) {
-          two = fmax(two, fmin(one, v[i]));
-          one = fmax(one, v[i]);
-        }
-        s_best[threadIdx.x][0] = one;
-        s_best[threadIdx.x][1] = two;
-        __syncthreads();
-        for (int g = lane; g < a.how.groups; g += a.lanes) {
-          double first = Wide::none(), second = Wide::none();
-          for (int q = 0; q < a.lanes_of; ++q) {
-            const int from = threadIdx.x - lane + g * a.lanes_of + q;
-            const double p = s_best[from][0], r = s_best[from][1];
-            second = fmax(fmax(second, r), fmin(first, p));
-            first = fmax(first, p);
-          }
-          s_group[local * a.how.groups + g] = worth(first, second);
-        }
-      } else {
-        for (int q = 0; q < a.groups_of; ++q) {
-          const int g = lane * a.groups_of + q;
-          if (g >= a.how.groups) break;
-          double one = Wide::none(), two = Wide::none();
-#pragma unroll
-          for (int i = 0; i < NC * 8; ++i) {
-            const double w = i / a.per == q ? v[i] : Wide::none();
-            two = fmax(two, fmin(one, w));
-            one = fmax(one, w);
-          }
-          s_group[local * a.how.groups + g] = worth(one, two);
-        }
-      }
-      __syncthreads();
-      for (int q = 0; q < a.groups_of; ++q) {
-        const int g = a.groups_of == 1 ? lane / a.lanes_of : lane * a.groups_of + q;
-        const double w = g < a.how.groups ? s_group[local * a.how.groups + g] : Wide::none();
-        int better = 0;
-        for (int o = 0; o < a.how.groups; ++o) {
-          const double u = s_group[local * a.how.groups + o];
-          better += u > w || (u == w && o < g);
-        }
-#pragma unroll
-        for (int i = 0; i < NC * 8; ++i) {
-          const bool of = a.groups_of == 1 || i / a.per == q;
-          if (of && better >= a.how.topk_groups) v[i] = Wide::none();
-        }
-      }
-    }
+    for (int i = 0; i < K; ++i) chosen_ids[i] = W::index(list[i]);
   }
-  Key list[K];
-  keep_largest<W, K, NC * 8>(v, list);
-  merge_lanes<W, K>(list, a.lanes);
 
   // slot j belongs to lane j % lanes: slots of a lane are K / lanes at most
   constexpr int kLaneSlots = K > kLeastLanes ? K / kLeastLanes : 1;
@@ -416,10 +572,9 @@ __global__ void __launch_bounds__(kThreads) nvfp4_moe_route_kernel(RouteArgs a) 
 #pragma unroll
   for (int q = 0; q < kLaneSlots; ++q) {
     const int slot = q * a.lanes + lane;
-    Key key = W::none();
+    ids[q] = -1;
 #pragma unroll
-    for (int i = 0; i < K; ++i) key = i == slot ? list[i] : key;
-    ids[q] = slot < a.how.topk ? W::index(key) : -1;
+    for (int i = 0; i < K; ++i) ids[q] = i == slot && i < a.how.topk ? chosen_ids[i] : ids[q];
     chosen[q] = ids[q] >= 0 ? load_logit(a.logits, a.dtype, token * a.row_stride + ids[q]) : -__builtin_inff();
     largest = fmaxf(largest, chosen[q]);
   }
@@ -430,16 +585,16 @@ __global__ void __launch_bounds__(kThreads) nvfp4_moe_route_kernel(RouteArgs a) 
 #pragma unroll
   for (int q = 0; q < kLaneSlots; ++q) {
     if (softmax) w[q] = exp_f32(chosen[q] - from);
-    else w[q] = ids[q] >= 0 ? 1.f / (1.f + exp_f32(-chosen[q])) : 0.f;
+    else w[q] = ids[q] >= 0 ? __builtin_amdgcn_rcpf(1.f + exp_f32(-chosen[q])) : 0.f;
     sum += w[q];
   }
   if (a.how.renormalize) total = sum_across(sum, share);
   else if (!softmax) total = 1.f;
-  if (total == 0.f) total = 1.f;
+  const float factor = total == 0.f ? a.how.scale : a.how.scale / total;
 #pragma unroll
   for (int q = 0; q < kLaneSlots; ++q) {
     const int slot = q * a.lanes + lane;
-    float y = w[q] / total * a.how.scale;
+    float y = w[q] * factor;
     if (ids[q] < 0) y = 0.f;
     else if (bad) y = __builtin_nanf("");
     if (slot < a.how.topk && mine < a.tokens) {
@@ -585,9 +740,11 @@ int at_least_pow2(int v) {
 }
 
 // Lanes of a token: few, as the lanes' merged lists are the same work in each of
-// them, but more where there are too few tokens to fill the chip.
-int widen(int lanes, int64_t tokens, int experts) {
-  while (lanes < 64 && tokens * lanes < kEnoughLanes && lanes * 8 < experts) lanes *= 2;
+// them, but more where there are too few tokens to fill the chip (15000 tokens x
+// 256 logits: 9.7 us with 8 lanes, 13.4 with 16; 16384 x 256 scores, which take
+// three times as long before the merges: 20 us with 8, 16.8 with 16).
+int widen(int lanes, int64_t tokens, int experts, int64_t enough) {
+  while (lanes < 64 && tokens * lanes < enough && lanes * 8 < experts) lanes *= 2;
   return lanes;
 }
 
@@ -596,10 +753,13 @@ int lay_out(RouteArgs& a) {
   const int groups = a.how.groups;
   a.per = a.experts / groups;
   a.lanes_of = a.groups_of = 1;
+  a.lane_bits = __builtin_ctz(a.lanes);
   if (groups == 1) return ceil_div(ceil_div(a.experts, 8), a.lanes);
   if (a.lanes >= groups) a.lanes_of = a.lanes / groups;
   else a.groups_of = ceil_div(groups, a.lanes);
-  return ceil_div(a.groups_of > 1 ? a.groups_of * a.per : ceil_div(a.per, a.lanes_of), 8);
+  a.inverse_of = ceil_div(1 << 16, a.lanes_of);
+  a.part = ceil_div(a.per, a.lanes_of);
+  return ceil_div(a.groups_of > 1 ? a.groups_of * a.per : a.part, 8);
 }
 
 template <int K, int NC> void launch_route(const RouteArgs& a, Mode mode, int64_t blocks, hipStream_t stream) {
@@ -632,6 +792,7 @@ int nvfp4_moe_route(const void* logits, int dtype, int64_t tokens, int experts, 
   if (tokens > 0 && (ids == nullptr || weights == nullptr)) return NVFP4_ERR_INVALID;
   if (!aligned(ids, 4) || !aligned(weights, 4) || !aligned(bias, 4)) return NVFP4_ERR_MISALIGNED;
   if (tokens == 0) return NVFP4_OK;
+  const Mode mode = bias != nullptr || choice->groups > 1 ? kScores : dtype == NVFP4_MOE_F32 ? kLogits32 : kLogits16;
   RouteArgs a = {};
   a.logits = logits;
   a.tokens = tokens;
@@ -642,14 +803,14 @@ int nvfp4_moe_route(const void* logits, int dtype, int64_t tokens, int experts, 
   a.experts = experts;
   a.dtype = dtype;
   a.vec = wide_rows(logits, dtype, row_stride);
+  a.bias_vec = aligned(bias, 16);
   a.how = *choice;
-  a.lanes = widen(kLeastLanes, tokens, experts);
+  a.lanes = widen(kLeastLanes, tokens, experts, mode == kScores ? kScoreLanes : kLogitLanes);
   int chunks = lay_out(a);
   while (chunks > 4) {
     a.lanes *= 2;
     chunks = lay_out(a);
   }
-  const Mode mode = bias != nullptr || choice->groups > 1 ? kScores : dtype == NVFP4_MOE_F32 ? kLogits32 : kLogits16;
   const int64_t blocks = ceil_div64(tokens, kThreads / a.lanes);
   const hipStream_t st = (hipStream_t)stream;
   if (choice->topk <= 2) launch_route<2>(a, chunks, mode, blocks, st);
@@ -681,7 +842,7 @@ int nvfp4_moe_route_backward(const void* logits, int dtype, int64_t tokens, int 
   a.vec = wide_rows(logits, dtype, row_stride);
   a.out_vec = wide_rows(dlogits, dtype, dlogits_stride);
   a.how = *choice;
-  a.lanes = widen(at_least_pow2(choice->topk < 4 ? 4 : choice->topk), tokens, experts);
+  a.lanes = widen(at_least_pow2(choice->topk < 4 ? 4 : choice->topk), tokens, experts, kScoreLanes);
   while (ceil_div(experts, 8 * a.lanes) > 4) a.lanes *= 2;
   const int chunks = ceil_div(experts, 8 * a.lanes);
   const dim3 grid((unsigned)ceil_div64(tokens, kThreads / a.lanes));
