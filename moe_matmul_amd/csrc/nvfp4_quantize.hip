@@ -5,13 +5,13 @@
 namespace moe {
 namespace {
 
-constexpr int kTileThreads = 512;
+constexpr int kTileThreads = 1024;
 constexpr int kTileAtoms = 4;                        // atoms along K of a tile: 256 K-elements
-constexpr int kTileBlocks = kTileAtoms * 4;          // 16-element blocks of a tile's row
+constexpr int kTileHalves = kTileAtoms * 8;          // halves of 16-element blocks of a tile's row
 constexpr int kRowThreads = 256;
 constexpr int64_t kMaxGrid = (1 << 23) - 1;          // workgroups: fewer than 2^32 threads, and 2^31 of a row kernel
 
-// ---- one block of 16 ---------------------------------------------------------
+// ---- half a block of 16 to a lane: a wave's loads and stores take whole lines ---------------------------------------------------------
 // The rounding of a quotient to few bits is exact where the quotient is rounded
 // to odd before: the nearest fp32 q to a / s, moved towards zero if it is above
 // a / s, with the last bit set if it is not a / s itself. `inverse` is the
@@ -50,57 +50,106 @@ __device__ inline uint32_t e2m1_word(const float* q) {
   return e2m1_pair<3>(w, q[6], q[7]);
 }
 
-struct Block {
-  u32x2 codes;
-  uint32_t scale;  // E4M3 byte
+// The other lane of a block's two.
+__device__ inline uint32_t pair(uint32_t v) { return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, false); }
+__device__ inline double pair(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, (uint64_t)pair((uint32_t)(u >> 32)) << 32 | pair((uint32_t)u));
+}
+
+struct Half {
+  uint32_t codes;  // of eight elements
+  uint32_t scale;  // E4M3 byte of their block
 };
 
 constexpr uint32_t kInfBits = 0x7F800000u, kScaleNan = 0x7Fu;
 
-__device__ inline Block encode(const float (&v)[16]) {
+__device__ inline Half encode(const float (&v)[8]) {
   uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) top = max(top, __builtin_bit_cast(uint32_t, v[i]) & 0x7FFFFFFFu);
-  Block b;
+  for (int i = 0; i < 8; ++i) top = max(top, __builtin_bit_cast(uint32_t, v[i]) & 0x7FFFFFFFu);
+  top = max(top, pair(top));
+  Half b;
   const float sixth = __builtin_bit_cast(float, quotient_to_odd(__builtin_bit_cast(float, top), 6.f, 1.f / 6.f));
   b.scale = e4m3_of(sixth);
   const float s = e4m3_value(b.scale), inverse = s == 0.f ? 0.f : 1.f / s;
-  float q[16];
+  float q[8];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
+  for (int i = 0; i < 8; ++i) {
     const uint32_t u = quotient_to_odd(fabsf(v[i]), s, inverse);
     q[i] = __builtin_bit_cast(float, u | (__builtin_bit_cast(uint32_t, v[i]) & 0x80000000u));
   }
-  b.codes.x = e2m1_word(q);
-  b.codes.y = e2m1_word(q + 8);
-  if (top >= kInfBits) {  // an infinity or NaN in the block
-    b.scale = kScaleNan;
-    b.codes = u32x2{0u, 0u};
-  } else if (b.scale == 0) {
-    b.codes = u32x2{0u, 0u};
-  }
+  b.codes = b.scale == 0 ? 0u : e2m1_word(q);
+  if (top >= kInfBits) b = {0u, kScaleNan};  // an infinity or NaN in the block
   return b;
 }
 
-// ---- where blocks come from ----------------------------------------------------
-template <class T> struct RowSource {
+// The same for 16-bit values as they are. They and the borders of the rounding
+// (s times 3-bit numbers) have so few bits that a quotient either is a border or
+// is off it by 2^-8 (bf16) or 2^-11 (fp16) of its value: bf16 quotients may lose
+// all but 11 bits before, which restores those that are borders from an error of
+// an ulp or two; fp16 ones are made the nearest fp32 as above.
+template <class T> __device__ inline Half encode_16bit(const Raw8<T>& x) {
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  constexpr uint32_t kInf16 = T::kId == NVFP4_MOE_F16 ? 0x7C00u : 0x7F80u;
+  u16x2 tops = {0, 0};  // magnitudes order as whole numbers
+#pragma unroll
+  for (int i = 0; i < 4; ++i) tops = __builtin_elementwise_max(tops, __builtin_bit_cast(u16x2, x.w[0][i] & 0x7FFF7FFFu));
+  uint32_t top = max((uint32_t)tops.x, (uint32_t)tops.y);
+  top = max(top, pair(top));
+  float largest, unused, v[8];
+  unpack2<T>(top, largest, unused);
+  Half b;
+  b.scale = e4m3_of(__builtin_bit_cast(float, quotient_to_odd(largest, 6.f, 1.f / 6.f)));
+  const float s = e4m3_value(b.scale), inverse = s == 0.f ? 0.f : 1.f / s;
+  x.values(v);
+  if constexpr (T::kId == NVFP4_MOE_BF16) {
+    f16x2 q[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      // a saturated scale leaves quotients beyond f16's range
+      q[i].x = (_Float16)__builtin_amdgcn_fmed3f(v[2 * i] * inverse, -16.f, 16.f);
+      q[i].y = (_Float16)__builtin_amdgcn_fmed3f(v[2 * i + 1] * inverse, -16.f, 16.f);
+    }
+    b.codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(0u, q[0], 1.f, 0);
+    b.codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(b.codes, q[1], 1.f, 1);
+    b.codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(b.codes, q[2], 1.f, 2);
+    b.codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(b.codes, q[3], 1.f, 3);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float near = v[i] * inverse;
+      v[i] = fmaf(fmaf(-near, s, v[i]), inverse, near);
+    }
+    b.codes = e2m1_word(v);
+  }
+  if (b.scale == 0) b.codes = 0u;
+  if (top >= kInf16) b = {0u, kScaleNan};
+  return b;
+}
+
+// ---- where halves come from ----------------------------------------------------
+// kAsIs: 16-bit rows whose factor is 1.
+template <class T, bool kAsIs> struct RowSource {
   const void* x;
   int64_t row_stride, batch_stride;
   int64_t m;  // rows of a batch
   float scale;
   int vec;
 
-  __device__ inline Block block(int64_t row, int, int kb) const {
-    const int64_t at = (m > 0 ? row / m * batch_stride + row % m * row_stride : row * row_stride) + kb * 16;
-    Raw8<T> raw[2];
-    raw[0].load(x, at, vec);
-    raw[1].load(x, at + 8, vec);
-    float v[16];
-    raw[0].values(v);
-    raw[1].values(v + 8);
+  // Half kh of a row.
+  __device__ inline Half half(int64_t row, int, int kh) const {
+    Raw8<T> raw;
+    raw.load(x, (m > 0 ? row / m * batch_stride + row % m * row_stride : row * row_stride) + kh * 8, vec);
+    if constexpr (kAsIs) {
+      return encode_16bit<T>(raw);
+    } else {
+      float v[8];
+      raw.values(v);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] *= scale;
-    return encode(v);
+      for (int i = 0; i < 8; ++i) v[i] *= scale;
+      return encode(v);
+    }
   }
 };
 
@@ -114,19 +163,18 @@ constexpr float kUnsure = 1.f / 65536;
 
 __device__ inline double silu_f64(double g) { return g / (1.0 + exp(-g)); }
 
-__device__ inline Block encode_f64(const double (&v)[16]) {
+__device__ inline Half encode_f64(const double (&v)[8]) {
   double top = 0.0;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) top = fmax(top, fabs(v[i]));
-  Block b;
+  for (int i = 0; i < 8; ++i) top = fmax(top, fabs(v[i]));
+  top = fmax(top, pair(top));
+  Half b;
   b.scale = e4m3_of(to_odd(top / 6.0));
   const double s = e4m3_value(b.scale), inverse = s == 0.0 ? 0.0 : 1.0 / s;
-  float q[16];
+  float q[8];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) q[i] = copysignf(to_odd(fmin(fabs(v[i]) * inverse, 16.0)), (float)v[i]);
-  b.codes.x = e2m1_word(q);
-  b.codes.y = e2m1_word(q + 8);
-  if (b.scale == 0) b.codes = u32x2{0u, 0u};
+  for (int i = 0; i < 8; ++i) q[i] = copysignf(to_odd(fmin(fabs(v[i]) * inverse, 16.0)), (float)v[i]);
+  b.codes = b.scale == 0 ? 0u : e2m1_word(q);
   return b;
 }
 
@@ -137,55 +185,51 @@ template <class T> struct SwigluSource {
   int k, vec;
   float scale;
 
-  __device__ inline Block block(int64_t row, int expert, int kb) const {
-    const int64_t at = row * row_stride + kb * 16;
-    Raw8<T> raw[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) raw[i].load(c, at + i / 2 * k + i % 2 * 8, vec);
-    float g[16], u[16], v[16];
+  __device__ inline Half half(int64_t row, int expert, int kh) const {
+    const int64_t at = row * row_stride + kh * 8;
+    Raw8<T> raw[2];
+    raw[0].load(c, at, vec);
+    raw[1].load(c, at + k, vec);
+    float g[8], u[8], v[8];
     raw[0].values(g);
-    raw[1].values(g + 8);
-    raw[2].values(u);
-    raw[3].values(u + 8);
-    const float al = alpha == nullptr ? 1.f : alpha[expert];
+    raw[1].values(u);
+    const float al = alpha == nullptr ? 1.f : alpha[expert], al_scale = al * scale;
     uint32_t top = 0;
     float factor = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float ga = g[i] * al, ua = u[i] * al * scale;
+    for (int i = 0; i < 8; ++i) {
+      const float ga = g[i] * al, ua = u[i] * al_scale;
       const float sigmoid = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(ga * -1.44269502f));
       v[i] = ga * sigmoid * ua;
       factor = fmaxf(factor, fabsf(ua));
       top = max(top, __builtin_bit_cast(uint32_t, v[i]) & 0x7FFFFFFFu);
     }
-    Block b;
+    top = max(top, pair(top));
+    Half b;
     const float sixth = __builtin_bit_cast(float, top) * (1.f / 6.f);
     b.scale = e4m3_of(sixth * (1.f - kUnsure));
     // a sigmoid below 2^-126 is 0 here: g times it would count with a factor this large only
-    bool unsure = factor > 0x1p+90f || b.scale != e4m3_of(sixth * (1.f + kUnsure));
+    uint32_t unsure = factor > 0x1p+90f || b.scale != e4m3_of(sixth * (1.f + kUnsure));
     const float s = e4m3_value(b.scale), inverse = s == 0.f ? 0.f : __builtin_amdgcn_rcpf(s);
     const float low = inverse * (1.f - kUnsure), high = inverse * (1.f + kUnsure);
-    float q[16], r[16];
+    float q[8], r[8];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < 8; ++i) {
       q[i] = v[i] * low;
       r[i] = v[i] * high;
     }
-    b.codes.x = e2m1_word(q);
-    b.codes.y = e2m1_word(q + 8);
-    unsure |= b.codes.x != e2m1_word(r) || b.codes.y != e2m1_word(r + 8);
+    b.codes = e2m1_word(q);
+    unsure |= b.codes != e2m1_word(r);
+    unsure |= pair(unsure);
+    if (b.scale == 0) b.codes = 0u;
     if (top >= kInfBits) {
       // an infinity or NaN in an operand, or a product beyond fp32
-      b.scale = kScaleNan;
-      b.codes = u32x2{0u, 0u};
+      b = {0u, kScaleNan};
     } else if (unsure) {
-      double w[16];
+      double w[8];
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        w[i] = silu_f64((double)g[i] * al) * ((double)u[i] * al) * scale;
+      for (int i = 0; i < 8; ++i) w[i] = silu_f64((double)g[i] * al) * ((double)u[i] * al) * scale;
       b = encode_f64(w);
-    } else if (b.scale == 0) {
-      b.codes = u32x2{0u, 0u};
     }
     return b;
   }
@@ -240,41 +284,43 @@ struct Rows {
   }
 };
 
-__device__ inline uint32_t or_quad(uint32_t v) {
-  v |= __builtin_amdgcn_mov_dpp(v, 0xB1, 0xF, 0xF, false);
-  return v | __builtin_amdgcn_mov_dpp(v, 0x4E, 0xF, 0xF, false);
+// The scales of an atom's row, in the eight lanes that hold its halves: bytes in
+// the order of the blocks.
+__device__ inline uint32_t scale_word(uint32_t scale, int kh) {
+  uint32_t v = scale << (kh / 2 % 4 * 8);
+  v |= (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, false);         // from the pair beside
+  return v | (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, false);  // from the other four
 }
 
-// A row of blocks, padded to whole atoms: block kb of row `row`, from the index
-// of a thread.
+// A row of halves, padded to whole atoms: half kh of row `row`, from the index of
+// a thread.
 struct Place {
   int64_t row;
-  int kb;
+  int kh;
 };
 __device__ inline Place place_of(uint32_t index, uint32_t padded) {
   return {(int64_t)(index / padded), (int)(index % padded)};
 }
 
-// Few rows per expert: a thread per block; four lanes join their scales to the
-// word of an atom's row.
+// Few rows per expert: eight lanes join the scales of an atom's row to a word.
 template <class Source>
 __global__ void __launch_bounds__(kRowThreads)
-    nvfp4_quantize_rows_kernel(Source src, Rows rows, int blocks, uint8_t* a, uint8_t* sfa) {
-  const int padded = ceil_div(blocks, 4) * 4;
-  const Place p = place_of(blockIdx.x * kRowThreads + threadIdx.x, padded);
+    nvfp4_quantize_rows_kernel(Source src, Rows rows, int blocks, uint32_t* a, uint8_t* sfa) {
+  const int along = ceil_div(blocks, 4);
+  const Place p = place_of(blockIdx.x * kRowThreads + threadIdx.x, along * 8);
   const int64_t end = rows.offsets == nullptr ? rows.rows : rows.offsets[rows.experts];
-  if (p.row >= end) return;  // for four lanes at a time
+  if (p.row >= end) return;  // for eight lanes at a time
   int expert, r;
   int64_t atom;
   rows.find(p.row, expert, atom, r);
   uint32_t scale = 0;
-  if (p.kb < blocks) {
-    const Block b = src.block(p.row, expert, p.kb);
-    *(u32x2*)(a + (p.row * blocks + p.kb) * 8) = b.codes;
-    scale = b.scale << (p.kb % 4 * 8);
+  if (p.kh < 2 * blocks) {
+    const Half b = src.half(p.row, expert, p.kh);
+    a[p.row * 2 * blocks + p.kh] = b.codes;
+    scale = b.scale;
   }
-  scale = or_quad(scale);
-  if (p.kb % 4 == 0) *(uint32_t*)(sfa + (atom * (padded / 4) + p.kb / 4) * kAtomBytes + atom_row(r)) = scale;
+  scale = scale_word(scale, p.kh);
+  if (p.kh % 8 == 0) *(uint32_t*)(sfa + (atom * along + p.kh / 8) * kAtomBytes + atom_row(r)) = scale;
 }
 
 // Many rows: a workgroup per tile of 128 rows x 256 K-elements. Codes are
@@ -282,25 +328,26 @@ __global__ void __launch_bounds__(kRowThreads)
 // shared memory and stored as the 2 KB that they are.
 template <class Source>
 __global__ void __launch_bounds__(kTileThreads)
-    nvfp4_quantize_tiles_kernel(Source src, Rows rows, int blocks, uint8_t* a, uint8_t* sfa) {
+    nvfp4_quantize_tiles_kernel(Source src, Rows rows, int blocks, uint32_t* a, uint8_t* sfa) {
   __shared__ uint32_t s_sf[kTileAtoms * kAtomBytes / 4];
+  constexpr int kPassRows = kTileThreads / kTileHalves;
   const int along = ceil_div(blocks, 4), chunks = ceil_div(along, kTileAtoms);
   const int64_t atom = blockIdx.x / chunks;
   const int first_atom = blockIdx.x % chunks * kTileAtoms;
   int count, expert;
   const int64_t first = rows.first_row(atom, count, expert);
   if (count == 0) return;
-  const int kt = threadIdx.x % kTileBlocks, kb = first_atom * 4 + kt;
+  const int half = threadIdx.x % kTileHalves, kh = first_atom * 8 + half;
 #pragma unroll
-  for (int pass = 0; pass < kAtomRows / (kTileThreads / kTileBlocks); ++pass) {
-    const int r = pass * (kTileThreads / kTileBlocks) + threadIdx.x / kTileBlocks;
+  for (int pass = 0; pass < kAtomRows / kPassRows; ++pass) {
+    const int r = pass * kPassRows + threadIdx.x / kTileHalves;
     uint32_t scale = 0;
-    if (r < count && kb < blocks) {
-      const Block b = src.block(first + r, expert, kb);
-      *(u32x2*)(a + ((first + r) * blocks + kb) * 8) = b.codes;
+    if (r < count && kh < 2 * blocks) {
+      const Half b = src.half(first + r, expert, kh);
+      a[(first + r) * 2 * blocks + kh] = b.codes;
       scale = b.scale;
     }
-    ((uint8_t*)s_sf)[kt / 4 * kAtomBytes + atom_row(r) + kt % 4] = (uint8_t)scale;
+    if (half % 2 == 0) ((uint8_t*)s_sf)[half / 8 * kAtomBytes + atom_row(r) + half / 2 % 4] = (uint8_t)scale;
   }
   __syncthreads();
   const int words = min(kTileAtoms, along - first_atom) * (kAtomBytes / 4);
@@ -309,34 +356,40 @@ __global__ void __launch_bounds__(kTileThreads)
 }
 
 // Dispatch: a token's row is quantised once and its codes stored to the rows of
-// all its slots. kDirect: so are its scales, a word at a time; else they go to
+// all its slots, four slots at a time: each lane of four takes a slot and stores
+// the codes of all four. kDirect: so are the scales, a word at a time; else they go to
 // token_scales [tokens][atoms along k, padded to fours] and nvfp4_dispatch_scales_kernel lays them out.
 struct Slots {
   const int32_t *ids, *slot_rows, *offsets, *atoms;
   int topk, experts;
 };
-template <class T, bool kDirect>
+template <int kLane> __device__ inline uint32_t of_quad(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, kLane * 0x55, 0xF, 0xF, false);
+}
+template <class Source, bool kDirect>
 __global__ void __launch_bounds__(kRowThreads)
-    nvfp4_dispatch_kernel(RowSource<T> src, Slots slots, int64_t tokens, int blocks, uint8_t* a, uint8_t* sfa,
+    nvfp4_dispatch_kernel(Source src, Slots slots, int64_t tokens, int blocks, uint32_t* a, uint8_t* sfa,
                           uint32_t* token_scales) {
-  const int padded = ceil_div(blocks, 4) * 4;
-  const Place p = place_of(blockIdx.x * kRowThreads + threadIdx.x, padded);
-  if (p.row >= tokens) return;
-  Block b = {u32x2{0u, 0u}, 0u};
-  if (p.kb < blocks) b = src.block(p.row, 0, p.kb);
-  const uint32_t word = or_quad(b.scale << (p.kb % 4 * 8));
-  for (int j = 0; j < slots.topk; ++j) {
+  const int along = ceil_div(blocks, 4);
+  const Place p = place_of(blockIdx.x * kRowThreads + threadIdx.x, along * 8);
+  if (p.row >= tokens) return;  // for eight lanes at a time
+  const bool there = p.kh < 2 * blocks;  // for four: k is a multiple of 32
+  Half b = {0u, 0u};
+  if (there) b = src.half(p.row, 0, p.kh);
+  const uint32_t word = scale_word(b.scale, p.kh);
+  const u32x4 codes = {of_quad<0>(b.codes), of_quad<1>(b.codes), of_quad<2>(b.codes), of_quad<3>(b.codes)};
+  for (int j = p.kh % 4; j < slots.topk; j += 4) {
     const int64_t slot = p.row * slots.topk + j;
     const int row = slots.slot_rows[slot];
     if (row < 0) continue;
-    if (p.kb < blocks) *(u32x2*)(a + ((int64_t)row * blocks + p.kb) * 8) = b.codes;
-    if (kDirect && p.kb % 4 == 0) {
+    if (there) *(u32x4*)(a + (int64_t)row * 2 * blocks + p.kh / 4 * 4) = codes;
+    if (kDirect && p.kh % 8 < 4) {
       const int e = slots.ids[slot], at = row - slots.offsets[e];
       const int64_t atom = slots.atoms[e] + at / kAtomRows;
-      *(uint32_t*)(sfa + (atom * (padded / 4) + p.kb / 4) * kAtomBytes + atom_row(at % kAtomRows)) = word;
+      *(uint32_t*)(sfa + (atom * along + p.kh / 8) * kAtomBytes + atom_row(at % kAtomRows)) = word;
     }
   }
-  if (!kDirect && p.kb % 4 == 0) token_scales[p.row * (ceil_div(padded, 16) * 4) + p.kb / 4] = word;
+  if (!kDirect && p.kh % 8 == 0) token_scales[p.row * (ceil_div(along, 4) * 4) + p.kh / 8] = word;
 }
 
 // Scales of the rows sorted by expert, whole atoms at a time: thread = row of
@@ -388,16 +441,16 @@ template <class T>
 __global__ void __launch_bounds__(kRowThreads)
     nvfp4_dequantize_rows_kernel(const uint32_t* a, const uint8_t* sfa, Rows rows, int blocks, void* out,
                                  int64_t row_stride, int vec) {
-  const Place p = place_of(blockIdx.x * kRowThreads + threadIdx.x, 2 * blocks);  // halves of blocks
+  const Place p = place_of(blockIdx.x * kRowThreads + threadIdx.x, 2 * blocks);
   const int64_t end = rows.offsets == nullptr ? rows.rows : rows.offsets[rows.experts];
   if (p.row >= end) return;
   int expert, r;
   int64_t atom;
   rows.find(p.row, expert, atom, r);
-  const int kb = p.kb / 2;
+  const int kb = p.kh / 2;
   float v[8];
-  decode(a[p.row * 2 * blocks + p.kb], sfa[(atom * ceil_div(blocks, 4) + kb / 4) * kAtomBytes + atom_row(r) + kb % 4], v);
-  store8<T>(out, p.row * row_stride + p.kb * 8, vec, v);
+  decode(a[p.row * 2 * blocks + p.kh], sfa[(atom * ceil_div(blocks, 4) + kb / 4) * kAtomBytes + atom_row(r) + kb % 4], v);
+  store8<T>(out, p.row * row_stride + p.kh * 8, vec, v);
 }
 
 template <class T>
@@ -405,18 +458,18 @@ __global__ void __launch_bounds__(kTileThreads)
     nvfp4_dequantize_tiles_kernel(const uint32_t* a, const uint8_t* sfa, Rows rows, int blocks, void* out,
                                   int64_t row_stride, int vec) {
   __shared__ uint32_t s_sf[kTileAtoms * kAtomBytes / 4];
-  constexpr int kHalves = 2 * kTileBlocks, kPassRows = kTileThreads / kHalves;
+  constexpr int kPassRows = kTileThreads / kTileHalves;
   const int along = ceil_div(blocks, 4), chunks = ceil_div(along, kTileAtoms);
   const int64_t atom = blockIdx.x / chunks;
   const int first_atom = blockIdx.x % chunks * kTileAtoms;
   int count, expert;
   const int64_t first = rows.first_row(atom, count, expert);
   if (count == 0) return;
-  const int half = threadIdx.x % kHalves, kh = first_atom * 8 + half;
+  const int half = threadIdx.x % kTileHalves, kh = first_atom * 8 + half;
   uint32_t codes[kAtomRows / kPassRows];
 #pragma unroll
   for (int pass = 0; pass < kAtomRows / kPassRows; ++pass) {
-    const int r = pass * kPassRows + threadIdx.x / kHalves;
+    const int r = pass * kPassRows + threadIdx.x / kTileHalves;
     codes[pass] = r < count && kh < 2 * blocks ? __builtin_nontemporal_load(a + (first + r) * 2 * blocks + kh) : 0u;
   }
   const int words = min(kTileAtoms, along - first_atom) * (kAtomBytes / 4);
@@ -426,7 +479,7 @@ __global__ void __launch_bounds__(kTileThreads)
   if (kh >= 2 * blocks) return;
 #pragma unroll
   for (int pass = 0; pass < kAtomRows / kPassRows; ++pass) {
-    const int r = pass * kPassRows + threadIdx.x / kHalves;
+    const int r = pass * kPassRows + threadIdx.x / kTileHalves;
     if (r >= count) break;
     float v[8];
     decode(codes[pass], ((const uint8_t*)s_sf)[half / 8 * kAtomBytes + atom_row(r) + half / 2 % 4], v);
@@ -442,6 +495,17 @@ int64_t atom_rows(const Rows& r, int64_t batches) {
   return (r.rows - used) / kAtomRows + used;
 }
 
+// f(source) with the source of rows for their type and factor.
+template <class Fn>
+int with_rows(int dtype, const void* x, int64_t row_stride, int64_t batch_stride, int64_t m, float scale, bool vec, Fn f) {
+  if (dtype == NVFP4_MOE_F32) return f(RowSource<F32, false>{x, row_stride, batch_stride, m, scale, vec});
+  if (dtype == NVFP4_MOE_F16)
+    return scale == 1.f ? f(RowSource<F16, true>{x, row_stride, batch_stride, m, scale, vec})
+                        : f(RowSource<F16, false>{x, row_stride, batch_stride, m, scale, vec});
+  return scale == 1.f ? f(RowSource<BF16, true>{x, row_stride, batch_stride, m, scale, vec})
+                      : f(RowSource<BF16, false>{x, row_stride, batch_stride, m, scale, vec});
+}
+
 // Tiles pay from 16 rows of an atom on (of 128: below, most threads of a tile have no row).
 bool tiles_pay(const Rows& r) { return r.offsets == nullptr ? r.m >= 16 : r.rows >= (int64_t)16 * r.experts; }
 
@@ -450,11 +514,11 @@ int launch_quantize(const Source& src, const Rows& rows, int64_t batches, int bl
   if (tiles_pay(rows)) {
     const int64_t grid = atom_rows(rows, batches) * ceil_div(ceil_div(blocks, 4), kTileAtoms);
     if (grid > kMaxGrid) return NVFP4_ERR_INVALID;
-    nvfp4_quantize_tiles_kernel<<<(unsigned)grid, kTileThreads, 0, st>>>(src, rows, blocks, (uint8_t*)a, (uint8_t*)sfa);
+    nvfp4_quantize_tiles_kernel<<<(unsigned)grid, kTileThreads, 0, st>>>(src, rows, blocks, (uint32_t*)a, (uint8_t*)sfa);
   } else {
-    const int64_t grid = ceil_div64(rows.rows * (ceil_div(blocks, 4) * 4), kRowThreads);
+    const int64_t grid = ceil_div64(rows.rows * (ceil_div(blocks, 4) * 8), kRowThreads);
     if (grid > kMaxGrid) return NVFP4_ERR_INVALID;
-    nvfp4_quantize_rows_kernel<<<(unsigned)grid, kRowThreads, 0, st>>>(src, rows, blocks, (uint8_t*)a, (uint8_t*)sfa);
+    nvfp4_quantize_rows_kernel<<<(unsigned)grid, kRowThreads, 0, st>>>(src, rows, blocks, (uint32_t*)a, (uint8_t*)sfa);
   }
   return launched();
 }
@@ -497,8 +561,7 @@ int nvfp4_moe_quantize(const void* x, int dtype, int l, int64_t m, int k, int64_
   if (m == 0 || k == 0) return NVFP4_OK;
   const bool vec = wide_rows(x, dtype, row_stride) && (l == 1 || batch_stride * element_bytes(dtype) % 16 == 0);
   const Rows rows = {nullptr, nullptr, 1, l * m, m};
-  return with_type(dtype, [&](auto t) {
-    const RowSource<decltype(t)> src = {x, row_stride, batch_stride, l > 1 ? m : 0, scale, vec};
+  return with_rows(dtype, x, row_stride, batch_stride, l > 1 ? m : 0, scale, vec, [&](auto src) {
     return launch_quantize(src, rows, l, k / 16, a, sfa, (hipStream_t)stream);
   });
 }
@@ -524,21 +587,20 @@ int nvfp4_moe_dispatch(const void* x, int dtype, int64_t tokens, int topk, int k
   if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return NVFP4_ERR_WORKSPACE;
   if (need > 0 && !aligned(workspace, 256)) return NVFP4_ERR_MISALIGNED;
   const int blocks = k / 16, along = ceil_div(blocks, 4);
-  const int64_t grid = ceil_div64(tokens * along * 4, kRowThreads);
+  const int64_t grid = ceil_div64(tokens * along * 8, kRowThreads);
   const Rows rows = {offsets, atoms, experts, tokens * topk, 0};
   const int64_t scale_grid = atom_rows(rows, 1) * ceil_div(along, kScaleAtoms);
   if (grid > kMaxGrid || scale_grid > kMaxGrid) return NVFP4_ERR_INVALID;
   const Slots slots = {ids, slot_rows, offsets, atoms, topk, experts};
   const hipStream_t st = (hipStream_t)stream;
-  int rc = with_type(dtype, [&](auto t) {
-    using T = decltype(t);
-    const RowSource<T> src = {x, row_stride, 0, 0, scale, wide_rows(x, dtype, row_stride)};
+  int rc = with_rows(dtype, x, row_stride, 0, 0, scale, wide_rows(x, dtype, row_stride), [&](auto src) {
+    using Source = decltype(src);
     if (need == 0)
-      nvfp4_dispatch_kernel<T, true><<<(unsigned)grid, kRowThreads, 0, st>>>(src, slots, tokens, blocks, (uint8_t*)a,
-                                                                            (uint8_t*)sfa, nullptr);
+      nvfp4_dispatch_kernel<Source, true><<<(unsigned)grid, kRowThreads, 0, st>>>(src, slots, tokens, blocks, (uint32_t*)a,
+                                                                                 (uint8_t*)sfa, nullptr);
     else
-      nvfp4_dispatch_kernel<T, false><<<(unsigned)grid, kRowThreads, 0, st>>>(src, slots, tokens, blocks, (uint8_t*)a,
-                                                                             (uint8_t*)sfa, (uint32_t*)workspace);
+      nvfp4_dispatch_kernel<Source, false><<<(unsigned)grid, kRowThreads, 0, st>>>(src, slots, tokens, blocks, (uint32_t*)a,
+                                                                                  (uint8_t*)sfa, (uint32_t*)workspace);
     return launched();
   });
   if (rc != NVFP4_OK || need == 0) return rc;
