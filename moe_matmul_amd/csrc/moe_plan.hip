@@ -8,15 +8,20 @@ namespace {
 constexpr int kThreads = 1024;
 constexpr int kWaves = kThreads / 64;
 constexpr int kBins = NVFP4_MOE_MAX_EXPERTS;
-constexpr int kOneBlockSlots = 16384;  // up to here one workgroup does it all
-constexpr int kMaxBlocks = 256;
+// A workgroup places at least kOneBlockSlots slots. Up to kOnePassSlots each of
+// them counts all slots itself (2800 slots: 5 us, of which a launch is 4); beyond,
+// a launch of its own for the counts is faster (65536 slots of 256 experts: 11 us
+// with, 18 without). More than kMaxBlocks cost more in counts to add up than they save.
+constexpr int kOneBlockSlots = 1024;
+constexpr int kOnePassSlots = 8192;
+constexpr int kMaxBlocks = 128;
 
 struct PlanArgs {
   const int32_t* ids;
   int slots, experts, id_bits;  // id_bits: bits that tell the bins 0 .. experts apart
   int block_slots, blocks;
   int32_t *offsets, *atoms, *slot_rows, *row_slots;
-  int32_t* counts;  // [blocks][experts], of every block's slots
+  int32_t* counts;  // [blocks][experts], of every block's slots; null where every block counts all slots
   int num_products;
   nvfp4_moe_product products[NVFP4_MOE_MAX_PRODUCTS];
 };
@@ -25,7 +30,7 @@ __device__ inline int bin_of(int id, int experts) { return (unsigned)id < (unsig
 
 // Slots of this block per expert, and of each wave's part of them in s_wave.
 __device__ inline void count_block(const PlanArgs& a, int from, int to, int (*s_wave)[kBins]) {
-  for (int i = threadIdx.x; i < kWaves * kBins; i += kThreads) (&s_wave[0][0])[i] = 0;
+  for (int i = threadIdx.x; i < kWaves * a.experts; i += kThreads) s_wave[i / a.experts][i % a.experts] = 0;
   __syncthreads();
   const int wave = threadIdx.x / 64, part = ceil_div(ceil_div(to - from, kWaves), 64) * 64;
   const int begin = from + wave * part, end = min(to, begin + part);
@@ -48,16 +53,32 @@ __global__ void __launch_bounds__(kThreads) nvfp4_moe_count_kernel(PlanArgs a) {
   }
 }
 
-// Sums over the bins before, in shared memory; both arrays at once.
-__device__ inline void scan_bins(int* x, int* y) {
-  for (int d = 1; d < kBins; d *= 2) {
-    int u = 0, v = 0;
-    const int i = threadIdx.x;
-    if (i < kBins && i >= d) { u = x[i - d]; v = y[i - d]; }
-    __syncthreads();
-    if (i < kBins) { x[i] += u; y[i] += v; }
-    __syncthreads();
+// Slots from .. to - 1 per expert.
+__device__ inline void count_slots(const PlanArgs& a, int from, int to, int* bins) {
+#pragma unroll 8
+  for (int i = from + (int)threadIdx.x; i < to; i += kThreads) {
+    const int e = bin_of(a.ids[i], a.experts);
+    if (e >= 0) atomicAdd(&bins[e], 1);
   }
+}
+
+// Sums up to and with each bin, by one wave.
+__device__ inline void scan_bins(int* x, int lane) {
+  constexpr int kPart = kBins / 64;
+  int v[kPart], sum = 0;
+#pragma unroll
+  for (int i = 0; i < kPart; ++i) {
+    sum += x[lane * kPart + i];
+    v[i] = sum;
+  }
+  int before = sum;  // of the lanes up to this one
+  for (int d = 1; d < 64; d *= 2) {
+    const int u = __shfl_up(before, d);
+    before += lane >= d ? u : 0;
+  }
+  before -= sum;
+#pragma unroll
+  for (int i = 0; i < kPart; ++i) x[lane * kPart + i] = before + v[i];
 }
 
 // Second pass: the place of every slot. A wave walks its slots in order, 64 at
@@ -67,13 +88,24 @@ __global__ void __launch_bounds__(kThreads) nvfp4_moe_place_kernel(PlanArgs a) {
   __shared__ int s_wave[kWaves][kBins];
   __shared__ int s_rows[kBins], s_atoms[kBins];  // after the scan: sums up to and with the bin
   const int from = blockIdx.x * a.block_slots, to = min(a.slots, from + a.block_slots);
+  const bool all = a.blocks > 1 && a.counts == nullptr;
+  if (all && threadIdx.x < kBins) s_rows[threadIdx.x] = s_atoms[threadIdx.x] = 0;
   count_block(a, from, to, s_wave);
+  if (all) {
+    count_slots(a, 0, from, s_rows);            // slots before this block
+    count_slots(a, to, a.slots, s_atoms);       // and after it
+    __syncthreads();
+  }
   const int e = threadIdx.x;
   int total = 0, before = 0;  // slots of expert e in all blocks, in the blocks before
   if (e < a.experts) {
-    if (a.blocks == 1) {
+    if (a.counts == nullptr) {
+      before = all ? s_rows[e] : 0;
+      total = before + (all ? s_atoms[e] : 0);
+#pragma unroll
       for (int w = 0; w < kWaves; ++w) total += s_wave[w][e];
     } else {
+#pragma unroll 8
       for (int b = 0; b < a.blocks; ++b) {
         const int n = a.counts[(int64_t)b * a.experts + e];
         total += n;
@@ -86,7 +118,8 @@ __global__ void __launch_bounds__(kThreads) nvfp4_moe_place_kernel(PlanArgs a) {
     s_atoms[e] = ceil_div(total, kAtomRows);
   }
   __syncthreads();
-  scan_bins(s_rows, s_atoms);
+  if (threadIdx.x < 128) scan_bins(threadIdx.x < 64 ? s_rows : s_atoms, threadIdx.x & 63);
+  __syncthreads();
   const int rows = s_rows[kBins - 1];
   if (e < a.experts) {
     const int row = s_rows[e] - total, atom = s_atoms[e] - ceil_div(total, kAtomRows);
@@ -174,9 +207,8 @@ __global__ void nvfp4_moe_empty_plan_kernel(PlanArgs a) {
 
 // Slots of a block: at most kMaxBlocks blocks, whole waves' rounds.
 int block_slots(int64_t slots) {
-  if (slots <= kOneBlockSlots) return kOneBlockSlots;
   const int64_t even = ceil_div64(slots, kMaxBlocks);
-  return (int)(ceil_div64(even < 4096 ? 4096 : even, kThreads) * kThreads);
+  return (int)(ceil_div64(even < kOneBlockSlots ? kOneBlockSlots : even, kThreads) * kThreads);
 }
 
 bool plan_sizes(int64_t tokens, int topk, int experts) {
@@ -192,7 +224,7 @@ using namespace moe;
 extern "C" {
 
 size_t nvfp4_moe_plan_workspace_bytes(int64_t tokens, int topk, int experts) {
-  if (!plan_sizes(tokens, topk, experts) || tokens * topk <= kOneBlockSlots) return 0;
+  if (!plan_sizes(tokens, topk, experts) || tokens * topk <= kOnePassSlots) return 0;
   return (size_t)ceil_div64(tokens * topk, block_slots(tokens * topk)) * experts * sizeof(int32_t);
 }
 
@@ -233,14 +265,14 @@ int nvfp4_moe_plan(const int32_t* ids, int64_t tokens, int topk, int experts, in
   a.atoms = atoms;
   a.slot_rows = slot_rows;
   a.row_slots = row_slots;
-  a.counts = (int32_t*)workspace;
+  a.counts = need > 0 ? (int32_t*)workspace : nullptr;
   a.num_products = num_products;
   const hipStream_t st = (hipStream_t)stream;
   if (a.slots == 0) {
     nvfp4_moe_empty_plan_kernel<<<1, 256, 0, st>>>(a);
     return launched();
   }
-  if (a.blocks > 1) {
+  if (a.counts != nullptr) {
     nvfp4_moe_count_kernel<<<a.blocks, kThreads, 0, st>>>(a);
     if (int rc = launched()) return rc;
   }

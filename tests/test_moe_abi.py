@@ -82,12 +82,12 @@ def test_plan_refuses_and_sizes_its_workspace():
         v = dict(n=16, k=64, a=P, b=P, c=P, sfa=P, sfb=P, sizes=P, abc=P, sf=P) | bad
         entry = (c.nvfp4_moe_product * 1)(c.nvfp4_moe_product(*[v[n] for n, _ in c.nvfp4_moe_product._fields_]))
         refused(code, call, 4, 2, 8, P, P, entry, 1)
-    assert c.nvfp4_moe_plan_workspace_bytes(8192, 2, 8) == 0
-    need = c.nvfp4_moe_plan_workspace_bytes(8193, 2, 8)
+    assert c.nvfp4_moe_plan_workspace_bytes(4096, 2, 8) == 0
+    need = c.nvfp4_moe_plan_workspace_bytes(4097, 2, 8)
     assert need > 0
-    refused(WORKSPACE, call, 8193, 2)
-    refused(WORKSPACE, call, 8193, 2, 8, P, P, None, 0, 0x20000, need - 1)
-    refused(MISALIGNED, call, 8193, 2, 8, P, P, None, 0, 0x20010, need)
+    refused(WORKSPACE, call, 4097, 2)
+    refused(WORKSPACE, call, 4097, 2, 8, P, P, None, 0, 0x20000, need - 1)
+    refused(MISALIGNED, call, 4097, 2, 8, P, P, None, 0, 0x20010, need)
 
 
 def test_scale_bytes_hold_every_spread():

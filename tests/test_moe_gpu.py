@@ -213,7 +213,7 @@ def test_route_backward_against_differences():
 
 # ---- the plan --------------------------------------------------------------------------
 
-@pytest.mark.parametrize("tokens,topk,experts", [(1, 1, 1), (1, 8, 256), (63, 1, 7), (65, 3, 512), (2048, 8, 64), (8192, 2, 300),
+@pytest.mark.parametrize("tokens,topk,experts", [(1, 1, 1), (1, 8, 256), (63, 1, 7), (65, 3, 512), (1300, 3, 17), (4096, 2, 12), (2048, 8, 64), (8192, 2, 300),
                                                  (16385, 1, 5), (5000, 8, 256), (40000, 4, 33)])
 def test_plan(tokens, topk, experts):
     rng = rng_of(tokens, topk, experts)
