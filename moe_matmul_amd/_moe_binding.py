@@ -8,6 +8,7 @@ device addresses as integers (0: NULL). The library must have been built
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 from ._binding import NVFP4_ERR_HIP, NVFP4_OK, Nvfp4Error, nvfp4_error_string
@@ -104,14 +105,17 @@ nvfp4_moe_combine_backward = _checked("nvfp4_moe_combine_backward")
 nvfp4_moe_few_tokens = _checked("nvfp4_moe_few_tokens")
 
 
+@functools.lru_cache(maxsize=4096)
 def nvfp4_moe_plan_workspace_bytes(tokens: int, topk: int, experts: int) -> int:
     return load_moe_library().nvfp4_moe_plan_workspace_bytes(tokens, topk, experts)
 
 
+@functools.lru_cache(maxsize=4096)
 def nvfp4_moe_dispatch_workspace_bytes(tokens: int, topk: int, k: int, experts: int) -> int:
     return load_moe_library().nvfp4_moe_dispatch_workspace_bytes(tokens, topk, k, experts)
 
 
+@functools.lru_cache(maxsize=4096)
 def nvfp4_moe_sf_bytes(rows: int, experts: int, k: int) -> int:
     return load_moe_library().nvfp4_moe_sf_bytes(rows, experts, k)
 

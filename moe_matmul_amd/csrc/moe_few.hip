@@ -18,6 +18,9 @@ constexpr int kStageElements = 16384;  // of x in shared memory, at most (32 KB)
 constexpr int kEnoughWaves = 768;
 constexpr int kPad = 8;       // elements after a staged row: rows start in different banks
 
+// a stage of shared memory holds kDepth steps of every row of a pass, at least
+static_assert(kMaxRows * kDepth * kStep <= kStageElements, "a stage would hold no whole round of steps");
+
 struct FewArgs {
   const void* x;
   int64_t x_stride;
