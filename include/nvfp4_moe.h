@@ -165,7 +165,7 @@ int nvfp4_moe_dispatch(const void* x, int dtype, int64_t tokens, int topk, int k
                        const int32_t* ids, const int32_t* slot_rows, const int32_t* row_slots,
                        const int32_t* offsets, const int32_t* atoms, int experts, void* a, void* sfa,
                        void* workspace, size_t workspace_bytes, void* stream);
-size_t nvfp4_moe_dispatch_workspace_bytes(int64_t tokens, int topk, int k, int experts);
+size_t nvfp4_moe_dispatch_workspace_bytes(int64_t tokens, int topk, int k);
 
 /*
  * nvfp4_moe_swiglu - as nvfp4_moe_quantize for v = silu(g * alpha) * (u * alpha)

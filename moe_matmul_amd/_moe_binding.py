@@ -53,7 +53,7 @@ _SIGNATURES = {
     "nvfp4_moe_quantize": (_int, [_ptr, _int, _int, _i64, _int, _i64, _i64, _float, _ptr, _ptr, _ptr]),
     "nvfp4_moe_dispatch": (_int, [_ptr, _int, _i64, _int, _int, _i64, _float, _ptr, _ptr, _ptr, _ptr, _ptr, _int,
                                   _ptr, _ptr, _ptr, _size, _ptr]),
-    "nvfp4_moe_dispatch_workspace_bytes": (_size, [_i64, _int, _int, _int]),
+    "nvfp4_moe_dispatch_workspace_bytes": (_size, [_i64, _int, _int]),
     "nvfp4_moe_swiglu": (_int, [_ptr, _int, _i64, _int, _i64, _ptr, _float, _ptr, _ptr, _int, _ptr, _ptr, _ptr]),
     "nvfp4_moe_dequantize": (_int, [_ptr, _ptr, _int, _i64, _int, _ptr, _ptr, _int, _ptr, _int, _i64, _ptr]),
     "nvfp4_moe_combine": (_int, [_ptr, _int, _i64, _i64, _int, _int, _ptr, _ptr, _ptr, _ptr, _ptr, _ptr, _int, _i64,
@@ -111,8 +111,8 @@ def nvfp4_moe_plan_workspace_bytes(tokens: int, topk: int, experts: int) -> int:
 
 
 @functools.lru_cache(maxsize=4096)
-def nvfp4_moe_dispatch_workspace_bytes(tokens: int, topk: int, k: int, experts: int) -> int:
-    return load_moe_library().nvfp4_moe_dispatch_workspace_bytes(tokens, topk, k, experts)
+def nvfp4_moe_dispatch_workspace_bytes(tokens: int, topk: int, k: int) -> int:
+    return load_moe_library().nvfp4_moe_dispatch_workspace_bytes(tokens, topk, k)
 
 
 @functools.lru_cache(maxsize=4096)

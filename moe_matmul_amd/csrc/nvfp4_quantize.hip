@@ -157,17 +157,23 @@ template <class T, bool kAsIs> struct RowSource {
 // products, 1 + e^-g, its reciprocal and e^-g itself (|g| 2^-24 through its
 // argument, |g| < 100 where it counts) stay within kUnsure of the exact value.
 // Where a code or the scale would be another one within that bound, the block
-// is done again in fp64. So the results are those of the exact activation, and
-// do not depend on how exp is computed.
+// is done again in fp64; so are blocks whose factors leave the range where the
+// bound holds, and those that come out infinite or NaN. So the results are those
+// of the exact activation, and do not depend on how exp is computed.
 constexpr float kUnsure = 1.f / 65536;
 
 __device__ inline double silu_f64(double g) { return g / (1.0 + exp(-g)); }
 
 __device__ inline Half encode_f64(const double (&v)[8]) {
   double top = 0.0;
+  uint32_t bad = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = fmax(top, fabs(v[i]));
+  for (int i = 0; i < 8; ++i) {
+    top = fmax(top, fabs(v[i]));
+    bad |= !(fabsf((float)v[i]) < INFINITY);  // beyond fp32, or NaN
+  }
   top = fmax(top, pair(top));
+  if (bad | pair(bad)) return {0u, kScaleNan};
   Half b;
   b.scale = e4m3_of(to_odd(top / 6.0));
   const double s = e4m3_value(b.scale), inverse = s == 0.0 ? 0.0 : 1.0 / s;
@@ -194,6 +200,8 @@ template <class T> struct SwigluSource {
     raw[0].values(g);
     raw[1].values(u);
     const float al = alpha == nullptr ? 1.f : alpha[expert], al_scale = al * scale;
+    // (an infinite one makes `factor` infinite, or `top` NaN)
+    const bool in_range = fabsf(al_scale) >= 0x1p-126f || al == 0.f || scale == 0.f;
     uint32_t top = 0;
     float factor = 0.f;
 #pragma unroll
@@ -201,15 +209,17 @@ template <class T> struct SwigluSource {
       const float ga = g[i] * al, ua = u[i] * al_scale;
       const float sigmoid = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(ga * -1.44269502f));
       v[i] = ga * sigmoid * ua;
-      factor = fmaxf(factor, fabsf(ua));
+      factor = fmaxf(fmaxf(factor, fabsf(ua)), fabsf(ga));
       top = max(top, __builtin_bit_cast(uint32_t, v[i]) & 0x7FFFFFFFu);
     }
     top = max(top, pair(top));
     Half b;
     const float sixth = __builtin_bit_cast(float, top) * (1.f / 6.f);
     b.scale = e4m3_of(sixth * (1.f - kUnsure));
-    // a sigmoid below 2^-126 is 0 here: g times it would count with a factor this large only
-    uint32_t unsure = factor > 0x1p+90f || b.scale != e4m3_of(sixth * (1.f + kUnsure));
+    // a factor or a sigmoid below 2^-126 has lost bits or is 0: it would count beside one this large only, but
+    // alpha times scale counts beside any u
+    uint32_t unsure = top >= kInfBits || factor > 0x1p+90f || !in_range ||
+                      b.scale != e4m3_of(sixth * (1.f + kUnsure));
     const float s = e4m3_value(b.scale), inverse = s == 0.f ? 0.f : __builtin_amdgcn_rcpf(s);
     const float low = inverse * (1.f - kUnsure), high = inverse * (1.f + kUnsure);
     float q[8], r[8];
@@ -222,10 +232,7 @@ template <class T> struct SwigluSource {
     unsure |= b.codes != e2m1_word(r);
     unsure |= pair(unsure);
     if (b.scale == 0) b.codes = 0u;
-    if (top >= kInfBits) {
-      // an infinity or NaN in an operand, or a product beyond fp32
-      b = {0u, kScaleNan};
-    } else if (unsure) {
+    if (unsure) {
       double w[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) w[i] = silu_f64((double)g[i] * al) * ((double)u[i] * al) * scale;
@@ -302,7 +309,7 @@ __device__ inline Place place_of(uint32_t index, uint32_t padded) {
   return {(int64_t)(index / padded), (int)(index % padded)};
 }
 
-// Few rows per expert: eight lanes join the scales of an atom's row to a word.
+// Few rows: eight lanes join the scales of an atom's row to a word.
 template <class Source>
 __global__ void __launch_bounds__(kRowThreads)
     nvfp4_quantize_rows_kernel(Source src, Rows rows, int blocks, uint32_t* a, uint8_t* sfa) {
@@ -506,12 +513,22 @@ int with_rows(int dtype, const void* x, int64_t row_stride, int64_t batch_stride
                       : f(RowSource<BF16, false>{x, row_stride, batch_stride, m, scale, vec});
 }
 
-// Tiles pay from 16 rows of an atom on (of 128: below, most threads of a tile have no row).
-bool tiles_pay(const Rows& r) { return r.offsets == nullptr ? r.m >= 16 : r.rows >= (int64_t)16 * r.experts; }
+// Whether tiles beat rows: where an expert's (or a batch's) atoms are filled by a
+// quarter, and there are enough elements for the tiles of 128 x 256 to fill the
+// chip. Measured, rows - tiles: swiglu of 256 experts of 16 rows, k 2048, 18.0 -
+// 19.8 us, of 32 rows 32.7 - 26.8, of 64 rows 57 - 41; quantisation of 64 batches
+// of 16 rows of 7168 9.1 - 10.7, of 32 rows 14.7 - 14.0; one batch of 512 x 7168
+// 4.7 - 6.6, of 1024 6.9 - 7.0, of 2048 12.7 - 10.9. Rows of a batch need no
+// search for their expert on their way back: 4 x 2048 x 7168 26.7 - 27.6,
+// 16 x 1024 x 7168 71 - 49, while 256 experts of 64 rows of 2048 are 33 - 23.
+bool tiles_pay(const Rows& r, int blocks, bool back) {
+  const int64_t elements = r.rows * blocks * 16, per = r.offsets == nullptr ? r.m : r.rows / r.experts;
+  return per >= 32 && elements >= (int64_t)1 << (back && r.offsets == nullptr ? 26 : 23);
+}
 
 template <class Source>
 int launch_quantize(const Source& src, const Rows& rows, int64_t batches, int blocks, void* a, void* sfa, hipStream_t st) {
-  if (tiles_pay(rows)) {
+  if (tiles_pay(rows, blocks, false)) {
     const int64_t grid = atom_rows(rows, batches) * ceil_div(ceil_div(blocks, 4), kTileAtoms);
     if (grid > kMaxGrid) return NVFP4_ERR_INVALID;
     nvfp4_quantize_tiles_kernel<<<(unsigned)grid, kTileThreads, 0, st>>>(src, rows, blocks, (uint32_t*)a, (uint8_t*)sfa);
@@ -541,9 +558,13 @@ int check_sorted(const int32_t* offsets, const int32_t* atoms, int experts) {
   return aligned(offsets, 4) && aligned(atoms, 4) ? NVFP4_OK : NVFP4_ERR_MISALIGNED;
 }
 
-// Scales go straight to their atoms where an expert has few rows: its atoms'
-// lines would not fill up in any order, and one launch is saved.
-bool direct_scales(int64_t tokens, int topk, int experts) { return tokens * topk < (int64_t)16 * experts; }
+// Scales go straight to their atoms while all of them (2 MB here) stay in an
+// XCD's L2 until their lines are full; beyond, they are laid out in whole lines by
+// a second launch. Measured at 8 slots a token, 7168 elements, 8 experts, one
+// launch - two: 2048 slots 7.0 - 9.2 us, 4096 9.7 - 11.3, 8192 19.8 - 18.2, 16384
+// 35 - 26; the number of experts makes no difference (64 of 4096 elements: 8192
+// slots 10.5 - 12.8, 16384 21.7 - 20.3).
+bool direct_scales(int64_t slots, int k) { return slots * k <= (int64_t)1 << 25; }
 
 }  // namespace
 }  // namespace moe
@@ -566,8 +587,8 @@ int nvfp4_moe_quantize(const void* x, int dtype, int l, int64_t m, int k, int64_
   });
 }
 
-size_t nvfp4_moe_dispatch_workspace_bytes(int64_t tokens, int topk, int k, int experts) {
-  if (tokens <= 0 || topk < 1 || k <= 0 || direct_scales(tokens, topk, experts)) return 0;
+size_t nvfp4_moe_dispatch_workspace_bytes(int64_t tokens, int topk, int k) {
+  if (tokens <= 0 || topk < 1 || k <= 0 || direct_scales(tokens * topk, k)) return 0;
   return (size_t)tokens * ceil_div(k, 4 * kAtomK) * 16;
 }
 
@@ -583,7 +604,7 @@ int nvfp4_moe_dispatch(const void* x, int dtype, int64_t tokens, int topk, int k
   if (tokens > 0 && (ids == nullptr || slot_rows == nullptr || row_slots == nullptr)) return NVFP4_ERR_INVALID;
   if (!aligned(ids, 4) || !aligned(slot_rows, 4) || !aligned(row_slots, 4)) return NVFP4_ERR_MISALIGNED;
   if (tokens == 0 || k == 0) return NVFP4_OK;
-  const size_t need = nvfp4_moe_dispatch_workspace_bytes(tokens, topk, k, experts);
+  const size_t need = nvfp4_moe_dispatch_workspace_bytes(tokens, topk, k);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return NVFP4_ERR_WORKSPACE;
   if (need > 0 && !aligned(workspace, 256)) return NVFP4_ERR_MISALIGNED;
   const int blocks = k / 16, along = ceil_div(blocks, 4);
@@ -633,7 +654,7 @@ int nvfp4_moe_dequantize(const void* a, const void* sfa, int l, int64_t m, int k
   if (m == 0 || k == 0) return NVFP4_OK;
   const Rows rows = {offsets, atoms, experts, l * m, m};
   const int blocks = k / 16;
-  const bool tiles = tiles_pay(rows);
+  const bool tiles = tiles_pay(rows, blocks, true);
   const int64_t grid = tiles ? atom_rows(rows, l) * ceil_div(ceil_div(blocks, 4), kTileAtoms)
                              : ceil_div64(rows.rows * 2 * blocks, kRowThreads);
   if (grid > kMaxGrid) return NVFP4_ERR_INVALID;

@@ -237,7 +237,7 @@ def quantize(x, *, plan=None, scale=1.0, a=None, sfa=None, stream=None):
             raise ValueError(f"x must have the plan's {plan.tokens} tokens, on its device")
         a = _out(a, "a", (plan.rows, k // 2), torch.uint8, device)
         sfa = _out(sfa, "sfa", (c.nvfp4_moe_sf_bytes(plan.rows, plan.experts, k),), torch.uint8, device)
-        need = c.nvfp4_moe_dispatch_workspace_bytes(plan.tokens, plan.topk, k, plan.experts)
+        need = c.nvfp4_moe_dispatch_workspace_bytes(plan.tokens, plan.topk, k)
         workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
         offsets, atoms, slot_rows, row_slots = plan.addresses
         _enqueue(c.nvfp4_moe_dispatch, device, stream, x.data_ptr(), kind, plan.tokens, plan.topk, k, stride, scale,

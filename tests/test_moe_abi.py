@@ -124,10 +124,12 @@ def test_quantisation_refuses():
         refused(INVALID, d, P, 0, tokens, topk, k, 64, 1.0, P, P, P, P, P, experts, P, P, 0, 0, 0)
     refused(INVALID, d, P, 0, 4, 2, 64, 64, 1.0, 0, P, P, P, P, 8, P, P, 0, 0, 0)
     refused(INVALID, d, P, 0, 4, 2, 64, 64, 1.0, P, P, P, 0, P, 8, P, P, 0, 0, 0)
-    need = c.nvfp4_moe_dispatch_workspace_bytes(512, 2, 64, 8)
-    assert need > 0 and c.nvfp4_moe_dispatch_workspace_bytes(4, 2, 64, 8) == 0
-    refused(WORKSPACE, d, P, 0, 512, 2, 64, 64, 1.0, P, P, P, P, P, 8, P, P, 0, 0, 0)
-    refused(MISALIGNED, d, P, 0, 512, 2, 64, 64, 1.0, P, P, P, P, P, 8, P, P, P + 16, need, 0)
+    large = 1 << 19  # tokens of two slots of 64 elements
+    need = c.nvfp4_moe_dispatch_workspace_bytes(large, 2, 64)
+    assert need > 0 and c.nvfp4_moe_dispatch_workspace_bytes(4, 2, 64) == 0
+    refused(WORKSPACE, d, P, 0, large, 2, 64, 64, 1.0, P, P, P, P, P, 8, P, P, 0, 0, 0)
+    refused(WORKSPACE, d, P, 0, large, 2, 64, 64, 1.0, P, P, P, P, P, 8, P, P, P, need - 1, 0)
+    refused(MISALIGNED, d, P, 0, large, 2, 64, 64, 1.0, P, P, P, P, P, 8, P, P, P + 16, need, 0)
     s = c.nvfp4_moe_swiglu
     refused(INVALID, s, P, 1, 4, 64, 127, 0, 1.0, 0, 0, 1, P, P, 0)
     refused(INVALID, s, P, 1, 4, 64, 128, 0, 1.0, P, 0, 4, P, P, 0)

@@ -270,6 +270,31 @@ def test_quantize(dtype, m, k):
         assert np.array_equal(f64(moe.dequantize(a, sfa, dtype=out)), MO.values(codes, scales))
 
 
+@pytest.mark.parametrize("dtype,l,m,k", [("bf16", 1, 4099, 2080), ("fp16", 41, 131, 1632), ("fp32", 260, 33, 992)])
+def test_quantize_of_many_rows(dtype, l, m, k):
+    x = torch.randn(l, m, k, device="cuda", generator=torch.Generator("cuda").manual_seed(m)).to(TYPES[dtype])
+    x[:, ::5] *= 1e-3
+    a, sfa = moe.quantize(x)
+    an, sn, xn = a.cpu().numpy(), sfa.cpu().numpy(), f64(x)
+    for li in sorted({0, l // 2, l - 1}):
+        check_rows(an[li], sn, xn[li], k, atom=li * -(-m // 128))
+    values = moe.dequantize(a, sfa, dtype=torch.float32)
+    for li in sorted({0, l // 2, l - 1}):
+        rows = MO.unpack_rows(an[li], sn, m, k, li * -(-m // 128))
+        assert np.array_equal(f64(values[li]), MO.values(*rows))
+
+
+def test_dequantize_of_many_rows():
+    """The way back of 2^26 elements and a few, to all types, against single batches' way back."""
+    x = torch.randn(63, 1031, 1056, device="cuda", dtype=torch.float16, generator=torch.Generator("cuda").manual_seed(3))
+    a, sfa = moe.quantize(x)
+    per = mm.nvfp4_sf_bytes(1031, 1056)
+    for out in TYPES.values():
+        values = moe.dequantize(a, sfa, dtype=out)
+        for li in (0, 1, 40, 62):
+            assert torch.equal(values[li], moe.dequantize(a[li].clone(), sfa[li * per:(li + 1) * per].clone(), dtype=out))
+
+
 def test_quantize_at_the_borders():
     """Quotients on and next to every border of both roundings, zeros, the smallest and largest scales, and saturation."""
     rows = []
@@ -327,7 +352,8 @@ def test_quantize_batches_strides_and_guards():
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("tokens,topk,experts,k,dropped", [(1, 1, 1, 32, 0), (1, 8, 256, 7168, 0), (33, 8, 256, 96, 0.2), (130, 2, 3, 160, 0),
-                                                           (700, 4, 8, 1088, 0.5), (257, 3, 16, 320, 1.0), (64, 16, 40, 64, 0)])
+                                                           (700, 4, 8, 1088, 0.5), (257, 3, 16, 320, 1.0), (64, 16, 40, 64, 0),
+                                                           (4111, 8, 20, 1056, 0.01), (8200, 3, 300, 1440, 0.02)])
 def test_dispatch(dtype, tokens, topk, experts, k, dropped):
     rng = rng_of(tokens, topk, experts, k)
     ids = np.argsort(rng.random((tokens, experts)), axis=1)[:, :topk].astype(np.int32) if topk <= experts else None
@@ -351,7 +377,8 @@ def test_dispatch(dtype, tokens, topk, experts, k, dropped):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("tokens,topk,experts,k", [(1, 2, 8, 32), (9, 8, 64, 288), (400, 2, 5, 2048), (300, 4, 16, 96)])
+@pytest.mark.parametrize("tokens,topk,experts,k", [(1, 2, 8, 32), (9, 8, 64, 288), (400, 2, 5, 2048), (300, 4, 16, 96),
+                                                   (1031, 4, 7, 2080)])
 def test_swiglu(dtype, tokens, topk, experts, k):
     """Equal codes and scales: activations next to a border are decided in fp64 (the oracle's)."""
     rng = rng_of(tokens, topk, experts, k)
@@ -390,6 +417,30 @@ def test_swiglu_at_the_edges():
     assert np.isnan(v[3]).all() and np.isnan(v[4, :16]).all() and (v[4, 16:] == 0).all() and np.isnan(v[5, :16]).all()
     codes, scales = MO.quantize(MO.swiglu(f64(x[7:8])))
     assert np.array_equal(v[7:8], MO.values(codes, scales))
+
+
+@pytest.mark.parametrize("scale", [1e-20, 1.0, 1e20, 0.0])
+def test_swiglu_whose_factors_leave_the_range(scale):
+    """Products of alpha, scale and an operand below and beyond what fp32 has, where the activation is an ordinary number."""
+    alphas = [1e-30, 1e-25, 1e-19, 1e19, 1e25, 0.0]
+    ids = torch.arange(len(alphas), dtype=torch.int32).repeat_interleave(12).view(-1, 1)
+    p = moe.plan(ids.cuda(), len(alphas))
+    x = np.zeros((12 * len(alphas), 128), dtype=np.float32)
+    rng = rng_of(int(np.log2(scale)) + 999 if scale else 0)
+    for i, alpha in enumerate(np.repeat(np.array(alphas, dtype=np.float32), 12)):
+        al = float(alpha) or 1.0
+        for kb in range(4):  # of each block: g alpha, and what v is to be
+            g = np.float64(rng.choice([-60.0, -3.0, 1e-3, 1.0, 40.0, 1e12])) * rng.uniform(0.5, 1, 16)
+            v = np.float64(rng.choice([0.05, 1.0, 300.0])) * rng.standard_normal(16)
+            u = v / (g / (1 + np.exp(-g)) * al * (np.float64(np.float32(scale)) or 1.0))
+            x[i, kb * 16:kb * 16 + 16] = np.clip(g / al, -1e38, 1e38)
+            x[i, 64 + kb * 16:80 + kb * 16] = np.clip(u, -1e38, 1e38)
+    a, sfa = moe.swiglu_quantize(gpu(x), plan=p, alpha=gpu(np.array(alphas, dtype=np.float32)), scale=scale)
+    an, sn, atoms = a.cpu().numpy(), sfa.cpu().numpy(), p.atoms.cpu().numpy()
+    for e, alpha in enumerate(np.array(alphas, dtype=np.float32)):
+        v = MO.swiglu(x[e * 12:e * 12 + 12].astype(np.float64), float(alpha), float(np.float32(scale)))
+        v = np.where(np.abs(v) < 2.0 ** 128, v, np.inf)
+        check_rows(an[e * 12:e * 12 + 12], sn, v, 64, atom=int(atoms[e]))
 
 
 # ---- the combine ----------------------------------------------------------------------------
