@@ -192,30 +192,33 @@ int nvfp4_moe_dequantize(const void* a, const void* sfa, int l, int64_t m, int k
 /*
  * nvfp4_moe_combine - y[t] = residual[t] + sum over the slots j of t, in slot
  * order, of weights[t][j] * alpha[ids[t][j]] * c[slot_rows[t][j]], summed in
- * fp32 and rounded once to out_dtype. Slots of row -1 add nothing and are not read.
- *   c          device [rows][n] of c_dtype (fp16 or bf16 or fp32), rows c_stride apart
- *   slot_rows  NULL: the row of a slot is the slot
+ * fp32 and rounded once to out_dtype. Slots whose row is not in 0 .. c_rows - 1
+ * add nothing and read nothing.
+ *   c          device [c_rows][n] of c_dtype (fp16 or bf16 or fp32), rows c_stride apart
+ *   slot_rows  NULL: the row of a slot is the slot (then c_rows >= tokens*topk)
  *   weights    fp32 [tokens][topk], NULL: 1
- *   alpha      fp32 [experts], NULL: 1; needs ids
- *   ids        int32 [tokens][topk]; where given, a slot whose id is negative adds nothing
+ *   alpha      fp32 [experts], NULL: 1 (and experts is not looked at); needs ids
+ *   ids        int32 [tokens][topk]; where given, a slot whose id is negative, or with alpha not below experts, adds
+ *              nothing
  *   residual   [tokens][n] of out_dtype, rows out_stride apart, or NULL
  *   out        [tokens][n] of out_dtype, rows out_stride apart
  */
-int nvfp4_moe_combine(const void* c, int c_dtype, int64_t c_stride, int64_t tokens, int topk, int n,
+int nvfp4_moe_combine(const void* c, int c_dtype, int64_t c_stride, int64_t c_rows, int64_t tokens, int topk, int n,
                       const int32_t* slot_rows, const float* weights, const float* alpha, const int32_t* ids,
-                      const void* residual, void* out, int out_dtype, int64_t out_stride, void* stream);
+                      int experts, const void* residual, void* out, int out_dtype, int64_t out_stride, void* stream);
 
 /*
  * nvfp4_moe_combine_backward - gradients of nvfp4_moe_combine:
  *   dc[slot_rows[t][j]] = weights[t][j] * alpha * dy[t]   (of c_dtype, rows c_stride apart)
  *   dweights[t][j] = alpha * sum over n of dy[t] * c[slot_rows[t][j]]   (fp32)
- * Rows of dc that no slot names are not written; dweights of slots without a
- * row are 0. The residual's gradient is dy.
+ * Rows of dc that no slot names are not written; rows of slots without an expert
+ * are 0, and so are dweights of slots without a row or an expert. No two slots
+ * may name one row. The residual's gradient is dy.
  */
 int nvfp4_moe_combine_backward(const void* dy, int dy_dtype, int64_t dy_stride, const void* c, int c_dtype,
-                               int64_t c_stride, int64_t tokens, int topk, int n, const int32_t* slot_rows,
-                               const float* weights, const float* alpha, const int32_t* ids, void* dc,
-                               float* dweights, void* stream);
+                               int64_t c_stride, int64_t c_rows, int64_t tokens, int topk, int n,
+                               const int32_t* slot_rows, const float* weights, const float* alpha, const int32_t* ids,
+                               int experts, void* dc, float* dweights, void* stream);
 
 /*
  * nvfp4_moe_few_tokens - the experts' product of a few tokens with activations

@@ -56,10 +56,10 @@ _SIGNATURES = {
     "nvfp4_moe_dispatch_workspace_bytes": (_size, [_i64, _int, _int]),
     "nvfp4_moe_swiglu": (_int, [_ptr, _int, _i64, _int, _i64, _ptr, _float, _ptr, _ptr, _int, _ptr, _ptr, _ptr]),
     "nvfp4_moe_dequantize": (_int, [_ptr, _ptr, _int, _i64, _int, _ptr, _ptr, _int, _ptr, _int, _i64, _ptr]),
-    "nvfp4_moe_combine": (_int, [_ptr, _int, _i64, _i64, _int, _int, _ptr, _ptr, _ptr, _ptr, _ptr, _ptr, _int, _i64,
-                                 _ptr]),
-    "nvfp4_moe_combine_backward": (_int, [_ptr, _int, _i64, _ptr, _int, _i64, _i64, _int, _int, _ptr, _ptr, _ptr,
-                                          _ptr, _ptr, _ptr, _ptr]),
+    "nvfp4_moe_combine": (_int, [_ptr, _int, _i64, _i64, _i64, _int, _int, _ptr, _ptr, _ptr, _ptr, _int, _ptr, _ptr, _int,
+                                 _i64, _ptr]),
+    "nvfp4_moe_combine_backward": (_int, [_ptr, _int, _i64, _ptr, _int, _i64, _i64, _i64, _int, _int, _ptr, _ptr, _ptr,
+                                          _ptr, _int, _ptr, _ptr, _ptr]),
     "nvfp4_moe_few_tokens": (_int, [_ptr, _int, _i64, _int, _ptr, _i64, _int, _int, _int, _int, _ptr, _ptr, _ptr,
                                     _int, _ptr, _int, _ptr]),
     "nvfp4_moe_last_hip_error": (_int, []),

@@ -9,7 +9,7 @@ constexpr int kThreads = 256;
 
 struct CombineArgs {
   const void* c;
-  int64_t c_stride, tokens, out_stride, dy_stride;
+  int64_t c_stride, c_rows, tokens, out_stride, dy_stride;
   const int32_t *slot_rows, *ids;
   const float *weights, *alpha;
   const void* residual;
@@ -17,11 +17,12 @@ struct CombineArgs {
   const void* dy;
   void* dc;
   float* dweights;
-  int topk, n, chunks, c_vec, out_vec, dy_vec;
+  int topk, n, experts, chunks, c_vec, out_vec, dy_vec;
 };
 
-// A token's slots, one to a lane: row (-1: none), weight and expert's factor
-// (both 0 without a row).
+// A token's slots, one to a lane: row, weight and expert's factor. Slots that add
+// nothing have a negative row and factors of 0: -1, or where they have a row but
+// no expert, -2 - row (it gets gradients of 0).
 struct Slot {
   int64_t row;
   float weight, factor;
@@ -33,7 +34,10 @@ __device__ inline Slot slot_of(const CombineArgs& a, int64_t token, int lane) {
     const int id = a.ids == nullptr ? 0 : a.ids[slot];
     const int64_t row = a.slot_rows == nullptr ? slot : a.slot_rows[slot];
     const float weight = a.weights == nullptr ? 1.f : a.weights[slot];
-    if (id >= 0 && row >= 0) s = {row, weight, a.alpha == nullptr ? 1.f : a.alpha[id]};
+    if (row >= 0 && row < a.c_rows) {
+      if (id >= 0 && id < a.experts) s = {row, weight, a.alpha == nullptr ? 1.f : a.alpha[id]};
+      else s.row = -2 - row;
+    }
   }
   return s;
 }
@@ -70,7 +74,7 @@ __global__ void __launch_bounds__(kThreads) nvfp4_moe_combine_kernel(CombineArgs
     Raw8<C> v[K];
 #pragma unroll
     for (int j = 0; j < K; ++j) {
-      const int64_t row = row_of(slot, from + j);  // -1 from topk on
+      const int64_t row = row_of(slot, from + j);  // negative from topk on
       v[j] = Raw8<C>{};
       if (row >= 0 && mine) v[j].load(a.c, row * a.c_stride + col, a.c_vec);
     }
@@ -100,7 +104,7 @@ __global__ void __launch_bounds__(kThreads) nvfp4_moe_combine_backward_kernel(Co
   float w[K], sum[K];
 #pragma unroll
   for (int j = 0; j < K; ++j) {
-    row[j] = row_of(slot, j);  // -1 from topk on
+    row[j] = row_of(slot, j);  // negative from topk on
     w[j] = lane_value(gain, j);
     sum[j] = 0.f;
   }
@@ -115,7 +119,11 @@ __global__ void __launch_bounds__(kThreads) nvfp4_moe_combine_backward_kernel(Co
     raw.values(dy);
 #pragma unroll
     for (int j = 0; j < K; ++j) {
-      if (row[j] < 0) continue;
+      if (row[j] < 0) {
+        const float zeros[8] = {};
+        if (row[j] < -1) store8<C>(a.dc, (-2 - row[j]) * a.c_stride + col, a.c_vec, zeros);
+        continue;
+      }
       float x[8], d[8];
       v[j].values(x);
 #pragma unroll
@@ -145,7 +153,8 @@ int check_combine(const CombineArgs& a, int c_dtype, int dtype, int64_t stride, 
   if (a.tokens < 0 || a.tokens >= (int64_t)1 << 30 || a.topk < 1 || a.topk > NVFP4_MOE_MAX_TOPK) return NVFP4_ERR_INVALID;
   if (a.n < 0 || a.n % 8 || a.c_stride < a.n || stride < a.n) return NVFP4_ERR_INVALID;
   if (a.c_stride > (int64_t)1 << 30 || stride > (int64_t)1 << 30) return NVFP4_ERR_INVALID;
-  if (a.alpha != nullptr && a.ids == nullptr) return NVFP4_ERR_INVALID;
+  if (a.alpha != nullptr && (a.ids == nullptr || a.experts < 1)) return NVFP4_ERR_INVALID;
+  if (a.c_rows < 0 || (a.slot_rows == nullptr && a.tokens * a.topk > a.c_rows)) return NVFP4_ERR_INVALID;
   if (a.tokens > 0 && a.n > 0 && (a.c == nullptr || p == nullptr || q == nullptr)) return NVFP4_ERR_INVALID;
   if (!aligned(a.slot_rows, 4) || !aligned(a.ids, 4) || !aligned(a.weights, 4) || !aligned(a.alpha, 4))
     return NVFP4_ERR_MISALIGNED;
@@ -160,16 +169,18 @@ using namespace moe;
 
 extern "C" {
 
-int nvfp4_moe_combine(const void* c, int c_dtype, int64_t c_stride, int64_t tokens, int topk, int n,
+int nvfp4_moe_combine(const void* c, int c_dtype, int64_t c_stride, int64_t c_rows, int64_t tokens, int topk, int n,
                       const int32_t* slot_rows, const float* weights, const float* alpha, const int32_t* ids,
-                      const void* residual, void* out, int out_dtype, int64_t out_stride, void* stream) {
+                      int experts, const void* residual, void* out, int out_dtype, int64_t out_stride, void* stream) {
   CombineArgs a = {};
   a.c = c;
   a.c_stride = c_stride;
+  a.c_rows = c_rows;
   a.tokens = tokens;
   a.out_stride = out_stride;
   a.slot_rows = slot_rows;
   a.ids = ids;
+  a.experts = alpha == nullptr ? INT32_MAX : experts;
   a.weights = weights;
   a.alpha = alpha;
   a.residual = residual;
@@ -199,17 +210,19 @@ int nvfp4_moe_combine(const void* c, int c_dtype, int64_t c_stride, int64_t toke
 }
 
 int nvfp4_moe_combine_backward(const void* dy, int dy_dtype, int64_t dy_stride, const void* c, int c_dtype,
-                               int64_t c_stride, int64_t tokens, int topk, int n, const int32_t* slot_rows,
-                               const float* weights, const float* alpha, const int32_t* ids, void* dc,
-                               float* dweights, void* stream) {
+                               int64_t c_stride, int64_t c_rows, int64_t tokens, int topk, int n,
+                               const int32_t* slot_rows, const float* weights, const float* alpha, const int32_t* ids,
+                               int experts, void* dc, float* dweights, void* stream) {
   CombineArgs a = {};
   a.c = c;
   a.c_stride = c_stride;
+  a.c_rows = c_rows;
   a.tokens = tokens;
   a.dy = dy;
   a.dy_stride = dy_stride;
   a.slot_rows = slot_rows;
   a.ids = ids;
+  a.experts = alpha == nullptr ? INT32_MAX : experts;
   a.weights = weights;
   a.alpha = alpha;
   a.dc = dc;

@@ -154,6 +154,7 @@ class Product:
         sizes = self._tables.data_ptr()
         abc = sizes + 16 * experts
         self.tables = (sizes, abc, (abc + 24 * experts + 15) // 16 * 16)
+        self.planned = False
 
     def entry(self):
         return c.nvfp4_moe_product(self.n, self.k, self.a.data_ptr(), self.b.data_ptr(), self.out.data_ptr(),
@@ -161,6 +162,8 @@ class Product:
 
     def run(self, tile_config=-1, status=None, stream=None):
         """Enqueue the product, after a ``plan`` that this one was given to."""
+        if not self.planned:
+            raise ValueError("no plan has filled this product's tables")
         _enqueue(nvfp4_grouped_gemm_device, self.b.device, stream, *self.tables, self.experts, tile_config,
                  _at(status))
         return self.out
@@ -205,6 +208,8 @@ def plan(ids, experts, products=(), *, stream=None) -> Plan:
     workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
     _enqueue(c.nvfp4_moe_plan, device, stream, ids.data_ptr(), p.tokens, p.topk, experts, *p.addresses, entries,
              len(products), _at(workspace), need)
+    for q in products:
+        q.planned = True
     return p
 
 
@@ -340,13 +345,15 @@ def combine(x, weights, rows=None, *, alpha=None, ids=None, residual=None, dtype
     out = _out(out, "out", (tokens, n), dtype, device)
     if residual is not None:
         _like(residual, "residual", (tokens, n), dtype, device)
-    _enqueue(c.nvfp4_moe_combine, device, stream, x.data_ptr(), _type(x, "x"), stride, tokens, topk, n, _at(rows),
-             _at(weights), _at(alpha), _at(ids), _at(residual), out.data_ptr(), _type(out, "out"), n)
+    _enqueue(c.nvfp4_moe_combine, device, stream, x.data_ptr(), _type(x, "x"), stride, x.shape[0], tokens, topk, n,
+             _at(rows), _at(weights), _at(alpha), _at(ids), 0 if alpha is None else alpha.shape[0], _at(residual),
+             out.data_ptr(), _type(out, "out"), n)
     return out
 
 
 def combine_backward(dy, x, weights, rows=None, *, alpha=None, ids=None, dc=None, stream=None):
-    """(d x, d weights) of ``combine``; rows of d x that no slot has are not written."""
+    """(d x, d weights) of ``combine``; rows of d x that no slot has are not written, those of slots without an
+    expert are 0."""
     device = _gpu(x, "x")
     stride = _rows(x, "x")
     tokens, topk, rows, ids = _slots(weights, rows, alpha, ids, x, device)
@@ -359,8 +366,8 @@ def combine_backward(dy, x, weights, rows=None, *, alpha=None, ids=None, dc=None
         raise ValueError("dc must have x's shape, strides, type and device")
     dweights = torch.empty((tokens, topk), dtype=torch.float32, device=device)
     _enqueue(c.nvfp4_moe_combine_backward, device, stream, dy.data_ptr(), _type(dy, "dy"), dy_stride, x.data_ptr(),
-             _type(x, "x"), stride, tokens, topk, x.shape[1], _at(rows), _at(weights), _at(alpha), _at(ids),
-             dc.data_ptr(), dweights.data_ptr())
+             _type(x, "x"), stride, x.shape[0], tokens, topk, x.shape[1], _at(rows), _at(weights), _at(alpha), _at(ids),
+             0 if alpha is None else alpha.shape[0], dc.data_ptr(), dweights.data_ptr())
     return dc, dweights
 
 

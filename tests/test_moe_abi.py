@@ -146,15 +146,19 @@ def test_combine_refuses():
     for cd, cs, tokens, topk, n, od, os_ in ((3, 64, 4, 2, 64, 1, 64), (1, 63, 4, 2, 64, 1, 64), (1, 64, -1, 2, 64, 1, 64),
                                              (1, 64, 4, 0, 64, 1, 64), (1, 64, 4, 17, 64, 1, 64), (1, 64, 4, 2, 60, 1, 64),
                                              (1, 64, 4, 2, 64, 9, 64), (1, 64, 4, 2, 64, 1, 56)):
-        refused(INVALID, f, P, cd, cs, tokens, topk, n, P, P, 0, 0, 0, P, od, os_, 0)
-    refused(INVALID, f, P, 1, 64, 4, 2, 64, P, P, P, 0, 0, P, 1, 64, 0)  # alpha without ids
-    refused(INVALID, f, 0, 1, 64, 4, 2, 64, P, P, 0, 0, 0, P, 1, 64, 0)
-    refused(MISALIGNED, f, P, 1, 64, 4, 2, 64, P, P, 0, 0, 0, P + 1, 1, 64, 0)
-    refused(MISALIGNED, f, P, 1, 64, 4, 2, 64, P + 2, P, 0, 0, 0, P, 1, 64, 0)
+        refused(INVALID, f, P, cd, cs, 8, tokens, topk, n, P, P, 0, 0, 0, 0, P, od, os_, 0)
+    refused(INVALID, f, P, 1, 64, 8, 4, 2, 64, P, P, P, 0, 4, 0, P, 1, 64, 0)  # alpha without ids
+    refused(INVALID, f, P, 1, 64, 8, 4, 2, 64, P, P, P, P, 0, 0, P, 1, 64, 0)  # alpha of no experts
+    refused(INVALID, f, P, 1, 64, 7, 4, 2, 64, 0, P, 0, 0, 0, 0, P, 1, 64, 0)  # fewer rows than slots
+    refused(INVALID, f, P, 1, 64, -1, 4, 2, 64, P, P, 0, 0, 0, 0, P, 1, 64, 0)
+    refused(INVALID, f, 0, 1, 64, 8, 4, 2, 64, P, P, 0, 0, 0, 0, P, 1, 64, 0)
+    refused(MISALIGNED, f, P, 1, 64, 8, 4, 2, 64, P, P, 0, 0, 0, 0, P + 1, 1, 64, 0)
+    refused(MISALIGNED, f, P, 1, 64, 8, 4, 2, 64, P + 2, P, 0, 0, 0, 0, P, 1, 64, 0)
     b = c.nvfp4_moe_combine_backward
-    refused(INVALID, b, P, 1, 64, P, 1, 64, 4, 2, 64, P, P, 0, 0, P, 0, 0)
-    refused(INVALID, b, P, 1, 64, P, 1, 64, 4, 2, 64, P, P, 0, 0, 0, P, 0)
-    refused(MISALIGNED, b, P, 1, 64, P, 1, 64, 4, 2, 64, P, P, 0, 0, P + 1, P, 0)
+    refused(INVALID, b, P, 1, 64, P, 1, 64, 8, 4, 2, 64, P, P, 0, 0, 0, P, 0, 0)
+    refused(INVALID, b, P, 1, 64, P, 1, 64, 8, 4, 2, 64, P, P, 0, 0, 0, 0, P, 0)
+    refused(INVALID, b, P, 1, 64, P, 1, 64, 7, 4, 2, 64, 0, P, 0, 0, 0, P, P, 0)
+    refused(MISALIGNED, b, P, 1, 64, P, 1, 64, 8, 4, 2, 64, P, P, 0, 0, 0, P + 1, P, 0)
 
 
 def test_few_tokens_refuses():

@@ -508,6 +508,29 @@ def test_combine_slots_in_order_strides_and_refusals():
             bad()
 
 
+def test_combine_of_slots_without_rows_or_experts():
+    """Rows and experts that are not there add nothing, and what they name gets gradients of 0."""
+    x = torch.randn(8, 72, device="cuda")
+    alpha = torch.tensor([2.0, 3.0, 5.0], device="cuda")
+    ids = torch.tensor([[0, 3, 1], [-1, 2, 2 ** 31 - 1]], dtype=torch.int32, device="cuda")
+    w = torch.tensor([[0.5, 7.0, 1.0], [float("inf"), 2.0, float("nan")]], device="cuda")
+    dy = torch.full((2, 72), float("inf"), device="cuda")
+    dy[0] = 1.0
+    dy[1, 0] = 2.0
+    f = f64(x)
+    want = np.stack([0.5 * 2 * f[0] + 3 * f[2], 2 * 5 * f[4]])
+    close(moe.combine(x[:6], w, ids=ids, alpha=alpha), want, 4 * H[torch.float32] * np.abs(f).max() * 8, torch.float32)
+    dc = torch.full_like(x, 9.0)
+    _, dw = moe.combine_backward(dy, x[:6], w, ids=ids, alpha=alpha, dc=dc[:6])
+    assert (dc[[1, 3, 5]] == 0).all() and (dc[6:] == 9).all() and (dc[0] == 1).all() and (dc[2] == 3).all()
+    assert dc[4, 0] == 20 and (dw[[0, 1, 1], [1, 0, 2]] == 0).all()
+    rows = torch.tensor([[8, 0, -7], [2 ** 31 - 1, 7, -2 ** 31]], dtype=torch.int32, device="cuda")
+    ones = torch.ones_like(w)
+    assert torch.equal(moe.combine(x, ones, rows), x[[0, 7]])
+    dc, dw = moe.combine_backward(torch.ones_like(dy), x, ones, rows, dc=torch.full_like(x, 9.0))
+    assert (dc[[0, 7]] == 1).all() and (dc[1:7] == 9).all() and (dw[[0, 0, 1, 1], [0, 2, 0, 2]] == 0).all()
+
+
 def test_combine_backward_against_differences():
     """Of the kernel's own forward pass in fp32 (a sum of products: differences are exact but for rounding)."""
     x, rows, w, ids, alpha = combine_case(6, 3, 16, torch.float32, seed=3)
