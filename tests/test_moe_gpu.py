@@ -771,3 +771,41 @@ def test_other_streams_and_determinism():
     dc2 = moe.combine_backward(x, torch.randn(80, 512, device="cuda", generator=torch.Generator("cuda").manual_seed(1)), w,
                                torch.arange(80, dtype=torch.int32, device="cuda").view(40, 2))
     assert all(torch.equal(a, b) for a, b in zip(dc1, dc2))
+
+
+def test_what_a_call_on_another_stream_allocates_is_that_streams():
+    """Memory of the current stream may still be in use there, and may be used there again at once."""
+    layer, _, _, x, logits = layer_case(2000, 4, 2, 512, 256, "bf16", seed=4)
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        ids, w = moe.route(logits, 2)
+        torch.cuda.synchronize()
+        y = layer.grouped(x, ids, w, stream=stream)
+        a, sfa = moe.quantize(x, stream=stream)
+        side.synchronize()
+        at = {y.data_ptr(), a.data_ptr()}
+        del y, a, sfa
+        assert not at & {torch.empty(2000, n, dtype=torch.uint8, device="cuda").data_ptr() for n in (1024, 256)}
+        before = torch.cuda.memory_reserved()
+        with torch.cuda.stream(side):
+            layer.grouped(x, ids, w)   # finds what the calls before left there
+        assert torch.cuda.memory_reserved() == before
+    torch.cuda.synchronize()
+
+
+def test_products_and_layers_refuse_what_does_not_fit():
+    layer, _, _, x, logits = layer_case(8, 4, 2, 256, 128, "bf16", seed=5)
+    ids, w = moe.route(logits, 2)
+    for bad in (lambda: layer.grouped(x[:, :128], ids, w), lambda: layer.grouped(x[:7], ids, w), lambda: layer.grouped(x, ids.long(), w),
+                lambda: layer.grouped(x, ids, w.double()), lambda: layer.grouped(x, ids, w[:7]), lambda: layer.grouped(x.cpu(), ids, w),
+                lambda: layer.grouped(x, ids, w, residual=x.float()), lambda: layer.grouped(x.t(), ids, w), lambda: layer.few(x[:7], ids, w),
+                lambda: layer.few(x.float(), ids, w), lambda: moe.FeedForward(layer.b1, layer.sfb1, layer.b1, layer.sfb1),
+                lambda: moe.FeedForward(layer.b1, layer.sfb1, layer.b2, layer.sfb2, alpha1=w[0])):
+        with pytest.raises((ValueError, moe.c.Nvfp4MoeError)):
+            bad()
+    a, sfa = moe.quantize(x)
+    q = moe.Product(a, torch.zeros(moe.c.nvfp4_moe_sf_bytes(8, 4, 256), dtype=torch.uint8, device="cuda"), layer.b1, layer.sfb1,
+                    torch.zeros(8, 256, dtype=torch.float16, device="cuda"))
+    with pytest.raises(ValueError, match="plan"):
+        q.run()
+    assert layer.grouped(x[:0], ids[:0], w[:0]).shape == (0, 256)
