@@ -53,7 +53,9 @@ __device__ inline float lane_value(float v, int j) {
 
 // A wave takes 512 columns of a token, eight to a lane; its rows are read at
 // once and added in slot order. Bound by memory: each row of c is read once, in
-// whole lines that are not kept.
+// whole lines that are not kept. 8192 tokens of 8 rows of 7168 fp16, one in 20
+// dropped, to bf16: 1.01 GB in 169 us, 6.0 TB/s (a copy, half of it written, 4.9;
+// with one row under way at a time 177 us).
 template <class C, class Out, int K>
 __global__ void __launch_bounds__(kThreads) nvfp4_moe_combine_kernel(CombineArgs a) {
   const uint32_t wave = blockIdx.x * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -92,7 +94,8 @@ __global__ void __launch_bounds__(kThreads) nvfp4_moe_combine_kernel(CombineArgs
 
 // A workgroup per token: dy is read once, its rows of c once, dc written once.
 // The sums of d weights go thread by thread, then lanes, then waves: always in
-// the same order.
+// the same order. Bound by memory, half of it written: 4099 tokens of 4 rows of
+// 4096 fp16, 302 MB in 63 us, 4.8 TB/s.
 template <class C, class Dy, int K>
 __global__ void __launch_bounds__(kThreads) nvfp4_moe_combine_backward_kernel(CombineArgs a) {
   __shared__ float s_sum[K][kThreads / 64];

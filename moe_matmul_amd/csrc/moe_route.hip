@@ -79,11 +79,13 @@ struct Narrow {
 
 // ---- exp and sigmoid in fp64 -------------------------------------------------
 // 2^n times the Taylor series of e^r, |r| <= ln 2 / 2: 13 terms leave 2^-53 / 4.
+// r = x - n ln 2 with ln 2 in two parts (Cody and Waite): its first 42 bits, times
+// which an n of up to 11 bits is exact, and the rest.
 __device__ inline double exp_f64(double x) {
   x = fmin(fmax(x, -700.0), 700.0);
   const double n = __builtin_rint(x * 1.4426950408889634);
-  double r = fma(-n, 6.93147180369123816490e-01, x);
-  r = fma(-n, 1.90821492927058770002e-10, r);
+  double r = fma(-n, 0x1.62e42fefa38p-1, x);
+  r = fma(-n, 0x1.ef35793c7673p-45, r);
   double p = 1.0 / 479001600;
   p = fma(p, r, 1.0 / 39916800);
   p = fma(p, r, 1.0 / 3628800);
@@ -285,44 +287,37 @@ __device__ inline float load_logit(const void* logits, int dtype, int64_t at) {
                                   : load1<BF16>(logits, at);
 }
 
-// Whether the choice goes by the logits (as 32-bit keys where they have 16 bits)
-// or by scores (a bias, or groups).
-enum Mode { kLogits16, kLogits32, kScores };
+// Whether the choice goes by the logits (as 32-bit keys where they have 16 bits),
+// by scores (a bias), or by scores in groups.
+enum Mode { kLogits16, kLogits32, kScores, kGroups };
 
-// How many groups precede group g of a token, by worth and then by index:
-// certainly, and possibly, where worths within 2 * margin of each other may be equal.
-template <class V> __device__ inline void rank_of(const V* worth, int groups, int g, V margin, int& least, int& most) {
-  const V w = worth[g];
-  least = most = 0;
-  for (int o = 0; o < groups; ++o) {
-    const V u = worth[o];
-    const bool before = u > w || (u == w && o < g);
-    least += margin == V(0) ? before : u > w + 2 * margin;
-    most += margin == V(0) ? before : o != g && u + 2 * margin >= w;
-  }
+// How many groups precede group g of a token, by worth and then by index.
+__device__ inline int rank_of(const double* worth, int groups, int g) {
+  const double w = worth[g];
+  int before = 0;
+  for (int o = 0; o < groups; ++o) before += worth[o] > w || (worth[o] == w && o < g);
+  return before;
 }
 
-template <class Key> __device__ inline void best_two(Key v, Key& one, Key& two) {
-  two = max(two, min(one, v));
-  one = max(one, v);
+__device__ inline void best_two(double v, double& one, double& two) {
+  two = fmax(two, fmin(one, v));
+  one = fmax(one, v);
 }
 
 // The choice by scores in fp32, as 23-bit fixed-point numbers below the token's
 // largest choice value (0 for one that is 1 or more below it, and for none) over
-// the index: half the instructions of the
-// fp64 choice, and cheaper ones. In units of 2^-22 a number is off the exact
+// the index: half the instructions of the fp64 choice. In units of 2^-22 a number is off the exact
 // value by 1 for the score (e^-x within (|x| + 2) 2^-24, times s (1 - s); its sum
 // and reciprocal), 1 for the sum with a bias (values up to 5), 1.75 for the
 // difference and its truncation; with softmax by as much for the
 // score, and 11 more for the sum of up to 512 terms (a factor that all scores
 // share). Returns whether the list is that of the exact values: no two
-// neighbours in it, no candidate next to its end and no groups at the cut are
-// as near to each other as two such errors.
+// neighbours in it and no candidate next to its end are as near to each other as
+// two such errors.
 constexpr uint32_t kSigmoidMargin = 8, kSoftmaxMargin = 32;
 template <int K, int NC>
 __device__ inline bool choose_fp32(const RouteArgs& a, const Share& s, int lane, const float (&x)[NC * 8],
-                                   const float (&bias)[NC * 8], float from, float inverse, uint32_t (*s_best)[4],
-                                   uint32_t* s_worth, uint32_t (&list)[K]) {
+                                   const float (&bias)[NC * 8], float from, float inverse, uint32_t (&list)[K]) {
   const bool softmax = a.how.score == NVFP4_MOE_SOFTMAX;
   const uint32_t margin = softmax ? kSoftmaxMargin : kSigmoidMargin;
   float value[NC * 8], top = -__builtin_inff();
@@ -342,49 +337,6 @@ __device__ inline bool choose_fp32(const RouteArgs& a, const Share& s, int lane,
     const float fixed = fmaxf(fmaf(value[i], 0x1p22f, 0x1p22f - top * 0x1p22f), 0.f);  // 0 for NaN
     v[i] = (uint32_t)fminf(fixed, 0x1p22f) << 9 | (uint32_t)(kIndexMask - e);
   }
-  if (a.how.groups > 1) {
-    auto worth = [&](uint32_t one, uint32_t two) {
-      if (a.how.group_best == 1) return one >> 9;
-      sure &= two >> 9 > 0;  // without a second candidate, or with a far one, sums cannot be compared
-      return (one >> 9) + (two >> 9);
-    };
-    if (a.groups_of == 1) {
-      uint32_t one = 0, two = 0;
-#pragma unroll
-      for (int i = 0; i < NC * 8; ++i) best_two(v[i], one, two);
-      s_best[threadIdx.x][0] = one;
-      s_best[threadIdx.x][1] = two;
-      wave_sync();
-      for (int g = lane; g < a.how.groups; g += a.lanes) {
-        one = two = 0;
-        for (int q = 0; q < a.lanes_of; ++q) {
-          const int at = threadIdx.x - lane + g * a.lanes_of + q;
-          two = max(s_best[at][1], two);
-          best_two(s_best[at][0], one, two);
-        }
-        s_worth[g] = worth(one, two);
-      }
-    } else {
-      for (int q = 0; q < a.groups_of; ++q) {
-        const int g = lane * a.groups_of + q;
-        if (g >= a.how.groups) break;
-        uint32_t one = 0, two = 0;
-#pragma unroll
-        for (int i = 0; i < NC * 8; ++i) best_two(i / a.per == q ? v[i] : 0u, one, two);
-        s_worth[g] = worth(one, two);
-      }
-    }
-    wave_sync();
-    for (int q = 0; q < a.groups_of; ++q) {
-      const int g = a.groups_of == 1 ? group_of(a, lane) : lane * a.groups_of + q;
-      int least = a.how.groups, most = a.how.groups;
-      if (g < a.how.groups) rank_of(s_worth, a.how.groups, g, margin, least, most);
-      sure &= least >= a.how.topk_groups || most < a.how.topk_groups;
-#pragma unroll
-      for (int i = 0; i < NC * 8; ++i)
-        if ((a.groups_of == 1 || i / a.per == q) && least >= a.how.topk_groups) v[i] = 0u;
-    }
-  }
   keep_largest<Narrow, K, NC * 8>(v, list);
   merge_lanes<Narrow, K>(list, a.lanes);
   uint32_t last = 0;  // the last chosen
@@ -402,7 +354,7 @@ __device__ inline bool choose_fp32(const RouteArgs& a, const Share& s, int lane,
 }
 
 // The same in fp64, for any values.
-template <int K, int NC>
+template <int K, int NC, bool kGrouped>
 __device__ inline void choose_fp64(const RouteArgs& a, const Share& s, int lane, const float (&x)[NC * 8],
                                    const float (&bias)[NC * 8], float top, double (*s_best)[2], double* s_worth,
                                    double (&list)[K]) {
@@ -428,7 +380,7 @@ __device__ inline void choose_fp64(const RouteArgs& a, const Share& s, int lane,
     const int e = s.base + i / 8 * s.step + i % 8;
     v[i] = x[i] > -__builtin_inff() ? Wide::make(v[i] + bias[i], e) : Wide::none();  // none for a NaN logit, too
   }
-  if (a.how.groups > 1) {
+  if constexpr (kGrouped) {
     auto worth = [&](double one, double two) {
       return a.how.group_best == 1 || !Wide::there(two) ? Wide::value(one) : Wide::value(one) + Wide::value(two);
     };
@@ -461,8 +413,7 @@ __device__ inline void choose_fp64(const RouteArgs& a, const Share& s, int lane,
     wave_sync();
     for (int q = 0; q < a.groups_of; ++q) {
       const int g = a.groups_of == 1 ? group_of(a, lane) : lane * a.groups_of + q;
-      int before = a.how.groups, most;
-      if (g < a.how.groups) rank_of(s_worth, a.how.groups, g, 0.0, before, most);
+      const int before = g < a.how.groups ? rank_of(s_worth, a.how.groups, g) : a.how.groups;
 #pragma unroll
       for (int i = 0; i < NC * 8; ++i)
         if ((a.groups_of == 1 || i / a.per == q) && before >= a.how.topk_groups) v[i] = Wide::none();
@@ -477,11 +428,19 @@ __device__ inline void choose_fp64(const RouteArgs& a, const Share& s, int lane,
 // merge them in: two instructions for each comparison), and the lanes' lists are
 // merged in log2(lanes) steps. Bound by these instructions, not by the logits.
 // A choice by scores is made in fp32, and again in fp64 by a wave that holds a
-// token for which fp32 cannot tell.
+// token for which fp32 cannot tell (one token of 256 experts in 600); in groups in fp64 at once, as
+// with sums of groups to compare in both the registers no longer suffice, and the
+// few waves that go twice end last. In fp32 first - in fp64, sigmoid scores of bf16
+// logits with bias: 40000 x 64 9.3 - 10.2 us, 131072 x 64 19.3 - 22.9, 24000 x 128 11.1 -
+// 11.8; in 4 of 8 groups 16384 x 256 16.4 - 16.6, 131072 x 256 92 - 89, in 2 of 4
+// groups 65536 x 128 33 - 29. By logits: 65537 x 64 in fp32, softmax, 6 chosen, 10.2
+// us (17 MB read and 3 written, 4 us of a copy's rate; a launch is 3). One token of
+// 256 grouped scores 5.6 us.
 template <int K, int NC, Mode kMode>
 __global__ void __launch_bounds__(kThreads, NC > 2 ? 2 : 4) nvfp4_moe_route_kernel(RouteArgs a) {
   extern __shared__ double s_worth[];  // [tokens][groups]
-  __shared__ double s_best[kMode == kScores ? kThreads : 1][2];
+  __shared__ double s_best[kMode == kGroups ? kThreads : 1][2];
+  constexpr bool kByScore = kMode == kScores || kMode == kGroups;
   const int lane = threadIdx.x & (a.lanes - 1), local = threadIdx.x >> a.lane_bits;
   const int64_t mine = (int64_t)blockIdx.x * (kThreads >> a.lane_bits) + local;
   const int64_t token = mine < a.tokens ? mine : a.tokens - 1;  // lanes past the end repeat the last token
@@ -502,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, NC > 2 ? 2 : 4) nvfp4_moe_route_kern
 
   const bool softmax = a.how.score == NVFP4_MOE_SOFTMAX;
   float total = 1.f;  // of e^(x - top) over all experts
-  if (softmax && (kMode == kScores || !a.how.renormalize)) {
+  if (softmax && (kByScore || !a.how.renormalize)) {
     top = max_across(top, a.lanes);
     const float from = top == -__builtin_inff() ? 0.f : top;
     total = 0.f;
@@ -510,12 +469,12 @@ __global__ void __launch_bounds__(kThreads, NC > 2 ? 2 : 4) nvfp4_moe_route_kern
 #pragma unroll
     for (int i = 0; i < NC * 8; ++i) {
       const float e = __builtin_amdgcn_exp2f((x[i] - from) * 1.44269502f);
-      total += kMode == kScores && x[i] != x[i] ? 0.f : e;
+      total += kByScore && x[i] != x[i] ? 0.f : e;
     }
     total = sum_across(total, a.lanes);
   }
   int chosen_ids[K];
-  if constexpr (kMode == kScores) {
+  if constexpr (kByScore) {
     float bias[NC * 8];
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
@@ -532,16 +491,16 @@ __global__ void __launch_bounds__(kThreads, NC > 2 ? 2 : 4) nvfp4_moe_route_kern
 #pragma unroll
       for (int j = 0; j < 8; ++j) bias[c * 8 + j] = b[j];
     }
-    // both forms of the choice use a wave's own parts of s_best and s_worth
-    uint32_t list[K];
-    const bool sure = choose_fp32<K, NC>(a, s, lane, x, bias, top, 1.f / total, (uint32_t(*)[4])s_best,
-                                         (uint32_t*)(s_worth + local * a.how.groups), list);
+    bool sure = false;
+    if constexpr (kMode == kScores) {
+      uint32_t list[K];
+      sure = choose_fp32<K, NC>(a, s, lane, x, bias, top, 1.f / total, list);
 #pragma unroll
-    for (int i = 0; i < K; ++i) chosen_ids[i] = kIndexMask - (int)(list[i] & kIndexMask);
+      for (int i = 0; i < K; ++i) chosen_ids[i] = kIndexMask - (int)(list[i] & kIndexMask);
+    }
     if (__any(!sure)) {
-      double exact[K];
-      wave_sync();
-      choose_fp64<K, NC>(a, s, lane, x, bias, top, s_best, s_worth + local * a.how.groups, exact);
+      double exact[K];  // a wave's own parts of s_best and s_worth
+      choose_fp64<K, NC, kMode == kGroups>(a, s, lane, x, bias, top, s_best, s_worth + local * a.how.groups, exact);
 #pragma unroll
       for (int i = 0; i < K; ++i) chosen_ids[i] = Wide::index(exact[i]);
     }
@@ -639,6 +598,8 @@ __device__ inline void store_share(void* row, const Share& s, bool vec, const fl
 // Only the softmax that is not renormalised has a gradient for experts that
 // were not chosen, and only it reads the whole row. The chosen experts' values
 // go to their lanes through shared memory; every lane then writes its share.
+// Bound by memory and the launch: 65537 x 64 fp32 logits of a dense softmax,
+// 34 MB and 3 MB of ids and dw, 10.4 us (7.5 us at a copy's rate, 3 a launch).
 template <int NC>
 __global__ void __launch_bounds__(kThreads) nvfp4_moe_route_backward_kernel(RouteBackwardArgs a) {
   __shared__ float s_dp[NC * 8][kThreads];
@@ -739,7 +700,7 @@ int at_least_pow2(int v) {
   return p;
 }
 
-// Lanes of a token: few, as the lanes' merged lists are the same work in each of
+// Lanes of a token: as few as hold its logits in registers, as the lanes' merged lists are the same work in each of
 // them, but more where there are too few tokens to fill the chip (15000 tokens x
 // 256 logits: 9.7 us with 8 lanes, 13.4 with 16; 16384 x 256 scores, which take
 // three times as long before the merges: 20 us with 8, 16.8 with 16).
@@ -765,7 +726,8 @@ int lay_out(RouteArgs& a) {
 template <int K, int NC> void launch_route(const RouteArgs& a, Mode mode, int64_t blocks, hipStream_t stream) {
   const dim3 grid((unsigned)blocks);
   const size_t shared = a.how.groups > 1 ? sizeof(double) * (kThreads / a.lanes) * a.how.groups : 0;
-  if (mode == kScores) nvfp4_moe_route_kernel<K, NC, kScores><<<grid, kThreads, shared, stream>>>(a);
+  if (mode == kGroups) nvfp4_moe_route_kernel<K, NC, kGroups><<<grid, kThreads, shared, stream>>>(a);
+  else if (mode == kScores) nvfp4_moe_route_kernel<K, NC, kScores><<<grid, kThreads, 0, stream>>>(a);
   else if (mode == kLogits16) nvfp4_moe_route_kernel<K, NC, kLogits16><<<grid, kThreads, 0, stream>>>(a);
   else nvfp4_moe_route_kernel<K, NC, kLogits32><<<grid, kThreads, 0, stream>>>(a);
 }
@@ -792,7 +754,10 @@ int nvfp4_moe_route(const void* logits, int dtype, int64_t tokens, int experts, 
   if (tokens > 0 && (ids == nullptr || weights == nullptr)) return NVFP4_ERR_INVALID;
   if (!aligned(ids, 4) || !aligned(weights, 4) || !aligned(bias, 4)) return NVFP4_ERR_MISALIGNED;
   if (tokens == 0) return NVFP4_OK;
-  const Mode mode = bias != nullptr || choice->groups > 1 ? kScores : dtype == NVFP4_MOE_F32 ? kLogits32 : kLogits16;
+  const Mode mode = choice->groups > 1         ? kGroups
+                    : bias != nullptr          ? kScores
+                    : dtype == NVFP4_MOE_F32   ? kLogits32
+                                               : kLogits16;
   RouteArgs a = {};
   a.logits = logits;
   a.tokens = tokens;
@@ -805,7 +770,7 @@ int nvfp4_moe_route(const void* logits, int dtype, int64_t tokens, int experts, 
   a.vec = wide_rows(logits, dtype, row_stride);
   a.bias_vec = aligned(bias, 16);
   a.how = *choice;
-  a.lanes = widen(kLeastLanes, tokens, experts, mode == kScores ? kScoreLanes : kLogitLanes);
+  a.lanes = widen(kLeastLanes, tokens, experts, mode == kScores || mode == kGroups ? kScoreLanes : kLogitLanes);
   int chunks = lay_out(a);
   while (chunks > 4) {
     a.lanes *= 2;

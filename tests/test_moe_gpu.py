@@ -142,6 +142,30 @@ def test_route_at_the_edges(dtype, options):
     assert torch.isnan(w[8]).any() and not torch.isnan(w[:8]).any()
 
 
+@pytest.mark.parametrize("experts,topk,dtype,options", [
+    (64, 6, "bf16", dict(score="sigmoid", bias=True)), (40, 4, "fp32", dict(groups=4, topk_groups=2, group_best=1)),
+    (128, 8, "fp32", dict(score="sigmoid", bias=True, groups=8, topk_groups=4, group_best=2, renormalize=False)),
+    (60, 10, "fp16", dict(groups=20, topk_groups=7, group_best=2, bias=True))])
+def test_route_of_many_tokens_is_that_of_few(experts, topk, dtype, options):
+    """Scores that are nearly or exactly equal, far apart, masked and not finite: in one call of 140000 tokens, and in
+    calls of 2000 (which the oracle checks above)."""
+    g = torch.Generator("cuda").manual_seed(experts)
+    x = torch.randn(140000, experts, device="cuda", generator=g)
+    x[1::5] = x[1::5] * 1e-5 + 0.5
+    x[2::5] = x[2::5] * 20
+    x[3::10, ::2] = x[3::10, 1::2]
+    x.masked_fill_(torch.rand(x.shape, device="cuda", generator=g) < 0.05, float("-inf"))
+    x[:200, 3], x[100:300, 5], x[400] = float("inf"), float("nan"), float("-inf")
+    x = x.to(TYPES[dtype])
+    how = dict(options)
+    bias = torch.randn(experts, device="cuda", generator=g) * 1e-6 if how.pop("bias", False) else None
+    ids, w = moe.route(x, topk, bias=bias, **how)
+    for i in range(0, 140000, 2000):
+        few_ids, few_w = moe.route(x[i:i + 2000], topk, bias=bias, **how)
+        assert torch.equal(ids[i:i + 2000], few_ids)
+        close(w[i:i + 2000], f64(few_w), 64 * H[torch.float32] * np.abs(np.nan_to_num(f64(few_w))), torch.float32)
+
+
 def test_route_strides_alignment_and_outputs():
     base = torch.randn(40, 3 + 61 + 4, device="cuda").to(torch.bfloat16)
     x = base[:, 3:64]                             # odd offset, odd width, rows 68 apart
