@@ -30,7 +30,9 @@
  * call with the same return codes (NVFP4_ERR_INVALID for sizes, types and null
  * pointers, NVFP4_ERR_MISALIGNED for addresses, NVFP4_ERR_WORKSPACE). Results
  * do not depend on timing: no sum's order does. Strides count elements.
- * Outputs may not overlap inputs. Calls with no work (0 tokens or rows) are
+ * Outputs may not overlap inputs. A call that would need more than about 2^31
+ * threads is NVFP4_ERR_INVALID (2^23 workgroups of 256: 2^34 elements of rows to
+ * quantise). Calls with no work (0 tokens or rows) are
  * NVFP4_OK and launch nothing, except that nvfp4_moe_plan of 0 tokens writes
  * its offsets.
  */

@@ -2,7 +2,9 @@
 
 The computation runs in the hand-written HIP library
 (``libnvfp4_grouped_gemm.so``, C ABI in ``include/nvfp4_grouped_gemm.h``);
-this package is its thin Python binding plus device-memory plumbing.
+this package is its thin Python binding plus device-memory plumbing. The
+operators around it (``libnvfp4_moe.so``, C ABI in ``include/nvfp4_moe.h``) are in
+``moe_matmul_amd.moe``.
 """
 from ._binding import (  # noqa: F401
     LIB_PATH, NVFP4_ERR_CONFIG, NVFP4_ERR_HIP, NVFP4_ERR_INVALID, NVFP4_ERR_MISALIGNED, NVFP4_ERR_WORKSPACE,
