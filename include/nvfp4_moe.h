@@ -158,7 +158,9 @@ int nvfp4_moe_quantize(const void* x, int dtype, int l, int64_t m, int k, int64_
 /*
  * nvfp4_moe_dispatch - as nvfp4_moe_quantize for x [tokens][k], each token's
  * row written to the rows of its slots in the plan (ids, and slot_rows, row_slots,
- * offsets and atoms of nvfp4_moe_plan for them).
+ * offsets and atoms of nvfp4_moe_plan for them). A row's expert is the one whose
+ * rows hold it; ids say where that is looked for first, and may have been rewritten
+ * since. Nothing is stored outside a and sfa, whatever the tables hold.
  *   a          device uint8 [tokens*topk][k/2]
  *   sfa        device uint8 [nvfp4_moe_sf_bytes(tokens*topk, experts, k)]
  *   workspace  device, 256-byte aligned, nvfp4_moe_dispatch_workspace_bytes (may be 0) bytes

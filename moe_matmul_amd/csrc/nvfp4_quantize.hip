@@ -243,21 +243,23 @@ template <class T> struct SwigluSource {
 };
 
 // ---- where rows lie ------------------------------------------------------------
+// The last of `count` parts whose start is at most v, 0 at the least.
+__device__ inline int last_at_most(const int32_t* starts, int count, int v) {
+  int low = 0, high = count;  // starts[low] <= v < starts[high]
+  while (high - low > 1) {
+    const int mid = (low + high) / 2;
+    if (starts[mid] <= v) low = mid;
+    else high = mid;
+  }
+  return low;
+}
+
 // Rows in batches of m (offsets null), or sorted by expert.
 struct Rows {
   const int32_t *offsets, *atoms;
   int experts;
   int64_t rows, m;  // all of them, of a batch
 
-  __device__ inline int last_at_most(const int32_t* starts, int v) const {
-    int low = 0, high = experts;  // starts[low] <= v < starts[high]
-    while (high - low > 1) {
-      const int mid = (low + high) / 2;
-      if (starts[mid] <= v) low = mid;
-      else high = mid;
-    }
-    return low;
-  }
   // Expert (or batch) of a row, its atom row and its row in that.
   __device__ inline void find(int64_t row, int& expert, int64_t& atom, int& r) const {
     if (offsets == nullptr) {
@@ -266,7 +268,7 @@ struct Rows {
       atom = batch * ceil_div64(m, kAtomRows) + at / kAtomRows;
       r = (int)(at % kAtomRows);
     } else {
-      expert = last_at_most(offsets, (int)row);
+      expert = last_at_most(offsets, experts, (int)row);
       const int at = (int)row - offsets[expert];
       atom = atoms[expert] + at / kAtomRows;
       r = at % kAtomRows;
@@ -284,9 +286,10 @@ struct Rows {
       count = expert = 0;
       return 0;
     }
-    expert = last_at_most(atoms, (int)atom);
+    expert = last_at_most(atoms, experts, (int)atom);
     const int at = ((int)atom - atoms[expert]) * kAtomRows, first = offsets[expert] + at;
     count = min(kAtomRows, offsets[expert + 1] - first);
+    if (first < 0 || (int64_t)first + count > rows) count = 0;  // not a plan's offsets: no rows rather than others' memory
     return first;
   }
 };
@@ -373,9 +376,20 @@ __global__ void __launch_bounds__(kTileThreads)
 // token_scales [tokens][atoms along k, padded to fours] and nvfp4_dispatch_scales_kernel lays them out.
 // Bound by memory: 4096 x 7168 bf16 to 31000 rows of 64 experts, 59 MB read and
 // 125 MB written in 36 us and 11 for the scales.
+// Nothing is stored outside a and sfa, whatever the tables hold: a row has to be
+// one of `rows`, an atom row one of `atom_rows`, and a slot's id says only where
+// its row's expert is looked for first: a caller may have written other ids there
+// since the plan was made.
 struct Slots {
   const int32_t *ids, *slot_rows, *offsets, *atoms;
-  int topk, experts;
+  int topk, experts, rows;
+  int64_t atom_rows;
+
+  __device__ inline int expert_of(int64_t slot, int row) const {
+    const int e = ids[slot];
+    if ((unsigned)e < (unsigned)experts && offsets[e] <= row && row < offsets[e + 1]) return e;
+    return last_at_most(offsets, experts, row);
+  }
 };
 template <int kLane> __device__ inline uint32_t of_quad(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, kLane * 0x55, 0xF, 0xF, false);
@@ -395,12 +409,13 @@ __global__ void __launch_bounds__(kRowThreads)
   for (int j = p.kh % 4; j < slots.topk; j += 4) {
     const int64_t slot = p.row * slots.topk + j;
     const int row = slots.slot_rows[slot];
-    if (row < 0) continue;
+    if ((unsigned)row >= (unsigned)slots.rows) continue;
     if (there) *(u32x4*)(a + (int64_t)row * 2 * blocks + p.kh / 4 * 4) = codes;
     if (kDirect && p.kh % 8 < 4) {
-      const int e = slots.ids[slot], at = row - slots.offsets[e];
-      const int64_t atom = slots.atoms[e] + at / kAtomRows;
-      *(uint32_t*)(sfa + (atom * along + p.kh / 8) * kAtomBytes + atom_row(at % kAtomRows)) = word;
+      const int e = slots.expert_of(slot, row), at = row - slots.offsets[e];
+      const int64_t atom = (int64_t)slots.atoms[e] + at / kAtomRows;
+      if ((uint64_t)atom < (uint64_t)slots.atom_rows)
+        *(uint32_t*)(sfa + (atom * along + p.kh / 8) * kAtomBytes + atom_row(at % kAtomRows)) = word;
     }
   }
   if (!kDirect && p.kh % 8 == 0) token_scales[p.row * (ceil_div(along, 4) * 4) + p.kh / 8] = word;
@@ -421,7 +436,8 @@ __global__ void __launch_bounds__(kScaleThreads)
   const int64_t first = rows.first_row(atom, count, expert);
   if (count == 0) return;
   const int r = threadIdx.x / 4 + threadIdx.x % 4 * 32;
-  const int64_t token = r < count ? row_slots[first + r] / topk : -1;
+  const int slot = r < count ? row_slots[first + r] : -1;
+  const int64_t token = slot >= 0 && slot < rows.rows ? slot / topk : -1;
   const uint32_t* in = token_scales + token * stride;
   uint32_t* out = (uint32_t*)(sfa + atom * along * kAtomBytes) + threadIdx.x;
   u32x4 word[kScaleAtoms / 4];
@@ -605,7 +621,8 @@ int nvfp4_moe_dispatch(const void* x, int dtype, int64_t tokens, int topk, int k
                        const int32_t* ids, const int32_t* slot_rows, const int32_t* row_slots,
                        const int32_t* offsets, const int32_t* atoms, int experts, void* a, void* sfa,
                        void* workspace, size_t workspace_bytes, void* stream) {
-  if (topk < 1 || topk > NVFP4_MOE_MAX_TOPK || tokens < 0 || tokens * topk > (int64_t)1 << 30) return NVFP4_ERR_INVALID;
+  if (topk < 1 || topk > NVFP4_MOE_MAX_TOPK || tokens < 0 || tokens > (int64_t)1 << 30 || tokens * topk > (int64_t)1 << 30)
+    return NVFP4_ERR_INVALID;
   if (int rc = check_source(x, dtype, tokens, k, row_stride)) return rc;
   if (int rc = check_operand(tokens * topk, k, a, sfa)) return rc;
   if (offsets == nullptr) return NVFP4_ERR_INVALID;
@@ -621,7 +638,7 @@ int nvfp4_moe_dispatch(const void* x, int dtype, int64_t tokens, int topk, int k
   const Rows rows = {offsets, atoms, experts, tokens * topk, 0};
   const int64_t scale_grid = atom_rows(rows, 1) * ceil_div(along, kScaleAtoms);
   if (grid > kMaxGrid || scale_grid > kMaxGrid) return NVFP4_ERR_INVALID;
-  const Slots slots = {ids, slot_rows, offsets, atoms, topk, experts};
+  const Slots slots = {ids, slot_rows, offsets, atoms, topk, experts, (int)rows.rows, atom_rows(rows, 1)};
   const hipStream_t st = (hipStream_t)stream;
   int rc = with_rows(dtype, x, row_stride, 0, 0, scale, wide_rows(x, dtype, row_stride), [&](auto src) {
     using Source = decltype(src);
