@@ -133,6 +133,15 @@ typedef struct nvfp4_moe_product {
 int nvfp4_moe_plan(const int32_t* ids, int64_t tokens, int topk, int experts, int32_t* offsets, int32_t* atoms,
                    int32_t* slot_rows, int32_t* row_slots, const nvfp4_moe_product* products, int num_products,
                    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * nvfp4_moe_plan_ex - as nvfp4_moe_plan, with a copy of the ids that belongs to
+ * the plan, for callers whose ids are rewritten while the plan is in use:
+ *   slot_ids   device int32 [tokens*topk]: expert of a slot, or -1 where it has none; or NULL
+ */
+int nvfp4_moe_plan_ex(const int32_t* ids, int64_t tokens, int topk, int experts, int32_t* offsets, int32_t* atoms,
+                      int32_t* slot_rows, int32_t* row_slots, int32_t* slot_ids, const nvfp4_moe_product* products,
+                      int num_products, void* workspace, size_t workspace_bytes, void* stream);
 size_t nvfp4_moe_plan_workspace_bytes(int64_t tokens, int topk, int experts);
 
 /* Bytes of the scales of up to `rows` rows sorted by expert: room for any

@@ -48,6 +48,7 @@ _SIGNATURES = {
     "nvfp4_moe_route": (_int, [_ptr, _int, _i64, _int, _i64, _ptr, _choice, _ptr, _ptr, _ptr]),
     "nvfp4_moe_route_backward": (_int, [_ptr, _int, _i64, _int, _i64, _choice, _ptr, _ptr, _ptr, _i64, _ptr]),
     "nvfp4_moe_plan": (_int, [_ptr, _i64, _int, _int, _ptr, _ptr, _ptr, _ptr, _products, _int, _ptr, _size, _ptr]),
+    "nvfp4_moe_plan_ex": (_int, [_ptr, _i64, _int, _int, _ptr, _ptr, _ptr, _ptr, _ptr, _products, _int, _ptr, _size, _ptr]),
     "nvfp4_moe_plan_workspace_bytes": (_size, [_i64, _int, _int]),
     "nvfp4_moe_sf_bytes": (_size, [_i64, _int, _int]),
     "nvfp4_moe_quantize": (_int, [_ptr, _int, _int, _i64, _int, _i64, _i64, _float, _ptr, _ptr, _ptr]),
@@ -96,6 +97,7 @@ def _checked(name):
 nvfp4_moe_route = _checked("nvfp4_moe_route")
 nvfp4_moe_route_backward = _checked("nvfp4_moe_route_backward")
 nvfp4_moe_plan = _checked("nvfp4_moe_plan")
+nvfp4_moe_plan_ex = _checked("nvfp4_moe_plan_ex")
 nvfp4_moe_quantize = _checked("nvfp4_moe_quantize")
 nvfp4_moe_dispatch = _checked("nvfp4_moe_dispatch")
 nvfp4_moe_swiglu = _checked("nvfp4_moe_swiglu")

@@ -21,6 +21,7 @@ struct PlanArgs {
   int slots, experts, id_bits;  // id_bits: bits that tell the bins 0 .. experts apart
   int block_slots, blocks;
   int32_t *offsets, *atoms, *slot_rows, *row_slots;
+  int32_t* slot_ids;  // or null
   int32_t* counts;  // [blocks][experts], of every block's slots; null where every block counts all slots
   int num_products;
   nvfp4_moe_product products[NVFP4_MOE_MAX_PRODUCTS];
@@ -179,6 +180,7 @@ __global__ void __launch_bounds__(kThreads) nvfp4_moe_place_kernel(PlanArgs a) {
     } else if (i < end) {
       a.slot_rows[i] = -1;
     }
+    if (a.slot_ids != nullptr && i < end) a.slot_ids[i] = bin;
     wave_sync();
   }
 }
@@ -238,11 +240,19 @@ size_t nvfp4_moe_sf_bytes(int64_t rows, int experts, int k) {
 int nvfp4_moe_plan(const int32_t* ids, int64_t tokens, int topk, int experts, int32_t* offsets, int32_t* atoms,
                    int32_t* slot_rows, int32_t* row_slots, const nvfp4_moe_product* products, int num_products,
                    void* workspace, size_t workspace_bytes, void* stream) {
+  return nvfp4_moe_plan_ex(ids, tokens, topk, experts, offsets, atoms, slot_rows, row_slots, nullptr, products, num_products,
+                           workspace, workspace_bytes, stream);
+}
+
+int nvfp4_moe_plan_ex(const int32_t* ids, int64_t tokens, int topk, int experts, int32_t* offsets, int32_t* atoms,
+                      int32_t* slot_rows, int32_t* row_slots, int32_t* slot_ids, const nvfp4_moe_product* products,
+                      int num_products, void* workspace, size_t workspace_bytes, void* stream) {
   if (!plan_sizes(tokens, topk, experts) || offsets == nullptr || atoms == nullptr) return NVFP4_ERR_INVALID;
   if (tokens > 0 && (ids == nullptr || slot_rows == nullptr || row_slots == nullptr)) return NVFP4_ERR_INVALID;
   if (num_products < 0 || num_products > NVFP4_MOE_MAX_PRODUCTS || (num_products > 0 && products == nullptr))
     return NVFP4_ERR_INVALID;
-  if (!aligned(ids, 4) || !aligned(offsets, 4) || !aligned(atoms, 4) || !aligned(slot_rows, 4) || !aligned(row_slots, 4))
+  if (!aligned(ids, 4) || !aligned(offsets, 4) || !aligned(atoms, 4) || !aligned(slot_rows, 4) || !aligned(row_slots, 4) ||
+      !aligned(slot_ids, 4))
     return NVFP4_ERR_MISALIGNED;
   PlanArgs a = {};
   for (int i = 0; i < num_products; ++i) {
@@ -265,6 +275,7 @@ int nvfp4_moe_plan(const int32_t* ids, int64_t tokens, int topk, int experts, in
   a.atoms = atoms;
   a.slot_rows = slot_rows;
   a.row_slots = row_slots;
+  a.slot_ids = slot_ids;
   a.counts = need > 0 ? (int32_t*)workspace : nullptr;
   a.num_products = num_products;
   const hipStream_t st = (hipStream_t)stream;

@@ -194,26 +194,27 @@ class Product:
 
 
 class Plan:
-    """Where the rows of every slot lie: ``offsets`` and ``atoms`` [experts + 1], ``slot_rows`` [tokens, topk] and
-    ``row_slots`` [tokens * topk] (all int32), and the ``ids`` that they were made from."""
+    """Where the rows of every slot lie: ``offsets`` and ``atoms`` [experts + 1], ``slot_rows`` and ``ids`` [tokens, topk]
+    and ``row_slots`` [tokens * topk] (all int32). ``ids`` are the plan's own (-1 where a slot has no expert): those that it
+    was made from may be rewritten once it is."""
 
-    def __init__(self, ids, experts):
-        self.ids, self.experts = ids, experts
-        self.tokens, self.topk = ids.shape
+    def __init__(self, tokens, topk, experts, device):
+        self.tokens, self.topk, self.experts, self.device = tokens, topk, experts, device
         #: the most rows there can be (those that are there: ``offsets[experts]``, on the device)
         self.rows = self.tokens * self.topk
-        self._store = torch.empty(2 * (experts + 1 + self.rows), dtype=torch.int32, device=ids.device)
-        at = self._store.data_ptr()
-        #: addresses of offsets, atoms, slot_rows and row_slots
-        self.addresses = (at, at + 4 * (experts + 1), at + 8 * (experts + 1), at + 8 * (experts + 1) + 4 * self.rows)
+        self._store = torch.empty(2 * (experts + 1) + 3 * self.rows, dtype=torch.int32, device=device)
+        at, rows = self._store.data_ptr(), 4 * self.rows
+        slots = at + 8 * (experts + 1)
+        #: addresses of offsets, atoms, slot_rows, row_slots and ids
+        self.addresses = (at, at + 4 * (experts + 1), slots, slots + rows, slots + 2 * rows)
 
     def __getattr__(self, name):
         # the views are made when they are first asked for
-        if name not in ("offsets", "atoms", "slot_rows", "row_slots"):
+        if name not in ("offsets", "atoms", "slot_rows", "row_slots", "ids"):
             raise AttributeError(name)
-        n = self.experts + 1
-        self.offsets, self.atoms, rows, self.row_slots = self._store.split((n, n, self.rows, self.rows))
-        self.slot_rows = rows.view(self.tokens, self.topk)
+        n, shape = self.experts + 1, (self.tokens, self.topk)
+        self.offsets, self.atoms, rows, self.row_slots, ids = self._store.split((n, n, self.rows, self.rows, self.rows))
+        self.slot_rows, self.ids = rows.view(shape), ids.view(shape)
         return self.__dict__[name]
 
 
@@ -224,14 +225,14 @@ def plan(ids, experts, products=(), *, stream=None) -> Plan:
     if ids.dim() != 2:
         raise ValueError(f"ids must have shape [tokens, topk], not {tuple(ids.shape)}")
     _like(ids, "ids", ids.shape, torch.int32, device)
-    p = Plan(ids, experts)
+    p = Plan(*ids.shape, experts, device)
     entries = (c.nvfp4_moe_product * len(products))(*[q.entry() for q in products]) if products else None
     for q in products:
         if q.experts != experts or q.a.shape[0] < p.rows or q.device != device:
             raise ValueError("a product must have the plan's experts and device, and room for its rows")
     need = c.nvfp4_moe_plan_workspace_bytes(p.tokens, p.topk, experts)
     workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
-    _enqueue(c.nvfp4_moe_plan, device, ids.data_ptr(), p.tokens, p.topk, experts, *p.addresses, entries,
+    _enqueue(c.nvfp4_moe_plan_ex, device, ids.data_ptr(), p.tokens, p.topk, experts, *p.addresses, entries,
              len(products), _at(workspace), need)
     for q in products:
         q.planned = True
@@ -264,15 +265,15 @@ def quantize(x, *, plan=None, scale=1.0, a=None, sfa=None, stream=None):
         raise ValueError(f"rows must have a multiple of 32 elements, not {k}")
     if plan is not None:
         stride = _rows(x, "x")
-        if x.shape[0] != plan.tokens or plan.ids.device != device:
+        if x.shape[0] != plan.tokens or plan.device != device:
             raise ValueError(f"x must have the plan's {plan.tokens} tokens, on its device")
         a = _out(a, "a", (plan.rows, k // 2), torch.uint8, device)
         sfa = _out(sfa, "sfa", (c.nvfp4_moe_sf_bytes(plan.rows, plan.experts, k),), torch.uint8, device)
         need = c.nvfp4_moe_dispatch_workspace_bytes(plan.tokens, plan.topk, k)
         workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
-        offsets, atoms, slot_rows, row_slots = plan.addresses
+        offsets, atoms, slot_rows, row_slots, ids = plan.addresses
         _enqueue(c.nvfp4_moe_dispatch, device, x.data_ptr(), kind, plan.tokens, plan.topk, k, stride, scale,
-                 plan.ids.data_ptr(), slot_rows, row_slots, offsets, atoms, plan.experts, a.data_ptr(), sfa.data_ptr(),
+                 ids, slot_rows, row_slots, offsets, atoms, plan.experts, a.data_ptr(), sfa.data_ptr(),
                  _at(workspace), need)
         return a, sfa
     if x.dim() not in (2, 3):
@@ -298,7 +299,7 @@ def swiglu_quantize(x, *, plan=None, alpha=None, scale=1.0, a=None, sfa=None, st
     if x.shape[1] % 64:
         raise ValueError(f"the halves of a row must have a multiple of 32 elements (row of {x.shape[1]})")
     experts = 1 if plan is None else plan.experts
-    if plan is not None and (rows != plan.rows or plan.ids.device != device):
+    if plan is not None and (rows != plan.rows or plan.device != device):
         raise ValueError(f"x must have the plan's {plan.rows} rows, on its device")
     if alpha is not None:
         _like(alpha, "alpha", (experts,), torch.float32, device)
@@ -319,7 +320,7 @@ def dequantize(a, sfa, *, plan=None, dtype=torch.float16, out=None, stream=None)
         raise ValueError(f"a must have shape [m, k/2] (or, without a plan, [l, m, k/2]), not {tuple(a.shape)}")
     _like(a, "a", a.shape, torch.uint8, device)
     l, m, k = a.shape[0] if a.dim() == 3 else 1, a.shape[-2], 2 * a.shape[-1]
-    if plan is not None and (m != plan.rows or plan.ids.device != device):
+    if plan is not None and (m != plan.rows or plan.device != device):
         raise ValueError(f"a must have the plan's {plan.rows} rows, on its device")
     need = nvfp4_sf_bytes(m, k, l) if plan is None else c.nvfp4_moe_sf_bytes(m, plan.experts, k)
     _like(sfa, "sfa", (need,), torch.uint8, device)

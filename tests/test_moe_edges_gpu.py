@@ -63,3 +63,29 @@ def test_dispatch_takes_experts_from_rows(tokens, topk, experts, k, other):
     beyond = rng.choice(np.array([-1, -2 ** 31, slots, slots + 1, 2 ** 31 - 1]), ids.shape).astype(np.int32)
     dispatch(gpu(beyond))
     assert (a == 0xAB).all() and (store[:512] == 0xCD).all() and (store[512 + room:] == 0xCD).all()
+
+
+def test_a_plan_keeps_its_ids():
+    """What a plan was made from may be rewritten: by the next layer's routing, say."""
+    rng = rng_of(31)
+    ids = rng.integers(-1, 6, (50, 3)).astype(np.int32)
+    x = gpu(rng.standard_normal((150, 64)), torch.float16)
+    w, alpha = rng.standard_normal((50, 3)).astype(np.float32), rng.uniform(0.5, 2, 5).astype(np.float32)
+    buffer = gpu(ids)
+    p = moe.plan(buffer, 5)
+    buffer.copy_((buffer + 1).clamp(max=4))
+    rows = MO.plan(ids, 5)[2]
+    assert np.array_equal(p.ids.cpu().numpy(), np.where(ids < 5, ids, -1))
+    want, size = MO.combine(f64(x), w, rows, alpha, ids)
+    close(moe.combine(x, gpu(w), p, alpha=gpu(alpha), dtype=torch.float32), want, 6 * H[torch.float32] * size, torch.float32)
+    a, sfa = moe.quantize(x[:50], plan=p)
+    values = f64(moe.dequantize(a, sfa, plan=p))
+    codes, scales = MO.quantize(f64(x[:50]))
+    for t, j in zip(*np.nonzero(rows >= 0)):
+        assert np.array_equal(values[rows[t, j]], MO.values(codes[t:t + 1], scales[t:t + 1])[0])
+    dy = gpu(rng.standard_normal((50, 64)), torch.float32)
+    want, want_w, size = MO.combine_backward(f64(dy), f64(x), w, rows, alpha, ids)
+    dc, dw = moe.combine_backward(dy, x, gpu(w), p, alpha=gpu(alpha), dc=torch.zeros_like(x))
+    named = np.flatnonzero(~np.isnan(want).any(axis=1))
+    close(dc[gpu(named)], want[named], 3 * H[torch.float32] * np.abs(want[named]), torch.float16)
+    close(dw, want_w, 13 * H[torch.float32] * size, torch.float32)
