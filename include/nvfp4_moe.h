@@ -86,7 +86,8 @@ typedef struct nvfp4_moe_choice {
  * logit, and with softmax one of +inf, makes the weights of its token's chosen
  * experts NaN. A choice value of NaN or -inf
  * (through the bias) is never chosen either. A sum of scores that is 0 counts
- * as 1.
+ * as 1. Sums are those of the scores themselves, also where these lie below fp32's
+ * range; a sigmoid of a logit below -708 (2^-1021) counts as 0.
  *
  *   logits   device [tokens][experts] of `dtype`, rows `row_stride` elements apart; tokens < 2^26
  *   bias     device fp32 [experts], or NULL

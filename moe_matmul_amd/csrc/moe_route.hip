@@ -107,6 +107,18 @@ __device__ inline double inverse_f64(double d) {
   return fma(fma(-d, r, 1.0), r, r);
 }
 
+// sigmoid(x) / e^from = e^(x - from) / (1 + e^x) of logits x and from, both below 0
+// or from 0. For scores that leave fp32's range, while their ratios are ordinary
+// numbers: those renormalised by a sum of such scores, and those below kSmallLogit.
+// What the difference of the logits loses (half an ulp of up to 700) is put back,
+// and results below 2^-126 are kept (v_exp and v_rcp give 0). What is 0 in fp64 is 0.
+constexpr float kSmallLogit = -64.f, kLeastLogit = -708.f;
+__device__ inline float sigmoid_over_exp(float x, float from) {
+  const float d = x - from, lost = (x - d) - from, up = d < -80.f ? 0x1p64f : 1.f;
+  const float e = exp_f32(d, d < -80.f ? 64.f : 0.f);
+  return x >= kLeastLogit ? fmaf(e, lost, e) / ((1.f + exp_f32(x)) * up) : 0.f;
+}
+
 // ---- sorted lists in registers -------------------------------------------------
 template <class W> __device__ inline void order(typename W::Key& a, typename W::Key& b) {  // a the larger
   const typename W::Key x = W::larger(a, b), y = W::smaller(a, b);
@@ -538,12 +550,15 @@ __global__ void __launch_bounds__(kThreads, NC > 2 ? 2 : 4) nvfp4_moe_route_kern
     largest = fmaxf(largest, chosen[q]);
   }
   const int share = a.lanes < K ? a.lanes : K;  // lanes that have a slot
-  if (softmax && a.how.renormalize) top = max_across(largest, share);
+  if (a.how.renormalize) largest = max_across(largest, share);
+  if (softmax && a.how.renormalize) top = largest;
   const float from = top == -__builtin_inff() ? 0.f : top;
+  const float over = a.how.renormalize ? fminf(largest, 0.f) : 0.f;  // sigmoids are divided by e^over
   float sum = 0.f;
 #pragma unroll
   for (int q = 0; q < kLaneSlots; ++q) {
     if (softmax) w[q] = exp_f32(chosen[q] - from);
+    else if (over < 0.f || chosen[q] < kSmallLogit) w[q] = sigmoid_over_exp(chosen[q], over);
     else w[q] = ids[q] >= 0 ? __builtin_amdgcn_rcpf(1.f + exp_f32(-chosen[q])) : 0.f;
     sum += w[q];
   }
@@ -594,7 +609,8 @@ __device__ inline void store_share(void* row, const Share& s, bool vec, const fl
 // of the chosen scores and q = s / S:
 //   renormalised: ds = (dp - sum dp q) / S, else ds = dp
 //   softmax: dx = s (ds - sum ds s) (renormalised, the sum is 0 and dx = q (dp - sum dp q))
-//   sigmoid: dx = ds s (1 - s)
+//   sigmoid: dx = ds s (1 - s) (renormalised, dx = q (dp - sum dp q) (1 - s))
+// q is formed from scores over a common factor, so that S may lie below fp32's range.
 // Only the softmax that is not renormalised has a gradient for experts that
 // were not chosen, and only it reads the whole row. The chosen experts' values
 // go to their lanes through shared memory; every lane then writes its share.
@@ -644,19 +660,20 @@ __global__ void __launch_bounds__(kThreads) nvfp4_moe_route_backward_kernel(Rout
     from = max_across(chosen, a.lanes);
     p = id >= 0 ? exp_f32(chosen - (from == -__builtin_inff() ? 0.f : from)) : 0.f;
   } else {
-    p = id >= 0 ? 1.f / (1.f + exp_f32(-chosen)) : 0.f;
+    const float over = a.how.renormalize ? fminf(max_across(chosen, a.lanes), 0.f) : 0.f;
+    if (over < 0.f || chosen < kSmallLogit) p = sigmoid_over_exp(chosen, over);
+    else p = id >= 0 ? 1.f / (1.f + exp_f32(-chosen)) : 0.f;
   }
-  float total = 1.f, q = p;
+  float q = p;
   if (a.how.renormalize) {
-    total = sum_across(p, a.lanes);
-    total = total == 0.f ? 1.f : total;
-    q = p / total;
+    const float total = sum_across(p, a.lanes);
+    q = total == 0.f ? 0.f : p / total;
   }
   const float dot = sum_across(id >= 0 ? dw * q : 0.f, a.lanes);
   float give;  // to the chosen expert's lane
   if (dense) give = dw;
   else if (softmax) give = q * (dw - dot);
-  else give = (a.how.renormalize ? (dw - dot) / total : dw) * p * (1.f / (1.f + exp_f32(chosen)));
+  else give = q * (dw - (a.how.renormalize ? dot : 0.f)) * (1.f / (1.f + exp_f32(chosen)));
   __syncthreads();
   if (id >= 0) {
     const int chunk = id / 8, owner = (threadIdx.x & ~(a.lanes - 1)) + (chunk & (a.lanes - 1));

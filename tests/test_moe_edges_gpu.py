@@ -89,3 +89,57 @@ def test_a_plan_keeps_its_ids():
     named = np.flatnonzero(~np.isnan(want).any(axis=1))
     close(dc[gpu(named)], want[named], 3 * H[torch.float32] * np.abs(want[named]), torch.float16)
     close(dw, want_w, 13 * H[torch.float32] * size, torch.float32)
+
+
+# ---- sigmoid scores that leave fp32 ------------------------------------------------
+
+@pytest.mark.parametrize("topk", [1, 2, 8, 13])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_sigmoid_renormalised_far_below_zero(dtype, topk):
+    """Logits of -80 .. -120, where sigmoids are denormal or 0 in fp32, of -700, and mixed with ordinary ones."""
+    rng = rng_of(topk, 80)
+    x = rng.uniform(-120, -80, (96, 16))
+    x[1::4] = rng.uniform(-95, -2, (24, 16))          # some of a token below 2^-126
+    x[2::4] = rng.uniform(-700, -600, (24, 16))
+    x[3::4] = rng.uniform(-100, 3, (24, 16))
+    x[0] = -90.0
+    x[4, 3:] = -np.inf
+    x[5, 1:] = -np.inf
+    x[8, :2] = -90.0, -91.0
+    x[8, 2:] = -110.0
+    x = gpu(x, TYPES[dtype])
+    how = dict(score="sigmoid", scale=2.5)
+    for bias in (None, gpu(np.zeros(16, dtype=np.float32))):
+        ids, w = moe.route(x, topk, bias=bias, **how)
+        want_ids, want_w = MO.route(f64(x), topk, **how)
+        if bias is None:
+            assert np.array_equal(ids.cpu().numpy(), want_ids)
+        else:  # scores this small count as equal beside a bias: weights of what was chosen
+            s = np.take_along_axis(MO.scores(f64(x), "sigmoid"), np.maximum(ids.cpu().numpy(), 0).astype(np.int64), 1)
+            s = np.where(ids.cpu().numpy() >= 0, s, 0)
+            want_w = 2.5 * s / s.sum(1, keepdims=True)
+        close(w, want_w, 64 * H[torch.float32] * want_w, torch.float32)
+    if topk == 2:
+        assert abs(float(w[8].sum()) - 2.5) < 1e-5 and abs(float(w[8, 0]) / 2.5 - 0.7310586) < 1e-5
+    ids, _ = moe.route(x, topk, **how)
+    dw = gpu(rng.standard_normal((96, topk)).astype(np.float32) * 4)
+    d = moe.route_backward(x, ids, dw, **how)
+    want, size = MO.route_backward(f64(x), ids.cpu().numpy(), f64(dw), **how)
+    close(d, want, 256 * H[torch.float32] * size, x.dtype)
+
+
+def test_sigmoid_renormalised_gradient_against_differences():
+    """Of the kernel's own forward pass, at logits around -90."""
+    x = -90 + torch.arange(12, device="cuda").float().view(1, 12).mul(0.37).sin().mul(3).repeat(24, 1)
+    dw = torch.randn(1, 5, device="cuda", generator=torch.Generator("cuda").manual_seed(2)).repeat(24, 1)
+    h = 2.0 ** -7
+    step = torch.cat((torch.eye(12), -torch.eye(12))).cuda() * h
+    ids, w = moe.route(x + step, 5, score="sigmoid", scale=1.5)
+    assert (ids == ids[0]).all()
+    loss = (w.double() * dw.double()).sum(1)
+    diff = (loss[:12] - loss[12:]) / (2 * h)
+    d = moe.route_backward(x[:1].contiguous(), ids[:1].contiguous(), dw[:1].contiguous(), score="sigmoid", scale=1.5)
+    # h^2 / 6 of the third derivative (below 8 times the weights' size), and 64 H of the weights over h
+    size = float(dw[0].abs().sum()) * 1.5
+    assert float(d.abs().max()) > 0.01
+    assert float((d[0].double() - diff).abs().max()) < h * h / 6 * size * 8 + 64 * 2.0 ** -24 * size * 2 / h
