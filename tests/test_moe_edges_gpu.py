@@ -143,3 +143,100 @@ def test_sigmoid_renormalised_gradient_against_differences():
     size = float(dw[0].abs().sum()) * 1.5
     assert float(d.abs().max()) > 0.01
     assert float((d[0].double() - diff).abs().max()) < h * h / 6 * size * 8 + 64 * 2.0 ** -24 * size * 2 / h
+
+
+# ---- the layer ---------------------------------------------------------------------
+
+def layer_of(tokens, experts, hidden, inner, dtype, low=0x18, high=0x20, alpha1=None, alpha2=None, **how):
+    rng = rng_of(tokens, experts, hidden, inner)
+    b1, sfb1, w1 = operand(rng, experts, 2 * inner, hidden, low, high)
+    b2, sfb2, w2 = operand(rng, experts, hidden, inner, low, high)
+    x = gpu(rng.standard_normal((tokens, hidden)), TYPES[dtype])
+    layer = moe.FeedForward(b1, sfb1, b2, sfb2, alpha1=None if alpha1 is None else gpu(alpha1),
+                            alpha2=None if alpha2 is None else gpu(alpha2), **how)
+    return layer, w1, w2, x
+
+
+def layer_reference(layer, x, ids, w, w1, w2, quantized, alpha1=None, alpha2=None, scale1=1.0, scale2=1.0):
+    """The layer by its steps' definitions. Products of the grouped form are rounded to fp16 and divided by the rows'
+    factor afterwards."""
+    xn, y = f64(x), np.zeros((x.shape[0], x.shape[1]))
+    one = np.ones(w1.shape[0], dtype=np.float32)
+    alpha1, alpha2 = one if alpha1 is None else alpha1, one if alpha2 is None else alpha2
+    nv = lambda v: MO.values(*MO.quantize(v)) if quantized else v  # noqa: E731
+    half = lambda v: v.astype(np.float16).astype(np.float64) if quantized else v  # noqa: E731
+    rows = nv((xn * scale1).astype(np.float32)) if quantized else xn
+    s1, s2 = (scale1, scale2) if quantized else (1.0, 1.0)
+    for e in range(w1.shape[0]):
+        t, j = np.nonzero(ids == e)
+        if t.size:
+            h = MO.swiglu(half(rows[t] @ w1[e].T), float(alpha1[e]) / s1, s2)
+            np.add.at(y, t, w[t, j].astype(np.float64)[:, None] * float(alpha2[e]) / s2 * half(nv(h) @ w2[e].T))
+    return y
+
+
+def near(got, want):
+    """Every step's own error is tested with the step; where a product's last bit differs, a code next to a border may,
+    by a third of its value at most: the few that do keep the relative norm below 2^-6."""
+    got = f64(got)
+    assert np.isfinite(got).all()
+    assert np.linalg.norm(got - want) <= 2.0 ** -6 * np.linalg.norm(want)
+
+
+@pytest.mark.parametrize("tokens,experts,topk,hidden,inner,dtype", [
+    (2, 5, 2, 256, 128, "fp16"), (70, 5, 2, 256, 128, "fp32"), (300, 7, 3, 512, 96, "bf16"), (600, 40, 4, 256, 64, "bf16"),
+    (90, 160, 6, 128, 64, "fp32"), (130, 300, 8, 128, 64, "fp16")])
+def test_layer_with_factors(tokens, experts, topk, hidden, inner, dtype):
+    """Factors that differ from expert to expert and between the products, in both forms, and in what a call chooses."""
+    rng = rng_of(tokens, experts, 5)
+    alpha1, alpha2 = rng.uniform(0.25, 1.5, experts).astype(np.float32), rng.uniform(0.125, 2, experts).astype(np.float32)
+    layer, w1, w2, x = layer_of(tokens, experts, hidden, inner, dtype, alpha1=alpha1, alpha2=alpha2)
+    ids, w = moe.route(gpu(rng.standard_normal((tokens, experts)), torch.float32), topk)
+    idn, wn = ids.cpu().numpy(), f64(w)
+    few = tokens * topk <= 3 * experts and dtype != "fp32"
+    for run, quantized in ((layer.grouped, True), (layer, not few)) + (((layer.few, False),) if dtype != "fp32" else ()):
+        residual = torch.randn_like(x)
+        want = layer_reference(layer, x, idn, wn, w1, w2, quantized, alpha1, alpha2)
+        near(run(x, ids, w), want)
+        near(run(x, ids, w, residual=residual), want + f64(residual))
+
+
+@pytest.mark.parametrize("rows,experts,hidden,inner,tiles", [
+    (4, 32, 2048, 64, (2, 1)), (4, 32, 256, 1024, (1, 2)), (100, 4, 2048, 64, (2, 2)), (100, 32, 256, 1024, (0, 2)),
+    (256, 32, 2048, 64, (2, 0))])
+def test_layer_by_every_tile(rows, experts, hidden, inner, tiles):
+    """Layers whose products take each of the tile configurations that the layer chooses from."""
+    layer, w1, w2, x = layer_of(rows * experts // 2, experts, hidden, inner, "bf16")
+    slots = rows * experts
+    assert (layer._tile(slots, 2 * inner), layer._tile(slots, hidden)) == tiles
+    ids = np.argsort(rng_of(rows, 3).random((x.shape[0], experts)), axis=1)[:, :2].astype(np.int32)
+    w = rng_of(rows, 4).uniform(0.1, 1, ids.shape).astype(np.float32)
+    y = layer.grouped(x, gpu(ids), gpu(w))
+    some = np.unique(np.concatenate(([0, 1, x.shape[0] - 1], rng_of(rows, 5).integers(0, x.shape[0], 60))))
+    near(y[gpu(some)], layer_reference(layer, x[gpu(some)], ids[some], w[some], w1, w2, True))
+    assert torch.equal(y, layer.grouped(x, gpu(ids), gpu(w)))
+
+
+def test_product_after_a_plan():
+    """The grouped GEMM by the public way: dispatch, a plan with its product, run."""
+    rng = rng_of(55)
+    b, sfb, w = operand(rng, 5, 136, 192)
+    x = gpu(rng.standard_normal((90, 192)), torch.float16)
+    ids = rng.integers(-1, 6, (90, 2)).astype(np.int32)
+    a = torch.empty(180, 96, dtype=torch.uint8, device="cuda")
+    sfa = torch.empty(c.nvfp4_moe_sf_bytes(180, 5, 192), dtype=torch.uint8, device="cuda")
+    out = torch.full((180, 136), 7.0, dtype=torch.float16, device="cuda")
+    status = torch.full((1,), -1, dtype=torch.int32, device="cuda")
+    q = moe.Product(a, sfa, b, sfb, out)
+    p = moe.plan(gpu(ids), 5, (q,))
+    moe.quantize(x, plan=p, a=a, sfa=sfa)
+    values = MO.values(*MO.quantize(f64(x)))
+    rows = MO.plan(ids, 5)[2]
+    for config in (-1, 0, 1, 2, 3, 4):
+        out.fill_(7.0)
+        assert q.run(config, status) is out and int(status) == 0
+        got = f64(out)
+        for t, j in zip(*np.nonzero(rows >= 0)):
+            want, size = w[ids[t, j]] @ values[t], np.abs(w[ids[t, j]]) @ np.abs(values[t])
+            assert (np.abs(got[rows[t, j]] - want) <= 1e-5 * size + 2 * 2.0 ** -11 * np.abs(want)).all()
+        assert (got[int((rows >= 0).sum()):] == 7).all()
