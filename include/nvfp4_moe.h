@@ -211,9 +211,9 @@ int nvfp4_moe_dequantize(const void* a, const void* sfa, int l, int64_t m, int k
  *   c          device [c_rows][n] of c_dtype (fp16 or bf16 or fp32), rows c_stride apart
  *   slot_rows  NULL: the row of a slot is the slot (then c_rows >= tokens*topk)
  *   weights    fp32 [tokens][topk], NULL: 1
- *   alpha      fp32 [experts], NULL: 1 (and experts is not looked at); needs ids
- *   ids        int32 [tokens][topk]; where given, a slot whose id is negative, or with alpha not below experts, adds
- *              nothing
+ *   alpha      fp32 [experts], NULL: 1; needs ids
+ *   ids        int32 [tokens][topk]; where given, a slot whose id is not in 0 .. experts - 1 adds nothing
+ *   experts    their number; without alpha it may be 0 or less: then no id is too large
  *   residual   [tokens][n] of out_dtype, rows out_stride apart, or NULL
  *   out        [tokens][n] of out_dtype, rows out_stride apart
  */

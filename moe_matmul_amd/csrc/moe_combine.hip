@@ -183,7 +183,7 @@ int nvfp4_moe_combine(const void* c, int c_dtype, int64_t c_stride, int64_t c_ro
   a.out_stride = out_stride;
   a.slot_rows = slot_rows;
   a.ids = ids;
-  a.experts = alpha == nullptr ? INT32_MAX : experts;
+  a.experts = alpha == nullptr && experts <= 0 ? INT32_MAX : experts;
   a.weights = weights;
   a.alpha = alpha;
   a.residual = residual;
@@ -225,7 +225,7 @@ int nvfp4_moe_combine_backward(const void* dy, int dy_dtype, int64_t dy_stride, 
   a.dy_stride = dy_stride;
   a.slot_rows = slot_rows;
   a.ids = ids;
-  a.experts = alpha == nullptr ? INT32_MAX : experts;
+  a.experts = alpha == nullptr && experts <= 0 ? INT32_MAX : experts;
   a.weights = weights;
   a.alpha = alpha;
   a.dc = dc;

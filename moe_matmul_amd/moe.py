@@ -336,8 +336,9 @@ def dequantize(a, sfa, *, plan=None, dtype=torch.float16, out=None, stream=None)
 
 # ---- the combine ----------------------------------------------------------------------
 
-def _slots(weights, rows, alpha, ids, slots_of, device):
-    """Checked (tokens, topk, row address, ids) of a combine's slots; ``rows`` a Plan, a tensor or None."""
+def _slots(weights, rows, alpha, ids, experts, slots_of, device):
+    """Checked (tokens, topk, rows, ids, number of experts or 0) of a combine's slots; ``rows`` a Plan, a tensor or
+    None."""
     if isinstance(rows, Plan):
         ids, rows = rows.ids, rows.slot_rows
     given = weights if weights is not None else rows
@@ -356,38 +357,44 @@ def _slots(weights, rows, alpha, ids, slots_of, device):
         if ids is None:
             raise ValueError("alpha needs ids")
         _like(alpha, "alpha", (alpha.shape[0],), torch.float32, device)
-    return shape[0], shape[1], rows, ids
+        if experts is not None and experts != alpha.shape[0]:
+            raise ValueError(f"alpha has {alpha.shape[0]} experts, not {experts}")
+        experts = alpha.shape[0]
+    elif experts is not None and (ids is None or experts < 1):
+        raise ValueError("experts needs ids, and at least one expert")
+    return shape[0], shape[1], rows, ids, experts or 0
 
 
 @_on_stream
-def combine(x, weights, rows=None, *, alpha=None, ids=None, residual=None, dtype=None, out=None, stream=None):
+def combine(x, weights, rows=None, *, alpha=None, ids=None, experts=None, residual=None, dtype=None, out=None, stream=None):
     """``out[t] = residual[t] + sum_j weights[t, j] * alpha[ids[t, j]] * x[rows[t, j]]``, summed in fp32 in slot order.
 
     ``x`` [rows, n]: the experts' rows; ``rows``: a Plan, int32 [tokens, topk] (-1: no row), or None where the slots'
-    rows follow each other; ``weights`` fp32 [tokens, topk] or None for 1. ``dtype`` of the result: that of ``out``
-    or ``residual``, else x's."""
+    rows follow each other; ``weights`` fp32 [tokens, topk] or None for 1. Slots whose id is below 0, or not below the
+    number of ``experts`` (that of ``alpha`` where there is one, else any), add nothing, whatever their weight holds.
+    ``dtype`` of the result: that of ``out`` or ``residual``, else x's."""
     device = _gpu(x, "x")
     stride = _rows(x, "x")
     n = x.shape[1]
-    tokens, topk, rows, ids = _slots(weights, rows, alpha, ids, x, device)
+    tokens, topk, rows, ids, experts = _slots(weights, rows, alpha, ids, experts, x, device)
     if dtype is None:
         dtype = out.dtype if out is not None else residual.dtype if residual is not None else x.dtype
     out = _out(out, "out", (tokens, n), dtype, device)
     if residual is not None:
         _like(residual, "residual", (tokens, n), dtype, device)
     _enqueue(c.nvfp4_moe_combine, device, x.data_ptr(), _type(x, "x"), stride, x.shape[0], tokens, topk, n,
-             _at(rows), _at(weights), _at(alpha), _at(ids), 0 if alpha is None else alpha.shape[0], _at(residual),
+             _at(rows), _at(weights), _at(alpha), _at(ids), experts, _at(residual),
              out.data_ptr(), _type(out, "out"), n)
     return out
 
 
 @_on_stream
-def combine_backward(dy, x, weights, rows=None, *, alpha=None, ids=None, dc=None, stream=None):
+def combine_backward(dy, x, weights, rows=None, *, alpha=None, ids=None, experts=None, dc=None, stream=None):
     """(d x, d weights) of ``combine``; rows of d x that no slot has are not written, those of slots without an
     expert are 0."""
     device = _gpu(x, "x")
     stride = _rows(x, "x")
-    tokens, topk, rows, ids = _slots(weights, rows, alpha, ids, x, device)
+    tokens, topk, rows, ids, experts = _slots(weights, rows, alpha, ids, experts, x, device)
     dy_stride = _rows(dy, "dy", x.shape[1])
     if dy.shape[0] != tokens or dy.device != device:
         raise ValueError(f"dy must have {tokens} rows, on {device}")
@@ -398,7 +405,7 @@ def combine_backward(dy, x, weights, rows=None, *, alpha=None, ids=None, dc=None
     dweights = torch.empty((tokens, topk), dtype=torch.float32, device=device)
     _enqueue(c.nvfp4_moe_combine_backward, device, dy.data_ptr(), _type(dy, "dy"), dy_stride, x.data_ptr(),
              _type(x, "x"), stride, x.shape[0], tokens, topk, x.shape[1], _at(rows), _at(weights), _at(alpha), _at(ids),
-             0 if alpha is None else alpha.shape[0], dc.data_ptr(), dweights.data_ptr())
+             experts, dc.data_ptr(), dweights.data_ptr())
     return dc, dweights
 
 
@@ -491,7 +498,7 @@ class FeedForward:
         """By the products of few tokens, with ``x`` (fp16 or bf16) as it is."""
         h = few_tokens(x, ids, self.b1, self.sfb1, alpha=self.alpha1, swiglu=True)
         y = few_tokens(h, ids, self.b2, self.sfb2, alpha=self.alpha2)
-        return combine(y.view(-1, self.hidden), weights, ids=ids, residual=residual, dtype=x.dtype)
+        return combine(y.view(-1, self.hidden), weights, ids=ids, experts=self.experts, residual=residual, dtype=x.dtype)
 
     @_on_stream
     def grouped(self, x, ids, weights, *, residual=None, stream=None):

@@ -240,3 +240,35 @@ def test_product_after_a_plan():
             want, size = w[ids[t, j]] @ values[t], np.abs(w[ids[t, j]]) @ np.abs(values[t])
             assert (np.abs(got[rows[t, j]] - want) <= 1e-5 * size + 2 * 2.0 ** -11 * np.abs(want)).all()
         assert (got[int((rows >= 0).sum()):] == 7).all()
+
+
+# ---- slots without an expert -------------------------------------------------------
+
+def test_combine_takes_the_number_of_experts():
+    """Without factors, too, a slot whose id is none of the experts' adds nothing and gets gradients of 0."""
+    x = torch.randn(8, 72, device="cuda")
+    ids = torch.tensor([[0, 3, 1, -1], [2, 2 ** 31 - 1, -2 ** 31, 5]], dtype=torch.int32, device="cuda")
+    nan, inf = float("nan"), float("inf")
+    w = torch.tensor([[0.5, nan, 1.0, inf], [2.0, nan, inf, nan]], device="cuda")
+    f = f64(x)
+    want = np.stack([0.5 * f[0] + f[2], 2 * f[4]])
+    close(moe.combine(x, w, ids=ids, experts=3), want, 6 * H[torch.float32] * 2 * np.abs(f).max(), torch.float32)
+    dy = torch.ones(2, 72, device="cuda")
+    dc, dw = moe.combine_backward(dy, x, w, ids=ids, experts=3, dc=torch.full_like(x, 9.0))
+    assert (dc[[1, 3, 5, 6, 7]] == 0).all() and (dc[0] == 0.5).all() and (dc[2] == 1).all() and (dc[4] == 2).all()
+    assert (dw[[0, 0, 1, 1, 1], [1, 3, 1, 2, 3]] == 0).all() and torch.isfinite(dw).all()
+
+
+@pytest.mark.parametrize("tokens", [3, 40])
+def test_layer_slots_without_an_expert(tokens):
+    """Both forms: ids below 0 and beyond the experts, whose weights are NaN or infinite."""
+    layer, w1, w2, x = layer_of(tokens, 6, 256, 128, "bf16")
+    rng = rng_of(tokens, 77)
+    ids = rng.integers(0, 6, (tokens, 3)).astype(np.int32)
+    bad = rng.random(ids.shape) < 0.4
+    ids[bad] = rng.choice(np.array([-1, 6, 7, 2 ** 31 - 1, -2 ** 31]), int(bad.sum()))
+    w = rng.uniform(0.1, 1, ids.shape).astype(np.float32)
+    w[bad] = rng.choice(np.array([np.nan, np.inf, -np.inf, 1.0], dtype=np.float32), int(bad.sum()))
+    ids[0], w[0] = 6, np.nan                          # a token without any
+    for run, quantized in ((layer.grouped, True), (layer.few, False), (layer, tokens * 3 > 18)):
+        near(run(x, gpu(ids), gpu(w)), layer_reference(layer, x, ids, w, w1, w2, quantized))
