@@ -468,14 +468,24 @@ class FeedForward:
     ``y[t] = sum_j w[t, j] * down[e] . (silu(gate[e] . x[t]) * (up[e] . x[t]))``, e = ids[t, j].
 
     ``b1``, ``sfb1``: gate rows, then up rows, [experts, 2 * inner, hidden / 2]; ``b2``, ``sfb2``: [experts, hidden,
-    inner / 2]; ``alpha1``, ``alpha2``: factors on each expert's products (fp32 [experts])."""
+    inner / 2]; ``alpha1``, ``alpha2``: factors on each expert's products (fp32 [experts]), as weights that were
+    quantised under a factor of their own need them.
+
+    ``scale1``, ``scale2`` are factors on the rows and on the activations before ``grouped`` quantises them; it takes
+    them out again with the products' factors (``alpha1 / scale1`` and ``alpha2 / scale2`` are formed here, once, where
+    a scale is not 1; powers of two lose nothing). They keep two things in range, which differ from weights to weights
+    and which nothing checks: the grouped GEMM writes its products, without ``alpha``, in fp16, so ``scale * y / alpha``
+    has to stay below 65504 (beyond, the layer gives infinities and NaN); and what is quantised keeps its 4 bits from
+    about 0.1 (a block's largest element; below 0.006 it is 0) to 2688 (beyond, it is 2688). ``few`` quantises neither
+    and needs no scale. Weights whose block scales go up to 448 have an alpha of about their largest entry / 2688: with
+    entries up to 0.1, a scale of 1 holds for y up to 2.4, one of 1/16 up to 39."""
 
     #: Up to this many slots an expert the products of few tokens are faster than the grouped ones (8 experts of
     #: 7168x2048, 2 and 4 slots an expert: 70 and 88 us against 78 both times; 64 of 4096x1024: 104 and 139 against 127
     #: and 131).
     FEW_ROWS = 3
 
-    def __init__(self, b1, sfb1, b2, sfb2, *, alpha1=None, alpha2=None):
+    def __init__(self, b1, sfb1, b2, sfb2, *, alpha1=None, alpha2=None, scale1=1.0, scale2=1.0):
         (self.b1, self.sfb1), (self.b2, self.sfb2) = _operand(b1, sfb1), _operand(b2, sfb2)
         self.experts, self.hidden, self.inner = b1.shape[0], 2 * b1.shape[2], 2 * b2.shape[2]
         if tuple(b1.shape[:2]) != (b2.shape[0], 2 * self.inner) or b2.shape[1] != self.hidden or b1.device != b2.device:
@@ -483,8 +493,22 @@ class FeedForward:
         for name, alpha in (("alpha1", alpha1), ("alpha2", alpha2)):
             if alpha is not None:
                 _like(alpha, name, (self.experts,), torch.float32, b1.device)
-        self.alpha1, self.alpha2 = alpha1, alpha2
+        for name, scale in (("scale1", scale1), ("scale2", scale2)):
+            if not 2.0 ** -126 <= scale <= 2.0 ** 126:
+                raise ValueError(f"{name} must be a positive number within fp32's range, not {scale}")
+        self.alpha1, self.alpha2, self.scale1, self.scale2 = alpha1, alpha2, float(scale1), float(scale2)
+        # the grouped products' own factors
+        self._gain1, self._gain2 = self._gain(alpha1, scale1), self._gain(alpha2, scale2)
+        if scale1 != 1 or scale2 != 1:
+            torch.cuda.current_stream(b1.device).synchronize()  # calls on any stream find them made
         self.units = torch.cuda.get_device_properties(b1.device).multi_processor_count
+
+    def _gain(self, alpha, scale):
+        """alpha / scale, in fp32 (None for 1)."""
+        if scale == 1:
+            return alpha
+        one = torch.ones(self.experts, dtype=torch.float32, device=self.b1.device) if alpha is None else alpha
+        return one / torch.full_like(one, scale)
 
     def __call__(self, x, ids, weights, *, residual=None, stream=None):
         """y [tokens, hidden] of ``x``'s type, by the products that suit the number of tokens."""
@@ -528,14 +552,14 @@ class FeedForward:
         def enqueue(stream):
             c.nvfp4_moe_plan(ids_at, tokens, topk, e, offsets, atoms, slot_rows, row_slots, products, 2, plan_room,
                              plan_bytes, stream)
-            c.nvfp4_moe_dispatch(x.data_ptr(), kind, tokens, topk, hidden, stride, 1.0, ids_at, slot_rows, row_slots,
+            c.nvfp4_moe_dispatch(x.data_ptr(), kind, tokens, topk, hidden, stride, self.scale1, ids_at, slot_rows, row_slots,
                                  offsets, atoms, e, a1, sf1, dispatch_room, dispatch_bytes, stream)
             nvfp4_grouped_gemm_device(sizes1, abc1, scales1, e, self._tile(rows, 2 * inner), 0, stream)
-            c.nvfp4_moe_swiglu(c1, c.NVFP4_MOE_F16, rows, inner, 2 * inner, _at(self.alpha1), 1.0, offsets, atoms, e, a2,
-                               sf2, stream)
+            c.nvfp4_moe_swiglu(c1, c.NVFP4_MOE_F16, rows, inner, 2 * inner, _at(self._gain1), self.scale2, offsets, atoms, e,
+                               a2, sf2, stream)
             nvfp4_grouped_gemm_device(sizes2, abc2, scales2, e, self._tile(rows, hidden), 0, stream)
             c.nvfp4_moe_combine(c2, c.NVFP4_MOE_F16, hidden, rows, tokens, topk, hidden, slot_rows, weights.data_ptr(),
-                                _at(self.alpha2), ids_at, e, _at(residual), out.data_ptr(), kind, hidden, stream)
+                                _at(self._gain2), ids_at, e, _at(residual), out.data_ptr(), kind, hidden, stream)
         _enqueue(enqueue, device)
         return out
 

@@ -272,3 +272,39 @@ def test_layer_slots_without_an_expert(tokens):
     ids[0], w[0] = 6, np.nan                          # a token without any
     for run, quantized in ((layer.grouped, True), (layer.few, False), (layer, tokens * 3 > 18)):
         near(run(x, gpu(ids), gpu(w)), layer_reference(layer, x, ids, w, w1, w2, quantized))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_layer_whose_products_need_a_factor_on_their_rows(dtype):
+    """Block scales near 448 and a factor of a weight tensor, as checkpoints have them: products of rows as they are leave
+    fp16. Factors on the rows that bring them back leave the layer's two forms the same function."""
+    rng = rng_of(8)
+    alpha1, alpha2 = rng.uniform(2e-5, 6e-5, 6).astype(np.float32), rng.uniform(2e-5, 6e-5, 6).astype(np.float32)
+    scales = dict(scale1=2.0 ** -4, scale2=2.0 ** -2)
+    layer, w1, w2, x = layer_of(64, 6, 512, 256, dtype, low=0x60, high=0x7F, alpha1=alpha1, alpha2=alpha2, **scales)
+    ids = rng.integers(0, 6, (64, 2)).astype(np.int32)
+    w = rng.uniform(0.1, 1, ids.shape).astype(np.float32)
+    x *= 3
+    plain = moe.FeedForward(layer.b1, layer.sfb1, layer.b2, layer.sfb2, alpha1=gpu(alpha1), alpha2=gpu(alpha2))
+    assert not torch.isfinite(plain.grouped(x, gpu(ids), gpu(w))).all()
+    want = layer_reference(layer, x, ids, w, w1, w2, True, alpha1, alpha2, **scales)
+    near(layer.grouped(x, gpu(ids), gpu(w)), want)
+    if dtype != "fp32":
+        few = layer_reference(layer, x, ids, w, w1, w2, False, alpha1, alpha2)
+        near(layer.few(x, gpu(ids), gpu(w)), few)
+        # rows, weights' products and activations in 4 bits against 16: a sixth of each value at most
+        assert np.linalg.norm(want - few) < 0.25 * np.linalg.norm(few)
+
+
+def test_layer_factors_of_rows_alone():
+    """Without the experts' factors, and of a factor that is no power of two."""
+    scales = dict(scale1=24.0, scale2=0.3)
+    layer, w1, w2, x = layer_of(50, 4, 256, 96, "bf16", **scales)
+    rng = rng_of(9)
+    ids = rng.integers(0, 4, (50, 2)).astype(np.int32)
+    w = rng.uniform(0.1, 1, ids.shape).astype(np.float32)
+    near(layer.grouped(x, gpu(ids), gpu(w)), layer_reference(layer, x, ids, w, w1, w2, True, **scales))
+    near(layer.few(x, gpu(ids), gpu(w)), layer_reference(layer, x, ids, w, w1, w2, False))
+    for bad in (0.0, -1.0, float("nan"), float("inf"), 1e39, 1e-46):
+        with pytest.raises(ValueError, match="scale"):
+            moe.FeedForward(layer.b1, layer.sfb1, layer.b2, layer.sfb2, scale2=bad)
