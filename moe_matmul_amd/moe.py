@@ -21,7 +21,7 @@ import functools
 import torch
 
 from . import _moe_binding as c
-from ._binding import nvfp4_grouped_gemm_device, nvfp4_sf_bytes
+from ._binding import nvfp4_device_group_tiles, nvfp4_grouped_gemm_device, nvfp4_sf_bytes
 
 _TYPES = {torch.float32: c.NVFP4_MOE_F32, torch.float16: c.NVFP4_MOE_F16, torch.bfloat16: c.NVFP4_MOE_BF16}
 _SCORES = {"softmax": c.NVFP4_MOE_SOFTMAX, "sigmoid": c.NVFP4_MOE_SIGMOID}
@@ -160,6 +160,23 @@ def route_backward(logits, ids, dweights, *, score="softmax", renormalize=True, 
 
 # ---- the plan --------------------------------------------------------------------
 
+def _group_fits(m, n, k):
+    """Whether the grouped GEMM takes a group of that size (else it leaves its rows as they are)."""
+    return m < 1 << 31 and nvfp4_device_group_tiles((m, n, k, 1), (4096,) * 5) >= 0
+
+
+@functools.lru_cache(maxsize=1024)
+def _most_rows(n, k):
+    """The most rows that a group of n columns and k elements can have: 2^31 bytes of codes, as a rule."""
+    low, high = 0, 1 << 30
+    if not _group_fits(1, n, k):
+        raise ValueError(f"the grouped GEMM does not take weights of {n} x {k}")
+    while low < high:
+        mid = (low + high + 1) // 2
+        low, high = (mid, high) if _group_fits(mid, n, k) else (low, mid - 1)
+    return low
+
+
 class Product:
     """A grouped product over rows sorted by expert, ``c[row] = a[row] . b[expert]``, and the group tables that
     ``plan`` fills for ``nvfp4_grouped_gemm_device``."""
@@ -185,9 +202,15 @@ class Product:
 
     @_on_stream
     def run(self, tile_config=-1, status=None, *, stream=None):
-        """Enqueue the product, after a ``plan`` that this one was given to."""
+        """Enqueue the product, after a ``plan`` that this one was given to.
+
+        An expert with more rows than the grouped GEMM takes in a group (2^31 bytes of codes) has no result. Where there
+        are so many rows in all, ``status`` (int32 [1]) says how many such experts there are, their rows left as they
+        were; without it their rows are NaN."""
         if not self.planned:
             raise ValueError("no plan has filled this product's tables")
+        if status is None and self.a.shape[0] > _most_rows(self.n, self.k):
+            self.out.fill_(float("nan"))
         _enqueue(nvfp4_grouped_gemm_device, self.device, *self.tables, self.experts, tile_config,
                  _at(status))
         return self.out
@@ -528,9 +551,10 @@ class FeedForward:
     def grouped(self, x, ids, weights, *, residual=None, stream=None):
         """By the grouped GEMM, on rows and activations quantised to NVFP4. The operators are enqueued with addresses
         in one workspace: a small layer takes the host longer than the GPU (64 tokens on 16 experts of 2048x1024, with
-        their routing: 87 us with tensors made and checked operator by operator, 48 like this)."""
-        device, e, hidden, inner = _gpu(x, "x"), self.experts, self.hidden, self.inner
-        kind, stride = _type(x, "x"), _rows(x, "x", hidden)
+        their routing: 87 us with tensors made and checked operator by operator, 48 like this). More tokens than a group of
+        the grouped GEMM is sure to hold (2^31 bytes of codes: 599186 rows of 7168) are taken in parts."""
+        device, hidden = _gpu(x, "x"), self.hidden
+        layout = _type(x, "x"), _rows(x, "x", hidden)
         if device != self.b1.device:
             raise ValueError(f"x must be on {self.b1.device}")
         tokens, topk = x.shape[0], ids.shape[-1]
@@ -538,10 +562,26 @@ class FeedForward:
         _like(weights, "weights", (tokens, topk), torch.float32, device)
         if residual is not None:
             _like(residual, "residual", (tokens, hidden), x.dtype, device)
+        out = torch.empty((tokens, hidden), dtype=x.dtype, device=device)
+        most = self._most_tokens(topk)
+        if tokens <= most:
+            self._grouped(x, layout, ids, weights, residual, out)
+        else:
+            for part in (slice(i, i + most) for i in range(0, tokens, most)):
+                self._grouped(x[part], layout, ids[part], weights[part], None if residual is None else residual[part],
+                              out[part])
+        return out
+
+    def _most_tokens(self, topk):
+        """The most tokens whose rows fit the grouped GEMM's groups, were they all one expert's."""
+        return max(1, min(_most_rows(2 * self.inner, self.hidden), _most_rows(self.hidden, self.inner)) // max(topk, 1))
+
+    def _grouped(self, x, layout, ids, weights, residual, out):
+        device, e, hidden, inner = x.device, self.experts, self.hidden, self.inner
+        (kind, stride), (tokens, topk) = layout, ids.shape
         rows = tokens * topk
         places, size, plan_bytes, dispatch_bytes = _layer_room(tokens, topk, e, hidden, inner)
         room = torch.empty(size, dtype=torch.uint8, device=device)
-        out = torch.empty((tokens, hidden), dtype=x.dtype, device=device)
         base, ids_at = room.data_ptr(), ids.data_ptr()
         (offsets, atoms, slot_rows, row_slots, plan_room, dispatch_room, a1, sf1, c1, a2, sf2, c2, sizes1, abc1, scales1,
          sizes2, abc2, scales2) = [base + p for p in places]
@@ -561,7 +601,6 @@ class FeedForward:
             c.nvfp4_moe_combine(c2, c.NVFP4_MOE_F16, hidden, rows, tokens, topk, hidden, slot_rows, weights.data_ptr(),
                                 _at(self._gain2), ids_at, e, _at(residual), out.data_ptr(), kind, hidden, stream)
         _enqueue(enqueue, device)
-        return out
 
     def _tile(self, rows, n):
         """The grouped GEMM's tile configuration for ``rows`` rows spread evenly: the one whose rounds of tiles over the

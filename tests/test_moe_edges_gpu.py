@@ -308,3 +308,50 @@ def test_layer_factors_of_rows_alone():
     for bad in (0.0, -1.0, float("nan"), float("inf"), 1e39, 1e-46):
         with pytest.raises(ValueError, match="scale"):
             moe.FeedForward(layer.b1, layer.sfb1, layer.b2, layer.sfb2, scale2=bad)
+
+
+# ---- more rows than a group of the grouped GEMM holds ----------------------------------
+
+def test_layer_in_parts(monkeypatch):
+    """A layer whose rows might not fit one group takes its tokens in parts, and gives what each part gives."""
+    layer, w1, w2, x = layer_of(300, 5, 256, 64, "bf16")
+    rng = rng_of(300, 1)
+    ids, w = gpu(rng.integers(-1, 5, (300, 2)).astype(np.int32)), gpu(rng.uniform(0.1, 1, (300, 2)).astype(np.float32))
+    residual = torch.randn_like(x)
+    assert layer._most_tokens(2) > 1 << 20
+    monkeypatch.setattr(moe.FeedForward, "_most_tokens", lambda self, topk: 128)
+    y = layer.grouped(x, ids, w, residual=residual)
+    monkeypatch.undo()
+    for lo in (0, 128, 256):
+        part = slice(lo, lo + 128)
+        assert torch.equal(y[part], layer.grouped(x[part], ids[part], w[part], residual=residual[part]))
+
+
+def test_layer_of_an_expert_with_more_rows_than_a_group_holds():
+    """262200 rows of 8192 bytes on one expert: the grouped GEMM refuses such a group and leaves its rows as they were."""
+    tokens, hidden = 262200, 16384
+    layer, w1, w2, _ = layer_of(1, 2, hidden, 32, "bf16")
+    x = torch.empty(tokens, hidden, dtype=torch.bfloat16, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(1))
+    ids = torch.zeros(tokens, 1, dtype=torch.int32, device="cuda")
+    ids[5] = 1
+    w = torch.rand(tokens, 1, device="cuda") + 0.5
+    y = layer.grouped(x, ids, w)
+    for some in (slice(0, 8), slice(tokens // 2 - 4, tokens // 2 + 4), slice(tokens - 8, tokens)):
+        near(y[some], layer_reference(layer, x[some], ids[some].cpu().numpy(), f64(w[some]), w1, w2, True))
+
+
+def test_product_of_a_group_that_is_refused():
+    """Its rows are NaN where no status is asked for, and as they were where one is."""
+    b, sfb, w = operand(rng_of(3), 2, 16, 16384)
+    rows = 262200
+    a = torch.zeros(rows, 8192, dtype=torch.uint8, device="cuda")
+    sfa = torch.zeros(c.nvfp4_moe_sf_bytes(rows, 2, 16384), dtype=torch.uint8, device="cuda")
+    q = moe.Product(a, sfa, b, sfb, torch.full((rows, 16), 7.0, dtype=torch.float16, device="cuda"))
+    ids = torch.zeros(rows, 1, dtype=torch.int32, device="cuda")
+    ids[-40:] = 1
+    moe.plan(ids, 2, (q,))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = q.run(status=status)
+    assert int(status) == 1 and (out[:-40] == 7).all() and (out[-40:] == 0).all()
+    out = q.run()
+    assert torch.isnan(out[:-40]).all() and (out[-40:] == 0).all()
