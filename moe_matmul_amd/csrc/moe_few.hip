@@ -387,7 +387,10 @@ __global__ void __launch_bounds__(kThreads, kMinWaves) nvfp4_few_tokens_kernel(F
     if (kScaled && threadIdx.x < kMaxRows) s_top[threadIdx.x] = 0;  // read again after the next barrier only
 
     // lane has rows lane / 16 * 4 + i of column lane % 16 of its runs
-    const float alpha = a.alpha == nullptr ? 1.f : a.alpha[expert];
+    // the factor's mantissa and exponent: a sum's own power of two is taken out together with the latter, so that what is
+    // between them does not leave fp32's range where the result does not
+    const float alpha = a.alpha == nullptr ? 1.f : a.alpha[expert], alpha_part = __builtin_amdgcn_frexp_mantf(alpha);
+    const int alpha_exp = __builtin_amdgcn_frexp_expf(alpha);
     float* sums = (float*)s_shared;  // [wave][run][row][column]
     if (a.k_waves > 1) {
       if (k_wave > 0) {
@@ -404,14 +407,12 @@ __global__ void __launch_bounds__(kThreads, kMinWaves) nvfp4_few_tokens_kernel(F
       for (int i = 0; i < 4; ++i) {
         const int r = lane / 16 * 4 + i;
         if (r >= rows) continue;
-        float unscale = alpha;
-        if constexpr (kScaled) unscale *= __builtin_bit_cast(float, (uint32_t)(254 - up[i]) << 23);
         float y[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           y[u] = sum[u][i];
           for (int w = 1; w < a.k_waves; ++w) y[u] += sums[(((wave + w) * U + u) * kMaxRows + r) * 16 + lane % 16];
-          y[u] *= unscale;
+          y[u] = kScaled ? __builtin_ldexpf(y[u] * alpha_part, alpha_exp + 127 - up[i]) : y[u] * alpha;
         }
 #pragma unroll
         for (int u = 0; u < SUB; ++u) {

@@ -355,3 +355,35 @@ def test_product_of_a_group_that_is_refused():
     assert int(status) == 1 and (out[:-40] == 7).all() and (out[-40:] == 0).all()
     out = q.run()
     assert torch.isnan(out[:-40]).all() and (out[-40:] == 0).all()
+
+
+# ---- a few tokens -----------------------------------------------------------------------
+
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_few_tokens_factors_beside_rows_of_any_size(swiglu):
+    """Rows whose largest element is at either end of bf16's range with factors at the other: results that are ordinary
+    numbers, and rows of weights that are 0."""
+    rng = rng_of(12)
+    b, sfb, w = operand(rng, 6, 64, 160)
+    b[:, 5] = 0
+    w[:, 5] = 0
+    sizes = np.array([2.0 ** 120, 2.0 ** -110, 2.0 ** 100, 2.0 ** -90, 1.0, 2.0 ** -110])
+    alpha = (rng.uniform(1, 2, 6) / sizes / 64).astype(np.float32)
+    alpha[2] = 2.0 ** 90                              # results beyond fp32, but for the row of zeros
+    alpha[5] = 2.0 ** -13 * 1.37                      # results of about 2^-118
+    x = rng.standard_normal((6, 160)) * sizes[:, None]
+    t = gpu(x, torch.bfloat16)
+    ids = np.arange(6, dtype=np.int32)[:, None]
+    y = moe.few_tokens(t, gpu(ids), b, sfb, alpha=gpu(alpha), swiglu=swiglu, dtype=torch.float32)
+    want, size = MO.few(f64(t), ids, w, alpha)
+    if swiglu:
+        some = [0, 1, 3, 4, 5]
+        bound = (160 + 16) * H[torch.float32] * size
+        g, u = np.split(want, 2, axis=-1)
+        bg, bu = np.split(bound, 2, axis=-1)
+        silu = g / (1 + np.exp(-np.clip(g, -700, None)))
+        close(y[some], (silu * u)[some], (1.1 * bg * (np.abs(u) + bu) + np.abs(silu) * bu + 16 * H[torch.float32] * np.abs(silu * u))[some],
+              torch.float32)
+    else:
+        close(y, want, (160 + 16) * H[torch.float32] * np.minimum(size, 1e300), torch.float32)
+        assert (y[:, 0, 5] == 0).all()
