@@ -208,7 +208,7 @@ int nvfp4_moe_dequantize(const void* a, const void* sfa, int l, int64_t m, int k
  * order, of weights[t][j] * alpha[ids[t][j]] * c[slot_rows[t][j]], summed in
  * fp32 and rounded once to out_dtype. Slots whose row is not in 0 .. c_rows - 1
  * add nothing and read nothing.
- *   c          device [c_rows][n] of c_dtype (fp16 or bf16 or fp32), rows c_stride apart
+ *   c          device [c_rows][n] of c_dtype (fp16 or bf16 or fp32), rows c_stride apart; NULL if c_rows is 0
  *   slot_rows  NULL: the row of a slot is the slot (then c_rows >= tokens*topk)
  *   weights    fp32 [tokens][topk], NULL: 1
  *   alpha      fp32 [experts], NULL: 1; needs ids

@@ -151,14 +151,15 @@ __global__ void __launch_bounds__(kThreads) nvfp4_moe_combine_backward_kernel(Co
   }
 }
 
-int check_combine(const CombineArgs& a, int c_dtype, int dtype, int64_t stride, const void* p, const void* q) {
+// p: dy or out, rows of `dtype` `stride` apart.
+int check_combine(const CombineArgs& a, int c_dtype, int dtype, int64_t stride, const void* p) {
   if (!known_type(c_dtype) || !known_type(dtype)) return NVFP4_ERR_INVALID;
   if (a.tokens < 0 || a.tokens >= (int64_t)1 << 30 || a.topk < 1 || a.topk > NVFP4_MOE_MAX_TOPK) return NVFP4_ERR_INVALID;
   if (a.n < 0 || a.n % 8 || a.c_stride < a.n || stride < a.n) return NVFP4_ERR_INVALID;
   if (a.c_stride > (int64_t)1 << 30 || stride > (int64_t)1 << 30) return NVFP4_ERR_INVALID;
   if (a.alpha != nullptr && (a.ids == nullptr || a.experts < 1)) return NVFP4_ERR_INVALID;
   if (a.c_rows < 0 || (a.slot_rows == nullptr && a.tokens * a.topk > a.c_rows)) return NVFP4_ERR_INVALID;
-  if (a.tokens > 0 && a.n > 0 && (a.c == nullptr || p == nullptr || q == nullptr)) return NVFP4_ERR_INVALID;
+  if (a.tokens > 0 && a.n > 0 && (p == nullptr || (a.c_rows > 0 && a.c == nullptr))) return NVFP4_ERR_INVALID;
   if (!aligned(a.slot_rows, 4) || !aligned(a.ids, 4) || !aligned(a.weights, 4) || !aligned(a.alpha, 4))
     return NVFP4_ERR_MISALIGNED;
   if (!aligned(a.c, element_bytes(c_dtype)) || !aligned(p, element_bytes(dtype))) return NVFP4_ERR_MISALIGNED;
@@ -190,7 +191,7 @@ int nvfp4_moe_combine(const void* c, int c_dtype, int64_t c_stride, int64_t c_ro
   a.out = out;
   a.topk = topk;
   a.n = n;
-  if (int rc = check_combine(a, c_dtype, out_dtype, out_stride, out, out)) return rc;
+  if (int rc = check_combine(a, c_dtype, out_dtype, out_stride, out)) return rc;
   if (!aligned(residual, element_bytes(out_dtype))) return NVFP4_ERR_MISALIGNED;
   if (tokens == 0 || n == 0) return NVFP4_OK;
   a.chunks = ceil_div(n, 512);
@@ -232,8 +233,8 @@ int nvfp4_moe_combine_backward(const void* dy, int dy_dtype, int64_t dy_stride, 
   a.dweights = dweights;
   a.topk = topk;
   a.n = n;
-  if (int rc = check_combine(a, c_dtype, dy_dtype, dy_stride, dy, dc)) return rc;
-  if (tokens > 0 && dweights == nullptr) return NVFP4_ERR_INVALID;
+  if (int rc = check_combine(a, c_dtype, dy_dtype, dy_stride, dy)) return rc;
+  if (tokens > 0 && (dweights == nullptr || (n > 0 && c_rows > 0 && dc == nullptr))) return NVFP4_ERR_INVALID;
   if (tokens >= (int64_t)1 << 24) return NVFP4_ERR_INVALID;
   if (!aligned(dc, element_bytes(c_dtype)) || !aligned(dweights, 4)) return NVFP4_ERR_MISALIGNED;
   if (tokens == 0) return NVFP4_OK;

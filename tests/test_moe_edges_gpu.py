@@ -387,3 +387,18 @@ def test_few_tokens_factors_beside_rows_of_any_size(swiglu):
     else:
         close(y, want, (160 + 16) * H[torch.float32] * np.minimum(size, 1e300), torch.float32)
         assert (y[:, 0, 5] == 0).all()
+
+
+# ---- combine ----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("kind", TYPES)
+def test_combine_of_no_rows(kind):
+    """Experts' rows that are none: the residual alone, and gradients of 0."""
+    x = torch.empty(0, 72, dtype=TYPES[kind], device="cuda")
+    rows = torch.tensor([[-1, -1], [0, 7], [-1, 2 ** 31 - 1]], dtype=torch.int32, device="cuda")
+    w = torch.full((3, 2), float("nan"), device="cuda")
+    residual = torch.randn(3, 72, device="cuda").to(TYPES[kind])
+    assert torch.equal(moe.combine(x, w, rows, residual=residual), residual)
+    assert (moe.combine(x, w, rows) == 0).all()
+    dc, dw = moe.combine_backward(residual, x, w, rows)
+    assert dc.shape == (0, 72) and (dw == 0).all()
