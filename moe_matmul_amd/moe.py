@@ -413,8 +413,8 @@ def combine(x, weights, rows=None, *, alpha=None, ids=None, experts=None, residu
 
 @_on_stream
 def combine_backward(dy, x, weights, rows=None, *, alpha=None, ids=None, experts=None, dc=None, stream=None):
-    """(d x, d weights) of ``combine``; rows of d x that no slot has are not written, those of slots without an
-    expert are 0."""
+    """(d x, d weights) of ``combine``; rows of d x whose slots have no expert are 0, and so are rows that no slot has.
+    Those are not written to a ``dc`` that is given: a program that keeps one cleared saves the clearing."""
     device = _gpu(x, "x")
     stride = _rows(x, "x")
     tokens, topk, rows, ids, experts = _slots(weights, rows, alpha, ids, experts, x, device)
@@ -423,6 +423,8 @@ def combine_backward(dy, x, weights, rows=None, *, alpha=None, ids=None, experts
         raise ValueError(f"dy must have {tokens} rows, on {device}")
     if dc is None:
         dc = torch.empty_strided(x.shape, (stride, 1), dtype=x.dtype, device=device)
+        if rows is not None or x.shape[0] > tokens * topk:  # else every row is a slot's
+            dc.zero_()
     elif dc.shape != x.shape or dc.dtype != x.dtype or dc.device != device or _rows(dc, "dc") != stride:
         raise ValueError("dc must have x's shape, strides, type and device")
     dweights = torch.empty((tokens, topk), dtype=torch.float32, device=device)

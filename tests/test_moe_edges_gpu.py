@@ -402,3 +402,22 @@ def test_combine_of_no_rows(kind):
     assert (moe.combine(x, w, rows) == 0).all()
     dc, dw = moe.combine_backward(residual, x, w, rows)
     assert dc.shape == (0, 72) and (dw == 0).all()
+
+
+@pytest.mark.parametrize("strided", [False, True])
+def test_combine_gradient_of_rows_that_no_slot_has(strided):
+    """0, in a gradient that the call allocates (whatever its memory held)."""
+    rng = rng_of(44)
+    ids = rng.integers(-1, 4, (64, 3)).astype(np.int32)
+    store = gpu(rng.standard_normal((192, 80)), torch.float16)
+    x = store[:, 8:72] if strided else store[:, :64].contiguous()
+    w, dy = gpu(rng.uniform(0.1, 1, (64, 3)).astype(np.float32)), gpu(rng.standard_normal((64, 64)), torch.float32)
+    p = moe.plan(gpu(ids), 4)
+    want = MO.combine_backward(f64(dy), f64(x), f64(w), MO.plan(ids, 4)[2])[0]
+    want = np.where(np.isnan(want), 0, want)
+    for _ in range(3):
+        for n in (192 * 64, 192 * 80):
+            torch.full((n,), float("nan"), dtype=torch.float16, device="cuda")  # freed at once: what comes next may lie there
+        dc, _ = moe.combine_backward(dy, x, w, p)
+        assert dc.stride() == x.stride()
+        close(dc, want, 3 * H[torch.float32] * np.abs(want), torch.float16)
