@@ -421,3 +421,82 @@ def test_combine_gradient_of_rows_that_no_slot_has(strided):
         dc, _ = moe.combine_backward(dy, x, w, p)
         assert dc.stride() == x.stride()
         close(dc, want, 3 * H[torch.float32] * np.abs(want), torch.float16)
+
+
+# ---- choice values that are nearly equal ------------------------------------------------
+
+def choice_values(x, how, bias):
+    s = MO.scores(x, how["score"])
+    return np.where(np.isneginf(x), -np.inf, s + (0 if bias is None else bias.astype(np.float64)))
+
+
+def told_apart(values, count):
+    """Tokens whose `count` largest values, and the next, differ from each other by more than 2^-41 or not at all (the
+    kernels take what is within 2^-42 for equal)."""
+    top = np.sort(values, axis=1)[:, ::-1][:, :count + 1]
+    gap = top[:, :-1] - top[:, 1:]
+    return ~((gap > 0) & (gap < 2.0 ** -41)).any(axis=1)
+
+
+@pytest.mark.parametrize("step", [2.0 ** -24, 2.0 ** -23, 2.0 ** -22, 2.0 ** -21, 2.0 ** -20, 2.0 ** -19, 2.0 ** -18, 2.0 ** -17])
+@pytest.mark.parametrize("score,experts,topk,dtype", [("sigmoid", 64, 6, "fp32"), ("softmax", 64, 6, "fp32"), ("sigmoid", 256, 8, "bf16"),
+                                                      ("softmax", 40, 3, "fp32"), ("softmax", 8, 1, "fp16")])
+def test_route_choice_values_around_the_margin(score, experts, topk, dtype, step):
+    """Neighbouring choice values a few `step` apart, by the logits and by the bias: the ids are the exact values'."""
+    rng = rng_of(experts, topk, int(-np.log2(step)))
+    tokens = 1500
+    slope = 0.24 if score == "sigmoid" else 1.0 / experts
+    x = 0.3 + rng.integers(-3, 4, (tokens, experts)) * (step / slope)     # all scores nearly the same
+    bias = (rng.integers(-4, 5, experts) * step * rng.choice([0.5, 1.0, 1.5], experts)).astype(np.float32)
+    x[1::3] = rng.standard_normal((len(x[1::3]), experts))                # scores apart, the bias makes up for it
+    x[2::3] = rng.standard_normal((len(x[2::3]), 1)) + rng.standard_normal((len(x[2::3]), experts)) * step * 8
+    x[5::30, ::2] = x[5::30, 1::2]
+    x[rng.random(x.shape) < 0.03] = -np.inf
+    x = gpu(x, TYPES[dtype])
+    how = dict(score=score)
+    told = told_apart(choice_values(f64(x), how, bias), topk)
+    assert told.mean() > 0.9
+    want_ids, want_w = MO.route(f64(x), topk, bias=bias.astype(np.float64), **how)
+    for many in (1, 90):                                                  # many lanes a token, and few
+        ids, w = moe.route(x.repeat(many, 1), topk, bias=gpu(bias), **how)
+        got = ids[-tokens:].cpu().numpy()
+        assert np.array_equal(got[told], want_ids[told])
+        assert torch.equal(ids[:tokens], ids[-tokens:])
+        close(w[-tokens:][gpu(np.flatnonzero(told))], want_w[told], 64 * H[torch.float32] * want_w[told], torch.float32)
+
+
+def test_route_bias_that_makes_up_for_the_scores():
+    """Each token's own scores all over [0, 1], lifted by the bias to values that differ by 2^-22 or so: the margin where the
+    scores' own errors are largest and differ."""
+    for score, experts in (("sigmoid", 64), ("softmax", 24)):
+        rng = rng_of(experts, 9)
+        x = rng.standard_normal((1, experts)).astype(np.float32) * 2
+        bias = (0.75 - MO.scores(x.astype(np.float64), score)[0] + rng.integers(-6, 7, experts) * 2.0 ** -24).astype(np.float32)
+        x = np.repeat(x, 1200, axis=0)
+        x += rng.integers(-3, 4, x.shape).astype(np.float32) * np.float32(2.0 ** -22)
+        told = told_apart(choice_values(x.astype(np.float64), dict(score=score), bias), 6)
+        assert told.mean() > 0.9
+        ids, _ = moe.route(gpu(x), 6, bias=gpu(bias), score=score)
+        want, _ = MO.route(x.astype(np.float64), 6, bias=bias.astype(np.float64), score=score)
+        assert np.array_equal(ids.cpu().numpy()[told], want[told])
+
+
+@pytest.mark.parametrize("experts,topk,how", [
+    (40, 4, dict(score="softmax", groups=4, topk_groups=2, group_best=1)),
+    (128, 8, dict(score="sigmoid", groups=8, topk_groups=4, group_best=2)),
+    (60, 10, dict(score="softmax", groups=20, topk_groups=7, group_best=2))])
+def test_route_groups_that_are_nearly_equal(experts, topk, how):
+    """The same inputs as of the calls of many tokens against few, here against the oracle."""
+    rng = rng_of(experts, 10)
+    x = rng.standard_normal((900, experts))
+    x[1::3] = x[1::3] * 1e-5 + 0.5
+    x[2::6, ::2] = x[2::6, 1::2]
+    x = x.astype(np.float32)
+    bias = (rng.standard_normal(experts) * 1e-6).astype(np.float32)
+    values = choice_values(x.astype(np.float64), how, bias)
+    best = np.sort(values.reshape(900, how["groups"], -1), axis=2)[:, :, ::-1][:, :, :how["group_best"]].sum(2)
+    told = told_apart(values, experts - 1) & told_apart(best, how["groups"] - 1)
+    assert told.mean() > 0.9
+    ids, _ = moe.route(gpu(x), topk, bias=gpu(bias), **how)
+    want, _ = MO.route(x.astype(np.float64), topk, bias=bias.astype(np.float64), **how)
+    assert np.array_equal(ids.cpu().numpy()[told], want[told])
