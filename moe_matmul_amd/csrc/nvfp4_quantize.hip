@@ -9,7 +9,8 @@ constexpr int kTileThreads = 1024;
 constexpr int kTileAtoms = 4;                        // atoms along K of a tile: 256 K-elements
 constexpr int kTileHalves = kTileAtoms * 8;          // halves of 16-element blocks of a tile's row
 constexpr int kRowThreads = 256;
-constexpr int64_t kMaxGrid = (1 << 23) - 1;          // workgroups: fewer than 2^32 threads, and 2^31 of a row kernel
+constexpr int64_t kMaxGrid = (1 << 23) - 1;          // workgroups of a row kernel: fewer than 2^31 threads
+constexpr int64_t kMaxTiles = (1 << 22) - 1;         // of a tile kernel: fewer than 2^32 threads, which a launch can have
 
 // ---- half a block of 16 to a lane: a wave's loads and stores take whole lines ---------------------------------------------------------
 // The rounding of a quotient to few bits is exact where the quotient is rounded
@@ -546,17 +547,18 @@ int with_rows(int dtype, const void* x, int64_t row_stride, int64_t batch_stride
 // 4.7 - 6.6, of 1024 6.9 - 7.0, of 2048 12.7 - 10.9. Rows of a batch need no
 // search for their expert on their way back: 4 x 2048 x 7168 26.7 - 27.6,
 // 16 x 1024 x 7168 71 - 49, while 256 experts of 64 rows of 2048 are 33 - 23.
-bool tiles_pay(const Rows& r, int blocks, bool back) {
+// 0 where rows do (or where there are more tiles than a launch can have), else the number of tiles.
+int64_t tiles_that_pay(const Rows& r, int64_t batches, int blocks, bool back) {
   const int64_t elements = r.rows * blocks * 16, per = r.offsets == nullptr ? r.m : r.rows / r.experts;
-  return per >= 32 && elements >= (int64_t)1 << (back && r.offsets == nullptr ? 26 : 23);
+  if (per < 32 || elements < (int64_t)1 << (back && r.offsets == nullptr ? 26 : 23)) return 0;
+  const int64_t tiles = atom_rows(r, batches) * ceil_div(ceil_div(blocks, 4), kTileAtoms);
+  return tiles <= kMaxTiles ? tiles : 0;
 }
 
 template <class Source>
 int launch_quantize(const Source& src, const Rows& rows, int64_t batches, int blocks, void* a, void* sfa, hipStream_t st) {
-  if (tiles_pay(rows, blocks, false)) {
-    const int64_t grid = atom_rows(rows, batches) * ceil_div(ceil_div(blocks, 4), kTileAtoms);
-    if (grid > kMaxGrid) return NVFP4_ERR_INVALID;
-    nvfp4_quantize_tiles_kernel<<<(unsigned)grid, kTileThreads, 0, st>>>(src, rows, blocks, (uint32_t*)a, (uint8_t*)sfa);
+  if (const int64_t tiles = tiles_that_pay(rows, batches, blocks, false)) {
+    nvfp4_quantize_tiles_kernel<<<(unsigned)tiles, kTileThreads, 0, st>>>(src, rows, blocks, (uint32_t*)a, (uint8_t*)sfa);
   } else {
     const int64_t grid = ceil_div64(rows.rows * (ceil_div(blocks, 4) * 8), kRowThreads);
     if (grid > kMaxGrid) return NVFP4_ERR_INVALID;
@@ -680,10 +682,9 @@ int nvfp4_moe_dequantize(const void* a, const void* sfa, int l, int64_t m, int k
   if (m == 0 || k == 0) return NVFP4_OK;
   const Rows rows = {offsets, atoms, experts, l * m, m};
   const int blocks = k / 16;
-  const bool tiles = tiles_pay(rows, blocks, true);
-  const int64_t grid = tiles ? atom_rows(rows, l) * ceil_div(ceil_div(blocks, 4), kTileAtoms)
-                             : ceil_div64(rows.rows * 2 * blocks, kRowThreads);
-  if (grid > kMaxGrid) return NVFP4_ERR_INVALID;
+  const int64_t tiles = tiles_that_pay(rows, l, blocks, true);
+  const int64_t grid = tiles ? tiles : ceil_div64(rows.rows * 2 * blocks, kRowThreads);
+  if (tiles == 0 && grid > kMaxGrid) return NVFP4_ERR_INVALID;
   const hipStream_t st = (hipStream_t)stream;
   return with_type(dtype, [&](auto t) {
     using T = decltype(t);

@@ -500,3 +500,18 @@ def test_route_groups_that_are_nearly_equal(experts, topk, how):
     ids, _ = moe.route(gpu(x), topk, bias=gpu(bias), **how)
     want, _ = MO.route(x.astype(np.float64), topk, bias=bias.astype(np.float64), **how)
     assert np.array_equal(ids.cpu().numpy()[told], want[told])
+
+
+# ---- more tiles than a launch can have -------------------------------------------------
+
+def test_quantize_of_more_tiles_than_a_launch_holds():
+    """2^22 batches and a few of 32 rows of 32, whose tiles would be more than 2^32 threads: to their codes and back."""
+    l = (1 << 22) + 9
+    x = torch.empty(l, 32, 32, dtype=torch.float16, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(6))
+    a, sfa = moe.quantize(x)
+    values = moe.dequantize(a, sfa)
+    for li in (0, 1, 8, 9, 1 << 21, l - 10, l - 9, l - 2, l - 1):
+        codes, scales = MO.quantize(f64(x[li]))
+        got_codes, got_scales = MO.unpack_rows(a[li].cpu().numpy(), sfa[li * 512:li * 512 + 512].cpu().numpy(), 32, 32)
+        assert np.array_equal(got_codes, codes) and np.array_equal(got_scales, scales)
+        assert np.array_equal(f64(values[li]), MO.values(codes, scales))
