@@ -139,16 +139,23 @@ template <class T> struct Raw8 {
   }
 };
 
-// exp in fp32, times 2^up: 2^(x log2 e) with the product's rounding error taken
-// back, so that the result is within about 2 ulp for every x (the plain product
-// loses |x| * 2^-24) where it is a normal number; below 2^-126 it is 0. -inf gives
-// 0, NaN gives NaN.
-__device__ inline float exp_f32(float x, float up = 0.f) {
+// exp in fp32: 2^(x log2 e) with the product's rounding error taken back, so that
+// the result is within about 2 ulp for every x (the plain product loses |x| *
+// 2^-24) where it is a normal number; below 2^-126 it is 0. -inf gives 0, NaN gives
+// NaN. With `up` (a whole number), times 2^up.
+__device__ inline float exp_f32_low(float x, float t) {  // the factor that is 1 but for the rounding of t = x log2 e
   const float kLog2e = 1.44269502f, kLog2eLow = 1.92596303e-8f, kLn2 = 0.693147182f;
-  const float t = x * kLog2e;
   // |x| beyond this over- or underflows whatever the low part; it would be inf - inf
   const float low = fabsf(x) < 200.f ? fmaf(x, kLog2eLow, fmaf(x, kLog2e, -t)) : 0.f;
-  return __builtin_amdgcn_exp2f(t + up) * fmaf(low, kLn2, 1.f);
+  return fmaf(low, kLn2, 1.f);
+}
+__device__ inline float exp_f32(float x) {
+  const float t = x * 1.44269502f;
+  return __builtin_amdgcn_exp2f(t) * exp_f32_low(x, t);
+}
+__device__ inline float exp_f32(float x, float up) {
+  const float t = x * 1.44269502f;
+  return __builtin_amdgcn_exp2f(t + up) * exp_f32_low(x, t);
 }
 
 // Stores to shared memory by lanes of this wave are seen by its other lanes.

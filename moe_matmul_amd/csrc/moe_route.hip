@@ -50,12 +50,6 @@ struct Wide {
   }
   static __device__ inline Key larger(Key a, Key b) { return fmax(a, b); }
   static __device__ inline Key smaller(Key a, Key b) { return fmin(a, b); }
-  template <int kCtrl> static __device__ inline Key from_lane(Key v) {
-    const uint64_t u = __builtin_bit_cast(uint64_t, v);
-    const uint32_t low = __builtin_amdgcn_mov_dpp((int)(uint32_t)u, kCtrl, 0xF, 0xF, false);
-    const uint32_t high = __builtin_amdgcn_mov_dpp((int)(uint32_t)(u >> 32), kCtrl, 0xF, 0xF, false);
-    return __builtin_bit_cast(double, (uint64_t)high << 32 | low);
-  }
 };
 
 // 16-bit logits: their bits, mapped so that they order as whole numbers, over the index.
@@ -72,13 +66,11 @@ struct Narrow {
   static __device__ inline int index(Key key) { return key == 0 ? -1 : kIndexMask - (int)(key & 0xFFFFu); }
   static __device__ inline Key larger(Key a, Key b) { return max(a, b); }
   static __device__ inline Key smaller(Key a, Key b) { return min(a, b); }
-  template <int kCtrl> static __device__ inline Key from_lane(Key v) {
-    return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, kCtrl, 0xF, 0xF, false);
-  }
 };
 
 // ---- exp and sigmoid in fp64 -------------------------------------------------
-// 2^n times the Taylor series of e^r, |r| <= ln 2 / 2: 13 terms leave 2^-53 / 4.
+// 2^n times the Taylor series of e^r, |r| <= ln 2 / 2: 13 terms leave r^13 / 13!, at
+// most 1.5 * 2^-53.
 // r = x - n ln 2 with ln 2 in two parts (Cody and Waite): its first 42 bits, times
 // which an n of up to 11 bits is exact, and the rest.
 __device__ inline double exp_f64(double x) {
@@ -108,11 +100,12 @@ __device__ inline double inverse_f64(double d) {
 }
 
 // sigmoid(x) / e^from = e^(x - from) / (1 + e^x) of logits x and from, both below 0
-// or from 0. For scores that leave fp32's range, while their ratios are ordinary
-// numbers: those renormalised by a sum of such scores, and those below kSmallLogit.
+// or from 0. For scores that leave fp32's range while their ratios are ordinary
+// numbers: those whose sum is below kSmallSum, of which a score's own rounding in
+// fp32's last steps would be more than 2^-126, and those below kSmallLogit.
 // What the difference of the logits loses (half an ulp of up to 700) is put back,
 // and results below 2^-126 are kept (v_exp and v_rcp give 0). What is 0 in fp64 is 0.
-constexpr float kSmallLogit = -64.f, kLeastLogit = -708.f;
+constexpr float kSmallLogit = -64.f, kLeastLogit = -708.f, kSmallSum = 0x1p-10f;
 __device__ inline float sigmoid_over_exp(float x, float from) {
   const float d = x - from, lost = (x - d) - from, up = d < -80.f ? 0x1p64f : 1.f;
   const float e = exp_f32(d, d < -80.f ? 64.f : 0.f);
@@ -171,13 +164,24 @@ __device__ inline void keep_largest(const typename W::Key (&v)[N], typename W::K
   }
 }
 
+template <int kCtrl> __device__ inline uint32_t lane_bits(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, kCtrl, 0xF, 0xF, false);
+}
+template <int kCtrl, class V> __device__ inline V from_lane(V v) {
+  if constexpr (sizeof(V) == 8) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    return __builtin_bit_cast(V, (uint64_t)lane_bits<kCtrl>((uint32_t)(u >> 32)) << 32 | lane_bits<kCtrl>((uint32_t)u));
+  } else {
+    return __builtin_bit_cast(V, lane_bits<kCtrl>(__builtin_bit_cast(uint32_t, v)));
+  }
+}
 constexpr int kXor1 = 0xB1, kXor2 = 0x4E;           // quad permutations
 constexpr int kMirror8 = 0x141, kMirror16 = 0x140;  // lane i <-> 7 - i, 15 - i
 
 template <class W, int K, int kCtrl> __device__ inline void merge_with(typename W::Key (&list)[K]) {
   typename W::Key other[K];
 #pragma unroll
-  for (int i = 0; i < K; ++i) other[i] = W::template from_lane<kCtrl>(list[i]);
+  for (int i = 0; i < K; ++i) other[i] = from_lane<kCtrl>(list[i]);
   merge_falling<W, K>(list, other);
 }
 template <class W, int K> __device__ inline void merge_across(typename W::Key (&list)[K], int distance) {
@@ -196,17 +200,6 @@ template <class W, int K> __device__ inline void merge_lanes(typename W::Key (&l
   if (lanes > 32) merge_across<W, K>(list, 32);
 }
 
-template <int kCtrl> __device__ inline uint32_t lane_bits(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, kCtrl, 0xF, 0xF, false);
-}
-template <int kCtrl, class V> __device__ inline V from_lane(V v) {
-  if constexpr (sizeof(V) == 8) {
-    const uint64_t u = __builtin_bit_cast(uint64_t, v);
-    return __builtin_bit_cast(V, (uint64_t)lane_bits<kCtrl>((uint32_t)(u >> 32)) << 32 | lane_bits<kCtrl>((uint32_t)u));
-  } else {
-    return __builtin_bit_cast(V, lane_bits<kCtrl>(__builtin_bit_cast(uint32_t, v)));
-  }
-}
 // op over the values of a token's `lanes` (a power of two), in all of them; in a fixed order.
 template <class V, class Op> __device__ inline V across(V v, int lanes, Op op) {
   if (lanes > 1) v = op(v, from_lane<kXor1>(v));
@@ -269,7 +262,7 @@ __device__ inline Share share_of(const RouteArgs& a, int lane) {
   return s;
 }
 
-// A lane's logits; NaN past its share (its own NaNs are noted first).
+// A lane's logits; -inf past its share.
 template <class T, int NC>
 __device__ inline void load_share(const void* row, const Share& s, bool vec, float (&x)[NC * 8]) {
 #pragma unroll
@@ -328,7 +321,7 @@ __device__ inline void best_two(double v, double& one, double& two) {
 // two such errors.
 constexpr uint32_t kSigmoidMargin = 8, kSoftmaxMargin = 32;
 template <int K, int NC>
-__device__ inline bool choose_fp32(const RouteArgs& a, const Share& s, int lane, const float (&x)[NC * 8],
+__device__ inline bool choose_fp32(const RouteArgs& a, const Share& s, const float (&x)[NC * 8],
                                    const float (&bias)[NC * 8], float from, float inverse, uint32_t (&list)[K]) {
   const bool softmax = a.how.score == NVFP4_MOE_SOFTMAX;
   const uint32_t margin = softmax ? kSoftmaxMargin : kSigmoidMargin;
@@ -506,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, NC > 2 ? 2 : 4) nvfp4_moe_route_kern
     bool sure = false;
     if constexpr (kMode == kScores) {
       uint32_t list[K];
-      sure = choose_fp32<K, NC>(a, s, lane, x, bias, top, 1.f / total, list);
+      sure = choose_fp32<K, NC>(a, s, x, bias, top, 1.f / total, list);
 #pragma unroll
       for (int i = 0; i < K; ++i) chosen_ids[i] = kIndexMask - (int)(list[i] & kIndexMask);
     }
@@ -550,20 +543,30 @@ __global__ void __launch_bounds__(kThreads, NC > 2 ? 2 : 4) nvfp4_moe_route_kern
     largest = fmaxf(largest, chosen[q]);
   }
   const int share = a.lanes < K ? a.lanes : K;  // lanes that have a slot
-  if (a.how.renormalize) largest = max_across(largest, share);
-  if (softmax && a.how.renormalize) top = largest;
+  if (softmax && a.how.renormalize) top = max_across(largest, share);
   const float from = top == -__builtin_inff() ? 0.f : top;
-  const float over = a.how.renormalize ? fminf(largest, 0.f) : 0.f;  // sigmoids are divided by e^over
   float sum = 0.f;
+  bool small = false;
 #pragma unroll
   for (int q = 0; q < kLaneSlots; ++q) {
     if (softmax) w[q] = exp_f32(chosen[q] - from);
-    else if (over < 0.f || chosen[q] < kSmallLogit) w[q] = sigmoid_over_exp(chosen[q], over);
     else w[q] = ids[q] >= 0 ? __builtin_amdgcn_rcpf(1.f + exp_f32(-chosen[q])) : 0.f;
     sum += w[q];
+    small |= ids[q] >= 0 && chosen[q] < kSmallLogit;
   }
   if (a.how.renormalize) total = sum_across(sum, share);
   else if (!softmax) total = 1.f;
+  if (!softmax && __any(small || (lane < share && total < kSmallSum))) {
+    largest = max_across(largest, share);
+    const float over = total < kSmallSum ? largest : 0.f;
+    sum = 0.f;
+#pragma unroll
+    for (int q = 0; q < kLaneSlots; ++q) {
+      if (over < 0.f || chosen[q] < kSmallLogit) w[q] = ids[q] >= 0 ? sigmoid_over_exp(chosen[q], over) : 0.f;
+      sum += w[q];
+    }
+    if (a.how.renormalize) total = sum_across(sum, share);
+  }
   const float factor = total == 0.f ? a.how.scale : a.how.scale / total;
 #pragma unroll
   for (int q = 0; q < kLaneSlots; ++q) {
@@ -661,8 +664,9 @@ __global__ void __launch_bounds__(kThreads) nvfp4_moe_route_backward_kernel(Rout
     p = id >= 0 ? exp_f32(chosen - (from == -__builtin_inff() ? 0.f : from)) : 0.f;
   } else {
     const float over = a.how.renormalize ? fminf(max_across(chosen, a.lanes), 0.f) : 0.f;
-    if (over < 0.f || chosen < kSmallLogit) p = sigmoid_over_exp(chosen, over);
-    else p = id >= 0 ? 1.f / (1.f + exp_f32(-chosen)) : 0.f;
+    if (id < 0) p = 0.f;
+    else if (over < 0.f || chosen < kSmallLogit) p = sigmoid_over_exp(chosen, over);
+    else p = 1.f / (1.f + exp_f32(-chosen));
   }
   float q = p;
   if (a.how.renormalize) {
