@@ -386,10 +386,19 @@ struct Slots {
   int topk, experts, rows;
   int64_t atom_rows;
 
-  __device__ inline int expert_of(int64_t slot, int row) const {
-    const int e = ids[slot];
-    if ((unsigned)e < (unsigned)experts && offsets[e] <= row && row < offsets[e + 1]) return e;
-    return last_at_most(offsets, experts, row);
+  // Of the expert that has a row, its first row and its first atom row; `id`: where to look first.
+  // For all lanes of a wave that have a slot: the search is theirs together, out of the way where no lane needs it
+  // (as a branch of each lane's 4096 x 7168 to one of 8 experts each 27.7 us, 25.9 so; 25.2 with the ids trusted).
+  __device__ inline void find(bool named, int row, int id, int& first, int& atom) const {
+    const int e = (int)min((unsigned)id, (unsigned)(experts - 1));
+    const int next = offsets[e + 1];
+    first = offsets[e];
+    atom = atoms[e];
+    if (__any(named && (row < first || row >= next))) {
+      const int other = last_at_most(offsets, experts, row);
+      first = offsets[other];
+      atom = atoms[other];
+    }
   }
 };
 template <int kLane> __device__ inline uint32_t of_quad(uint32_t v) {
@@ -403,20 +412,28 @@ __global__ void __launch_bounds__(kRowThreads)
   const Place p = place_of(blockIdx.x * kRowThreads + threadIdx.x, along * 8);
   if (p.row >= tokens) return;  // for eight lanes at a time
   const bool there = p.kh < 2 * blocks;  // for four: k is a multiple of 32
+  int j = p.kh % 4, row = -1, id = 0;
+  const int64_t slot = p.row * slots.topk;
+  auto next = [&] {
+    if (j >= slots.topk) return;
+    row = slots.slot_rows[slot + j];
+    if (kDirect) id = slots.ids[slot + j];
+  };
+  next();
   Half b = {0u, 0u};
   if (there) b = src.half(p.row, 0, p.kh);
   const uint32_t word = scale_word(b.scale, p.kh);
   const u32x4 codes = {of_quad<0>(b.codes), of_quad<1>(b.codes), of_quad<2>(b.codes), of_quad<3>(b.codes)};
-  for (int j = p.kh % 4; j < slots.topk; j += 4) {
-    const int64_t slot = p.row * slots.topk + j;
-    const int row = slots.slot_rows[slot];
-    if ((unsigned)row >= (unsigned)slots.rows) continue;
-    if (there) *(u32x4*)(a + (int64_t)row * 2 * blocks + p.kh / 4 * 4) = codes;
+  for (; j < slots.topk; j += 4, next()) {
+    const bool named = (unsigned)row < (unsigned)slots.rows;
+    if (there && named) *(u32x4*)(a + (int64_t)row * 2 * blocks + p.kh / 4 * 4) = codes;
     if (kDirect && p.kh % 8 < 4) {
-      const int e = slots.expert_of(slot, row), at = row - slots.offsets[e];
-      const int64_t atom = (int64_t)slots.atoms[e] + at / kAtomRows;
-      if ((uint64_t)atom < (uint64_t)slots.atom_rows)
-        *(uint32_t*)(sfa + (atom * along + p.kh / 8) * kAtomBytes + atom_row(at % kAtomRows)) = word;
+      int first, atom;
+      slots.find(named, row, id, first, atom);
+      const int at = named ? row - first : 0;
+      const int64_t place = (int64_t)atom + at / kAtomRows;
+      if (named && (uint64_t)place < (uint64_t)slots.atom_rows)
+        *(uint32_t*)(sfa + (place * along + p.kh / 8) * kAtomBytes + atom_row(at % kAtomRows)) = word;
     }
   }
   if (!kDirect && p.kh % 8 == 0) token_scales[p.row * (ceil_div(along, 4) * 4) + p.kh / 8] = word;
