@@ -77,7 +77,8 @@ typedef struct nvfp4_moe_choice {
  *   else s + bias (bias NULL: s), compared in fp64. With groups, the
  *   topk_groups groups of the largest value stay eligible. The topk largest v
  *   among the eligible experts are chosen, in falling order; equal values go to
- *   the lowest index (fp64 values within 2^-42 of each other count as equal).
+ *   the lowest index (fp64 values within 2^-42 of each other, or that part of values
+ *   beyond 1, may count as equal).
  *   w = scale * s / (renormalize ? sum of the chosen s : 1); the bias has no
  *   part in it.
  * A logit of -inf masks its expert: score 0 and never chosen. A token with
@@ -103,7 +104,9 @@ int nvfp4_moe_route(const void* logits, int dtype, int64_t tokens, int experts, 
  * nvfp4_moe_route with the choice held fixed (groups and bias have no part).
  * Every element of dlogits [tokens][experts], of `dtype`, is written. `ids` as
  * nvfp4_moe_route gave them (a token's ids differ; -1: no gradient); the bias
- * gets no gradient.
+ * gets no gradient. A logit of an expert that was not chosen is read only where the
+ * weights are a softmax that is not renormalised: a NaN there makes no other
+ * gradient NaN, though it made the weights so.
  */
 int nvfp4_moe_route_backward(const void* logits, int dtype, int64_t tokens, int experts, int64_t row_stride,
                              const nvfp4_moe_choice* choice, const int32_t* ids, const float* dweights,
@@ -239,7 +242,9 @@ int nvfp4_moe_combine_backward(const void* dy, int dy_dtype, int64_t dy_stride, 
  * as they are (fp16 or bf16), one output row per slot:
  *   y[t][j] = alpha[e] * W_e x,  e = ids[t][j]
  *   swiglu: silu(y[0 .. n/2-1]) * y[n/2 .. n-1]
- * Every weight that some slot needs is read once per 16 slots of its expert.
+ * The weights of an expert are read once for a pass of its slots: as many as there
+ * are tokens, rounded up to a power of two, 16 at most (an expert that a token names
+ * several times may take more passes than one).
  * Products are accumulated in fp32. Slots without an expert give zeros.
  *   x      device [tokens][k], or with per_slot [tokens*topk][k], rows x_stride apart
  *   b, sfb device uint8 [experts][n][k/2] and [experts][nvfp4_sf_bytes(n, k, 1)], 16-byte aligned

@@ -9,6 +9,10 @@ workspaces are allocated on that stream; its waiting for the inputs, and keeping
 alive what another stream uses (``Tensor.record_stream``), are the caller's
 part, as everywhere in torch.
 
+Rows may lie apart (a slice of wider rows), but their elements have to be adjacent
+and rows may not overlap: expanded tensors, such as the gradient of a sum, are
+refused and need ``contiguous()`` first.
+
 ``FeedForward`` runs them together: route -> plan -> quantise -> grouped GEMM ->
 gated activation -> grouped GEMM -> combine, or, for a few tokens, the experts'
 products with activations as they are.
@@ -541,7 +545,9 @@ class FeedForward:
         return one / torch.full_like(one, scale)
 
     def __call__(self, x, ids, weights, *, residual=None, stream=None):
-        """y [tokens, hidden] of ``x``'s type, by the products that suit the number of tokens."""
+        """y [tokens, hidden] of ``x``'s type, by the products that suit the number of tokens: up to ``FEW_ROWS`` slots an
+        expert ``few``, beyond ``grouped``, whose rows and activations are in 4 bits. The two differ by that rounding; a
+        program that wants one of them whatever the batch calls it by name."""
         slots = ids.numel()
         few = slots <= min(self.FEW_ROWS * self.experts, c.NVFP4_MOE_MAX_FEW_SLOTS) and x.dtype != torch.float32
         run = self.few if few else self.grouped
