@@ -11,9 +11,9 @@ constexpr int kStep = 256;    // K-elements of a step: 128 bytes of a weight row
 constexpr int kStepBytes = kStep / 2;
 constexpr int kPieces = kStepBytes / 16;  // 16-byte pieces of a row's step
 // Steps of weights in flight, in registers, and waves of a SIMD that the registers
-// have to allow. 13 tokens of 2 of 8 experts of 7168 x 2048: 24 us, with three steps 30;
-// one token of 8 experts of 4096 x 7168 with SwiGLU 28 us, with four waves 35, as
-// registers spill, with two waves the same.
+// have to allow. 13 tokens of 2 of 8 experts of 7168 x 2048: 21.5 us, with three steps
+// 27.8, with four waves 24.1; one token of 8 experts of 4096 x 7168 with SwiGLU 28.2 us,
+// 33.8 and 35.4, as registers spill; with two waves the same.
 constexpr int kDepth = 2;
 constexpr int kMinWaves = 3;
 constexpr int kHold = 4;      // pieces of x that a thread has under way
@@ -21,8 +21,8 @@ constexpr int kMaxRows = 16;  // slots of a pass: rows of the matrix instruction
 constexpr int kStageElements = 16384;  // of x in shared memory, at most (32 KB)
 // Waves that share the columns before any share K, three for four SIMDs: sharing K
 // gains where the columns leave SIMDs idle only. Alone - shared: a token of 2 experts
-// of 2048 x 7168 25.7 - 12.8 us; 4 tokens of 8 of 32 experts of 4096 x 7168 with SwiGLU
-// 68 - 94.
+// of 2048 x 7168 25.5 - 12.8 us; 4 tokens of 8 of 32 experts of 4096 x 7168 with SwiGLU
+// 67 - 92.
 constexpr int kEnoughWaves = 768;
 constexpr int kPad = 8;       // elements after a staged row: rows start in different banks
 
@@ -145,7 +145,7 @@ __device__ inline int scale_up(uint32_t top) { return min(max(127 + 14 + 127 - (
 // the expert's slots themselves, so no order of slots has to be made before.
 // Bound by reading the weights: a token of 8 experts of 4096 x 7168 with SwiGLU, 132
 // MB in 28 us, 4.7 TB/s (reads alone reach 6.4 here); 13 tokens of 2 of 8 experts of
-// 7168 x 2048, 66 MB in 21 us, of which about 7 pass before the first weights
+// 7168 x 2048, 66 MB in 21.5 us, 3.1 TB/s, of which about 7 pass before the first weights
 // arrive and after the last.
 //
 // Weights go from memory to registers, kDepth steps ahead, the first of them

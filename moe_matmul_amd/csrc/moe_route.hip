@@ -436,11 +436,11 @@ __device__ inline void choose_fp64(const RouteArgs& a, const Share& s, int lane,
 // token for which fp32 cannot tell (one token of 256 experts in 600); in groups in fp64 at once, as
 // with sums of groups to compare in both the registers no longer suffice, and the
 // few waves that go twice end last. In fp32 first - in fp64, sigmoid scores of bf16
-// logits with bias: 40000 x 64 9.3 - 10.2 us, 131072 x 64 19.3 - 22.9, 24000 x 128 11.1 -
-// 11.8; in 4 of 8 groups 16384 x 256 16.4 - 16.6, 131072 x 256 92 - 89, in 2 of 4
-// groups 65536 x 128 33 - 29. By logits: 65537 x 64 in fp32, softmax, 6 chosen, 10.2
-// us (17 MB read and 3 written, 4 us of a copy's rate; a launch is 3). One token of
-// 256 grouped scores 5.6 us.
+// logits with bias: 40000 x 64 9.1 - 9.6 us, 131072 x 64 19.2 - 21.8, 24000 x 128 10.4 -
+// 11.5; in 4 of 8 groups, when both were tried, 131072 x 256 92 - 89, in 2 of 4 groups
+// 65536 x 128 33 - 29. By logits: 65537 x 64 in fp32, softmax, 6 chosen, 10.2 us (17 MB
+// read and 3 written, 4 us of a copy's rate; a launch is 3). 16384 tokens of 256
+// grouped scores 14.9 us, one token 5.5 us.
 template <int K, int NC, Mode kMode>
 __global__ void __launch_bounds__(kThreads, NC > 2 ? 2 : 4) nvfp4_moe_route_kernel(RouteArgs a) {
   extern __shared__ double s_worth[];  // [tokens][groups]
@@ -723,8 +723,8 @@ int at_least_pow2(int v) {
 
 // Lanes of a token: as few as hold its logits in registers, as the lanes' merged lists are the same work in each of
 // them, but more where there are too few tokens to fill the chip (15000 tokens x
-// 256 logits: 9.7 us with 8 lanes, 13.4 with 16; 16384 x 256 scores, which take
-// three times as long before the merges: 20 us with 8, 16.8 with 16).
+// 256 fp32 logits: 8.0 us with 8 lanes, 8.8 with 16; 16384 x 256 scores, which take
+// longer before the merges: 14.7 us with 8, 12.4 with 16, in groups 16.3 and 16.0).
 int widen(int lanes, int64_t tokens, int experts, int64_t enough) {
   while (lanes < 64 && tokens * lanes < enough && lanes * 8 < experts) lanes *= 2;
   return lanes;

@@ -314,7 +314,7 @@ __device__ inline Place place_of(uint32_t index, uint32_t padded) {
 }
 
 // Few rows: eight lanes join the scales of an atom's row to a word. 2048 gated
-// rows of 2048 fp16, of 256 experts, 9.4 us, of which a launch is 3.
+// rows of 2048 fp16, 19 MB, 9.8 us, of which a launch is 3.
 template <class Source>
 __global__ void __launch_bounds__(kRowThreads)
     nvfp4_quantize_rows_kernel(Source src, Rows rows, int blocks, uint32_t* a, uint8_t* sfa) {
@@ -340,8 +340,8 @@ __global__ void __launch_bounds__(kRowThreads)
 // shared memory and stored as the 2 KB that they are. Bound by memory, and gated
 // rows by the vector instructions of the activation and of its two roundings:
 // 16384 x 7168 bf16, 301 MB in 59 us, 5.1 TB/s (a block of 16 to a lane, which
-// touches lines in quarters: 65 us); 16390 gated rows of 2048 fp16, 153 MB in 41 us,
-// 3.7 TB/s (with every activation in fp64 104 us).
+// touches lines in quarters: 65 us); 16390 gated rows of 2048 fp16, 153 MB in 42 us,
+// 3.6 TB/s (with every activation in fp64 104 us).
 template <class Source>
 __global__ void __launch_bounds__(kTileThreads)
     nvfp4_quantize_tiles_kernel(Source src, Rows rows, int blocks, uint32_t* a, uint8_t* sfa) {
