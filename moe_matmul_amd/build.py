@@ -3,7 +3,8 @@
 ``python -m moe_matmul_amd.build`` compiles ``csrc/nvfp4_grouped_gemm.hip``
 into ``moe_matmul_amd/libnvfp4_grouped_gemm.so`` next to this file, the operators
 around it (``csrc/moe_*.hip``, ``csrc/nvfp4_quantize.hip``) into
-``moe_matmul_amd/libnvfp4_moe.so``, and the mainloop measurement kernels
+``moe_matmul_amd/libnvfp4_moe.so``, the feed-forward block in 16 bits
+(``csrc/ffn_*.hip``) into ``moe_matmul_amd/libnvfp4_ffn.so``, and the mainloop measurement kernels
 ``csrc/mainloop_probe.hip`` into ``moe_matmul_amd/libnvfp4_mainloop_probe.so``.
 """
 from __future__ import annotations
@@ -22,6 +23,11 @@ LIB = os.path.join(HERE, "libnvfp4_grouped_gemm.so")
 MOE_SOURCES = [os.path.join(HERE, "csrc", f) for f in
                ("moe_route.hip", "moe_plan.hip", "nvfp4_quantize.hip", "moe_combine.hip", "moe_few.hip")]
 MOE_LIB = os.path.join(HERE, "libnvfp4_moe.so")
+# the feed-forward block in 16 bits and its training (include/nvfp4_ffn.h)
+FFN_SOURCES = [os.path.join(HERE, "csrc", f) for f in
+               ("ffn_product.hip", "ffn_gemm_forward.hip", "ffn_gemm_dx.hip", "ffn_gemm_dw.hip", "ffn_norm.hip",
+                "ffn_rows.hip")]
+FFN_LIB = os.path.join(HERE, "libnvfp4_ffn.so")
 # measurement kernels behind the mainloop choice (not part of the GEMM)
 PROBE_SOURCES = [os.path.join(HERE, "csrc", "mainloop_probe.hip")]
 PROBE_LIB = os.path.join(HERE, "libnvfp4_mainloop_probe.so")
@@ -43,10 +49,11 @@ def hipcc() -> str:
 
 
 def build(verbose: bool = False) -> str:
-    """Compile the library, the operators' library and the probe library (always,
+    """Compile the library, the operators' libraries and the probe library (always,
     even if built copies exist); return the library's path."""
     _compile(SOURCES, LIB, verbose)
     build_moe(verbose)
+    build_ffn(verbose)
     _compile(PROBE_SOURCES, PROBE_LIB, verbose)
     return LIB
 
@@ -55,6 +62,12 @@ def build_moe(verbose: bool = False) -> str:
     """Compile the operators' library alone; return its path."""
     _compile(MOE_SOURCES, MOE_LIB, verbose)
     return MOE_LIB
+
+
+def build_ffn(verbose: bool = False) -> str:
+    """Compile the feed-forward block's library alone; return its path."""
+    _compile(FFN_SOURCES, FFN_LIB, verbose)
+    return FFN_LIB
 
 
 def _compile(sources, lib, verbose):

@@ -1,0 +1,145 @@
+// Shared by the kernels of nvfp4_ffn.h: activations and their slopes, rows in 8
+// bits, the plan's rows, and the host's argument checks.
+#pragma once
+
+#include "moe_common.h"
+#include "nvfp4_ffn.h"
+
+namespace ffn {
+
+using namespace moe;
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+
+// Where the rows sorted by expert lie: nvfp4_ffn_plan, or one expert with all rows.
+struct Rows {
+  const int32_t* offsets;    // NULL: one expert, rows 0 .. rows-1
+  const int32_t* row_slots;  // rows are tokens' rows: row r is row row_slots[r] / topk of the operand; NULL: row r itself
+  int experts, topk;
+  int64_t rows, sources;     // the most rows, and the operand's rows
+  int clear;                 // rows of no expert are written as 0; else left
+};
+
+// First row of expert e (experts: the rows of no expert), in 0 .. rows whatever the table holds.
+__device__ inline int64_t first_row(const Rows& r, int e) {
+  if (!r.offsets) return e ? r.rows : 0;
+  const int64_t o = r.offsets[e];
+  return o < 0 ? 0 : o > r.rows ? r.rows : o;
+}
+// The operand's row for row r, -1 if the tables name none.
+__device__ inline int64_t source_row(const Rows& p, int64_t r) {
+  if (!p.row_slots) return r;
+  const int slot = p.row_slots[r];
+  return slot >= 0 && slot < p.rows ? slot / p.topk : -1;
+}
+// The expert whose rows hold row r, `experts` where none's do.
+__device__ inline int expert_of(const Rows& p, int64_t r) {
+  if (!p.offsets) return 0;
+  int low = 0, high = p.experts;  // the first e with offsets[e + 1] > r
+  while (low < high) {
+    const int mid = (low + high) / 2;
+    if (p.offsets[mid + 1] > r) high = mid;
+    else low = mid + 1;
+  }
+  return low;
+}
+
+// ---- activations --------------------------------------------------------------
+// 1 / (1 + e^-z). e^-z is infinite below -88.7, where the quotient is 0.
+__device__ inline float logistic(float z) { return 1.f / (1.f + exp_f32(-z)); }
+// silu(z) = z / (1 + e^-z); -inf gives 0 (its limit), as every z below -104.
+__device__ inline float silu(float z) { return z < -104.f ? 0.f : z * logistic(z); }
+// The normal distribution's function, 0.5 erfc(-z / sqrt 2): no cancellation for negative z.
+__device__ inline float normal_cdf(float z) { return 0.5f * erfcf(z * -0.707106781f); }
+__device__ inline float gelu(float z) { return z < -15.f ? 0.f : z * normal_cdf(z); }
+
+__device__ inline float activation(float z, int kind) {
+  switch (kind) {
+    case NVFP4_FFN_RELU: return z < 0.f ? 0.f : z;  // NaN stays
+    case NVFP4_FFN_SILU: return silu(z);
+    case NVFP4_FFN_GELU: return gelu(z);
+    default: return z;
+  }
+}
+// The activation (a) and its slope (s) at z. Where silu or gelu have reached their
+// limits, so have the slopes: 0, or 1 beyond.
+__device__ inline void activation_slope(float z, int kind, float& a, float& s) {
+  switch (kind) {
+    case NVFP4_FFN_RELU: a = z < 0.f ? 0.f : z; s = z > 0.f ? 1.f : z == z ? 0.f : z; return;
+    case NVFP4_FFN_SILU: {
+      const float p = logistic(z);
+      if (z < -104.f) { a = 0.f; s = 0.f; return; }
+      a = z * p;
+      s = z > 104.f ? 1.f : p * (1.f + z * (1.f - p));  // infinity: 1, not infinity times 0
+      return;
+    }
+    case NVFP4_FFN_GELU: {
+      const float p = normal_cdf(z);
+      if (z < -15.f) { a = 0.f; s = 0.f; return; }
+      a = z * p;
+      s = z > 15.f ? 1.f : p + z * 0.398942280f * exp_f32(z * z * -0.5f);
+      return;
+    }
+    default: a = z; s = 1.f; return;
+  }
+}
+
+// ---- rows in 8 bits -----------------------------------------------------------
+// A block of 32 elements has the scale 2^(byte - 127): the least, from 2^-126 on,
+// under which its largest element is at most 448, E4M3's largest value. Byte 255:
+// the block held an infinity or NaN, and all its values are NaN.
+constexpr int kBlock8 = 32;
+
+__device__ inline uint32_t abs_bits(float v) { return __builtin_bit_cast(uint32_t, v) & 0x7FFFFFFFu; }
+// The scale's byte from the bits of the largest magnitude (as integers, so that infinities and NaN are the largest).
+__device__ inline uint32_t scale8(uint32_t top) {
+  if (top >= 0x7F800000u) return 255;
+  // top = m 2^p, 1 <= m < 2, 448 = 1.75 * 2^8: 2^(p - 8) for m <= 1.75, else 2^(p - 7)
+  const int e = (int)(top >> 23) - 8 + ((top & 0x7FFFFFu) > 0x600000u);
+  return e < 1 ? 1 : e;
+}
+// 2^(byte - 127) and its inverse; byte 1 .. 246 as scale8 gives them.
+__device__ inline float scale8_value(uint32_t byte) { return __builtin_bit_cast(float, byte == 255 ? 0x7FC00000u : byte << 23); }
+__device__ inline float scale8_inverse(uint32_t byte) { return __builtin_bit_cast(float, byte == 255 ? 0x7FC00000u : (254u - byte) << 23); }
+// Four codes; the products are exact, so each code is rounded once (to nearest, ties to even).
+__device__ inline uint32_t encode4(float a, float b, float c, float d, float inverse) {
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32(a * inverse, b * inverse, 0, false);
+  w = __builtin_amdgcn_cvt_pk_fp8_f32(c * inverse, d * inverse, w, true);
+  return w;
+}
+__device__ inline void decode4(uint32_t w, float scale, float* v) {
+  const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(w, false), b = __builtin_amdgcn_cvt_pk_f32_fp8(w, true);
+  v[0] = a.x * scale;
+  v[1] = a.y * scale;
+  v[2] = b.x * scale;
+  v[3] = b.y * scale;
+}
+
+__device__ inline uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+__device__ inline float from_lane_xor(float v, int mask) { return __shfl_xor(v, mask, 64); }
+__device__ inline uint32_t from_lane_xor(uint32_t v, int mask) { return (uint32_t)__shfl_xor((int)v, mask, 64); }
+
+// A parameter of fp32 or of the rows' type T.
+template <class T> __device__ inline float param(const void* p, int64_t i, int f32) {
+  return f32 ? ((const float*)p)[i] : load1<T>(p, i);
+}
+template <class T> __device__ inline void param8(const void* p, int64_t i, int f32, bool vec, float* v) {
+  if (f32) load8<F32>(p, i, vec, v);
+  else load8<T>(p, i, vec, v);
+}
+
+// ---- host -----------------------------------------------------------------------
+inline bool known_activation(int a) { return a >= NVFP4_FFN_NONE && a <= NVFP4_FFN_GELU; }
+// Calls f with the tag of a 16-bit type.
+template <class Fn> inline auto with_type16(int dtype, Fn f) { return dtype == NVFP4_MOE_F16 ? f(F16{}) : f(BF16{}); }
+inline bool type16(int dtype) { return dtype == NVFP4_MOE_F16 || dtype == NVFP4_MOE_BF16; }
+
+// NVFP4_OK, or why the plan is none; fills rows.
+int plan_rows(const nvfp4_ffn_plan* plan, int64_t rows, bool gathered, Rows* out);
+// Compute units of the current device (256 if it cannot be asked).
+int compute_units();
+
+}  // namespace ffn
