@@ -14,6 +14,24 @@ typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 
+// Pairs of fp32 to 16 bits, to nearest even, by the card's own conversions.
+template <class T> __device__ __forceinline__ uint32_t pack16(float a, float b) {
+  if constexpr (T::kId == NVFP4_MOE_F16) {
+    return pack2<F16>(a, b);
+  } else {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    const f32x2 v = {a, b};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+  }
+}
+template <class T> __device__ __forceinline__ u32x4 pack16x8(const float* v) {
+  return u32x4{pack16<T>(v[0], v[1]), pack16<T>(v[2], v[3]), pack16<T>(v[4], v[5]), pack16<T>(v[6], v[7])};
+}
+template <class T> __device__ __forceinline__ void unpack16x8(u32x4 w, float* v) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) unpack2<T>(w[j], v[2 * j], v[2 * j + 1]);
+}
+
 // Where the rows sorted by expert lie: nvfp4_ffn_plan, or one expert with all rows.
 struct Rows {
   const int32_t* offsets;    // NULL: one expert, rows 0 .. rows-1

@@ -60,6 +60,14 @@ template <class T> __device__ __forceinline__ f32x16 mfma32(s16x8 a, s16x8 b, f3
   }
 }
 
+// f(0), f(1), .., f(N - 1), each a constant.
+template <int N, class Fn> __device__ __forceinline__ void each(Fn f) {
+  if constexpr (N > 0) {
+    each<N - 1>(f);
+    f(std::integral_constant<int, N - 1>{});
+  }
+}
+
 // ---- epilogues ------------------------------------------------------------------
 // What becomes of a product's sums. Columns come in eights at multiples of 8; every address is 16-byte aligned.
 struct Epilogue {
@@ -77,40 +85,34 @@ struct Epilogue {
   uint8_t *codes, *scales;
 };
 
+// Eight sums v of a row, the bias (b) and the residual (r) of their columns, 0 for none: z, its activation and y.
 // `live`: a row of an expert; the others become 0.
 template <class T>
-__device__ __forceinline__ void finish_linear(const Epilogue& p, int n, int e, bool live, int64_t row, int col, float* v) {
-  if (p.bias && live) {
-    float b[8];
-    param8<T>(p.bias, (int64_t)e * n + col, p.bias_f32, true, b);
+__device__ __forceinline__ void finish_linear(const Epilogue& p, int n, int64_t row, int col, float* v, const float* b, const float* r) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] += b[j];
-  }
-  if (p.z) store8<T>(p.z, row * n + col, true, v);
+  for (int j = 0; j < 8; ++j) v[j] += b[j];
+  if (p.z) *(u32x4*)((uint16_t*)p.z + row * n + col) = pack16x8<T>(v);
   if (p.act != NVFP4_FFN_NONE) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = activation(v[j], p.act);
   }
-  if (p.residual && live) {
-    float r[8];
-    load8<T>(p.residual, row * p.ldr + col, true, r);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] += r[j];
-  }
+  for (int j = 0; j < 8; ++j) v[j] += r[j];
   if (p.y_f32) store8<F32>(p.y, row * p.ldy + col, true, v);
-  else store8<T>(p.y, row * p.ldy + col, true, v);
+  else *(u32x4*)((uint16_t*)p.y + row * p.ldy + col) = pack16x8<T>(v);
 }
 // h, and g and u where they are kept in 16 bits, of eight columns.
 template <class T>
 __device__ __forceinline__ void finish_gated(const Epilogue& p, int64_t row, int col, const float* g, const float* u) {
   if (p.kept) {
-    store8<T>(p.kept, row * 2 * p.inner + col, true, g);
-    store8<T>(p.kept, row * 2 * p.inner + p.inner + col, true, u);
+    uint16_t* at = (uint16_t*)p.kept + row * 2 * p.inner + col;
+    *(u32x4*)at = pack16x8<T>(g);
+    *(u32x4*)(at + p.inner) = pack16x8<T>(u);
   }
   float h[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) h[j] = activation(g[j], p.act) * u[j];
-  store8<T>(p.y, row * p.ldy + col, true, h);
+  *(u32x4*)((uint16_t*)p.y + row * p.ldy + col) = pack16x8<T>(h);
 }
 __device__ __forceinline__ uint32_t top8(const float* v) {
   uint32_t top = abs_bits(v[0]);
@@ -118,11 +120,26 @@ __device__ __forceinline__ uint32_t top8(const float* v) {
   for (int j = 1; j < 8; ++j) top = umax(top, abs_bits(v[j]));
   return top;
 }
-__device__ __forceinline__ void store_codes8(uint8_t* at, const float* v, float inverse) {
-  u32x2 w;
-  w.x = encode4(v[0], v[1], v[2], v[3], inverse);
-  w.y = encode4(v[4], v[5], v[6], v[7], inverse);
-  *(u32x2*)at = w;
+// g and u in 8 bits: four lanes side by side hold a block of 32 columns (`in` alike in all four).
+__device__ __forceinline__ void finish_codes(const Epilogue& p, int64_t row, int col, bool in, const float* g, const float* u) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = h ? u[j] : g[j];
+    uint32_t top = top8(v);
+    top = umax(top, from_lane_xor(top, 1));
+    top = umax(top, from_lane_xor(top, 2));
+    if (!in) continue;
+    const uint32_t byte = scale8(top);
+    const float inverse = scale8_inverse(byte);
+    const int64_t k = row * 2 * p.inner + h * p.inner + col;
+    u32x2 w;
+    w.x = encode4(v[0], v[1], v[2], v[3], inverse);
+    w.y = encode4(v[4], v[5], v[6], v[7], inverse);
+    *(u32x2*)(p.codes + k) = w;
+    if (col % 32 == 0) p.scales[k / 32] = (uint8_t)byte;
+  }
 }
 
 // ---- the product ------------------------------------------------------------------
@@ -197,24 +214,19 @@ template <class T, int LAYOUT, int BX, int BK, int NW> struct Operand {
     }
   }
 
-  // Loads U0 .. U1-1 of the stage that begins at k, of which `left` elements are there (0 or less: none).
-  template <int U0, int U1> __device__ __forceinline__ void issue(uint32_t lds, int wave, int64_t k, int64_t left) const {
+  // The buffer of the stage that begins at k, of which `left` elements are there (0 or less: none).
+  __device__ __forceinline__ i32x4 stage(int64_t k, int64_t left) const {
     if constexpr (LAYOUT == kInside) {
-      const i32x4 r = buffer_at(base + k * 2, kMostBytes);
-      if (left >= BK) {
-#pragma unroll
-        for (int u = U0; u < U1; ++u) load_lds16(r, lds + (u * NW + wave) * 1024, voff[u]);
-      } else {
-        const bool there = chunk_k < left;
-#pragma unroll
-        for (int u = U0; u < U1; ++u) load_lds16(r, lds + (u * NW + wave) * 1024, there ? voff[u] : kOutside);
-      }
+      return buffer_at(base + k * 2, kMostBytes);
     } else {
       const int64_t lines = left < 0 ? 0 : left < BK ? left : BK;
-      const i32x4 r = buffer_at(base + k * ld_bytes, (int)(lines * ld_bytes));
-#pragma unroll
-      for (int u = U0; u < U1; ++u) load_lds16(r, lds + (u * NW + wave) * 1024, voff[u]);
+      return buffer_at(base + k * ld_bytes, (int)(lines * ld_bytes));
     }
+  }
+  // Load u of that stage.
+  template <int U> __device__ __forceinline__ void load(i32x4 buffer, uint32_t lds, int wave, int64_t left) const {
+    const bool there = LAYOUT == kOutsideK || chunk_k < left;
+    load_lds16(buffer, lds + (U * NW + wave) * 1024, there ? voff[U] : kOutside);
   }
 };
 
@@ -295,7 +307,7 @@ __global__ __launch_bounds__(256, PER_CU) void product_kernel(const Product p) {
   using A = Operand<T, AL, BM, BK, NW>;
   using B = Operand<T, BL, BN, BK, NW>;
   constexpr int STAGE = A::kBytes + B::kBytes, L = A::kLoads + B::kLoads;
-  static_assert(STEPS % 2 == 0 && NS >= 2 && (NS - 1) * L < 64, "fragments alternate, loads are counted");
+  static_assert(STEPS % 2 == 0 && NS >= 2 && (NS - 1) * L < 64 && A::kLoads <= MI && B::kLoads <= MI, "fragments alternate, loads are counted");
   static_assert(!GATED || (AL == kInside && BL == kInside && NI % 2 == 0 && BK == 32), "gate and up blocks of a wave");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[NS * STAGE];
   const uint32_t lds_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
@@ -388,143 +400,179 @@ __global__ __launch_bounds__(256, PER_CU) void product_kernel(const Product p) {
 
   if (stages > 0) {
     const int64_t k_end = min(at.k, (int64_t)(first + stages) * BK);
-    // Half H of the loads of stage s (of the tile's) to its buffer: A's or B's.
-    auto issue = [&](auto half, int s) __attribute__((always_inline)) {
-      const uint32_t to = lds_at + (uint32_t)(s % NS) * STAGE;
+    // Load u of A's or B's part of stage s (of the tile's) to its buffer.
+    struct Stage { i32x4 buffer; uint32_t lds; int64_t left; };
+    auto stage_a = [&](int s) __attribute__((always_inline)) {
       const int64_t k = (int64_t)(first + s) * BK;
-      if constexpr (decltype(half)::value == 0) a.template issue<0, A::kLoads>(to, wave, k, k_end - k);
-      else b.template issue<0, B::kLoads>(to + A::kBytes, wave, k, k_end - k);
+      return Stage{a.stage(k, k_end - k), lds_at + (uint32_t)(s % NS) * STAGE, k_end - k};
     };
-    std::integral_constant<int, 0> kA;
-    std::integral_constant<int, 1> kB;
+    auto stage_b = [&](int s) __attribute__((always_inline)) {
+      const int64_t k = (int64_t)(first + s) * BK;
+      return Stage{b.stage(k, k_end - k), lds_at + (uint32_t)(s % NS) * STAGE + A::kBytes, k_end - k};
+    };
+    auto load_a = [&](auto u, const Stage& s) __attribute__((always_inline)) { a.template load<decltype(u)::value>(s.buffer, s.lds, wave, s.left); };
+    auto load_b = [&](auto u, const Stage& s) __attribute__((always_inline)) { b.template load<decltype(u)::value>(s.buffer, s.lds, wave, s.left); };
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
-      issue(kA, s);
-      if (s < NS - 1) issue(kB, s);
+      const Stage sa = stage_a(s);
+      each<A::kLoads>([&](auto u) __attribute__((always_inline)) { load_a(u, sa); });
+      if (s < NS - 1) {
+        const Stage sb = stage_b(s);
+        each<B::kLoads>([&](auto u) __attribute__((always_inline)) { load_b(u, sb); });
+      }
     }
     s16x8 fa[2][MI], fb[2][NI];
-    auto read = [&](int buf, const uint8_t* stage, int step) __attribute__((always_inline)) {
-#pragma unroll
-      for (int j = 0; j < NI; ++j) fb[buf][j] = rb.read(stage + A::kBytes, j, step);
-#pragma unroll
-      for (int i = 0; i < MI; ++i) fa[buf][i] = ra.read(stage, i, step);
+    // Fragment f of a step: B's, then A's, as the MFMAs want them.
+    auto read = [&](int buf, const uint8_t* stage, int step, int f) __attribute__((always_inline)) {
+      if (f < NI) fb[buf][f] = rb.read(stage + A::kBytes, f, step);
+      else fa[buf][f - NI] = ra.read(stage, f - NI, step);
     };
     wait_loads<(NS - 2) * L + A::kLoads>();
     block_sync();
-    read(0, lds, 0);
+#pragma unroll
+    for (int f = 0; f < NI + MI; ++f) read(0, lds, 0, f);
     uint32_t now = 0;  // LDS offset of the stage under way
     for (int s = 0; s < stages; ++s) {
       const uint32_t next = now == (NS - 1) * STAGE ? 0 : now + STAGE;
-#pragma unroll
-      for (int t = 0; t < STEPS; ++t) {
-        if (t == STEPS - 1) {
+      Stage sb = stage_b(s + NS - 1), sa;
+      // a step: for every row block its share of the next step's reads, a load, its MFMAs
+      each<STEPS>([&](auto step) __attribute__((always_inline)) {
+        constexpr int t = decltype(step)::value;
+        if constexpr (t == STEPS - 1) {
+          sa = stage_a(s + NS);
           wait_loads<(NS - 2) * L>();
           block_sync();
-          issue(kA, s + NS);
         }
-        if (t == 0) issue(kB, s + NS - 1);
-        __builtin_amdgcn_sched_barrier(0);
-        read((t + 1) & 1, lds + (t == STEPS - 1 ? next : now), (t + 1) % STEPS);
+        each<MI>([&](auto block) __attribute__((always_inline)) {
+          constexpr int i = decltype(block)::value;
+          if constexpr (t == STEPS - 1 && i < A::kLoads) load_a(block, sa);
+          if constexpr (t == 0 && i < B::kLoads) load_b(block, sb);
 #pragma unroll
-        for (int i = 0; i < MI; ++i)
+          for (int f = i * (NI + MI) / MI; f < (i + 1) * (NI + MI) / MI; ++f)
+            read((t + 1) & 1, lds + (t == STEPS - 1 ? next : now), (t + 1) % STEPS, f);
 #pragma unroll
           for (int j = 0; j < NI; ++j) acc[i][j] = mfma32<T>(fb[t & 1][j], fa[t & 1][i], acc[i][j]);
-        // the reads of the next step among the MFMAs of this one
-        constexpr int READS = (AL == kInside ? MI : 2 * MI) + (BL == kInside ? NI : 2 * NI), PER = (READS + MI * NI - 1) / (MI * NI);
-#pragma unroll
-        for (int q = 0; q < READS / PER; ++q) {
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-          __builtin_amdgcn_sched_group_barrier(0x100, PER, 0);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      }
+          __builtin_amdgcn_sched_barrier(0);
+        });
+      });
       now = next;
     }
-    wait_loads<0>();  // nothing is written to LDS after the workgroup's end
+    // nothing more is written to the stages, nor read from them
+    wait_loads<0>();
+    block_sync();
   }
 
-  // ---- the epilogue. A lane holds row lane % 32 of a block, and of its columns four of
-  // every eight; one exchange with the lane 32 away gives it eight columns side by side.
-  const int half = lane >> 5;
-  auto columns8 = [&](const f32x16& c, int part, float* v) __attribute__((always_inline)) {
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      // copies: bit_cast of a vector's element itself takes the first one
-      const float low = c[part * 8 + r], high = c[part * 8 + 4 + r];
-      const auto x = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, low), __builtin_bit_cast(uint32_t, high), false, false);
-      const uint32_t first = x[0], second = x[1];
-      v[r] = __builtin_bit_cast(float, first);
-      v[r + 4] = __builtin_bit_cast(float, second);
-    }
+  // ---- the epilogue. A lane holds row lane % 32 of a block and four of every eight columns: 32 rows at a time go
+  // through LDS (of the wave's own), so that a row's lanes then have eight columns each side by side, and global
+  // loads and stores take whole lines. Rows are padded by 16 bytes: 16 lanes' writes take all banks once.
+  constexpr int C = BN / 2, ROOM = C + 4;             // columns of a wave
+  constexpr int LANES = (GATED ? C / 2 : C) / 8;      // of a row
+  constexpr int PASS = 64 / LANES, PASSES = 32 / PASS;
+  static_assert(4 * 32 * ROOM * 4 <= NS * STAGE, "the stages hold the waves' rooms");
+  float* room = (float*)lds + wave * 32 * ROOM;
+  const int my_row = lane / LANES, my_col = lane % LANES * 8;
+  const int col = at.col + wn * (GATED ? C / 2 : C) + my_col;
+  const int64_t row0 = at.row + wm * (BM / 2) + my_row;
+  const bool in_cols = col < (GATED ? p.ep.inner : p.n), parts = p.splits > 1;
+  const int64_t out0 = OVER_K ? at.expert * p.m : 0;  // output row of the tile's row 0
+  float* partial = parts ? p.partial + at.split * p.partial_step + out0 * p.n : nullptr;
+  const bool has_bias = !GATED && BL == kInside && p.ep.bias && at.live && !parts;
+  const bool has_residual = !GATED && BL == kInside && p.ep.residual && at.live && !parts;
+  float bias[8] = {};
+  if (has_bias && in_cols) param8<T>(p.ep.bias, (int64_t)at.expert * p.n + col, p.ep.bias_f32, true, bias);
+  // the residual of a pass; out of range: 0
+  auto residual_at = [&](int64_t row) __attribute__((always_inline)) {
+    return row < at.rows && in_cols ? *(const u32x4*)((const uint16_t*)p.ep.residual + row * p.ep.ldr + col) : u32x4{0, 0, 0, 0};
   };
+  constexpr bool GRADIENT = BL == kOutsideK;  // no bias, activation or residual
+  const bool plain = !GATED && !parts && !p.ep.y_f32 && (GRADIENT || (p.ep.act == NVFP4_FFN_NONE && !p.ep.z));
+  u32x4 residual[PASSES];
+  if (has_residual && plain) {
 #pragma unroll
-  for (int i = 0; i < MI; ++i) {
-    const int64_t row = at.row + wm * (BM / 2) + i * 32 + (lane & 31);
-    const bool in = row < at.rows;
-    if constexpr (GATED) {
+    for (int q = 0; q < PASSES; ++q) residual[q] = residual_at(row0 + q * PASS);
+  }
+  each<MI>([&](auto block) __attribute__((always_inline)) {
+    constexpr int i = decltype(block)::value;
+    // a wave's LDS operations keep their order; the fence keeps the compiler to it
+    wave_sync();
 #pragma unroll
-      for (int j = 0; j < NI / 2; ++j) {
-        const int col0 = at.col + wn * (BN / 4) + j * 32;
-        float g[2][8], u[2][8];
+    for (int j = 0; j < NI; ++j)
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          columns8(acc[i][j], q, g[q]);
-          columns8(acc[i][j + NI / 2], q, u[q]);
+      for (int q = 0; q < 4; ++q) {
+        const f32x4 v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+        *(f32x4*)(room + (lane & 31) * ROOM + j * 32 + 8 * q + 4 * (lane >> 5)) = v;
+      }
+    wave_sync();
+    const float* from = room + my_row * ROOM + my_col;
+    const int64_t first_of = row0 + i * 32;
+    if constexpr (!GATED) {
+      if (plain) {
+        // (the next block's residual is under way before this one's stores, which its wait would else include)
+        u32x4 mine[PASSES];
+        if (has_residual) {
+#pragma unroll
+          for (int q = 0; q < PASSES; ++q) {
+            mine[q] = residual[q];
+            if (i + 1 < MI) residual[q] = residual_at(first_of + 32 + q * PASS);
+          }
         }
-        if (p.splits > 1) {
-          float* to = p.partial + at.split * p.partial_step + row * p.n;
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const int col = col0 + 16 * q + 8 * half;
-            if (in && col < p.ep.inner) {
-              store8<F32>(to, col, true, g[q]);
-              store8<F32>(to, p.ep.inner + col, true, u[q]);
-            }
+        for (int q = 0; q < PASSES; ++q) {
+          const int64_t row = first_of + q * PASS;
+          float v[8];
+          load8<F32>(from, q * PASS * ROOM, true, v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] += bias[j];
+          if (has_residual) {
+            float r[8];
+            unpack16x8<T>(mine[q], r);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] += r[j];
+          }
+          if (row < at.rows && in_cols) *(u32x4*)((uint16_t*)p.ep.y + (out0 + row) * p.ep.ldy + col) = pack16x8<T>(v);
+        }
+        return;
+      }
+      u32x4 next = has_residual ? residual_at(first_of) : u32x4{0, 0, 0, 0};
+#pragma unroll 1
+      for (int q = 0; q < PASSES; ++q) {
+        const int64_t row = first_of + q * PASS;
+        const u32x4 mine = next;
+        if (has_residual && q + 1 < PASSES) next = residual_at(row + PASS);
+        float v[8], r[8];
+        load8<F32>(from, q * PASS * ROOM, true, v);
+        if (row >= at.rows || !in_cols) continue;
+        if (parts) {
+          store8<F32>(partial, row * p.n + col, true, v);
+          continue;
+        }
+        if constexpr (GRADIENT) {  // fp32
+          store8<F32>(p.ep.y, (out0 + row) * p.ep.ldy + col, true, v);
+          continue;
+        }
+        unpack16x8<T>(mine, r);
+        finish_linear<T>(p.ep, p.n, out0 + row, col, v, bias, r);
+      }
+    } else {
+#pragma unroll 1
+      for (int q = 0; q < PASSES; ++q) {
+        const int64_t row = first_of + q * PASS;
+        const bool in = row < at.rows && in_cols;
+        float g[8], u[8];
+        load8<F32>(from, q * PASS * ROOM, true, g);
+        load8<F32>(from, q * PASS * ROOM + C / 2, true, u);
+        if (parts) {
+          if (in) {
+            store8<F32>(partial, row * p.n + col, true, g);
+            store8<F32>(partial, row * p.n + p.ep.inner + col, true, u);
           }
           continue;
         }
-        if (p.ep.codes) {
-#pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            const float(&v)[2][8] = w ? u : g;
-            uint32_t top = umax(top8(v[0]), top8(v[1]));
-            top = umax(top, from_lane_xor(top, 32));
-            const uint32_t byte = scale8(top);
-            if (in && col0 < p.ep.inner) {
-              const int64_t k = row * 2 * p.ep.inner + w * p.ep.inner + col0;
-#pragma unroll
-              for (int q = 0; q < 2; ++q) store_codes8(p.ep.codes + k + 16 * q + 8 * half, v[q], scale8_inverse(byte));
-              if (half == 0) p.ep.scales[k / 32] = (uint8_t)byte;
-            }
-          }
-        }
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int col = col0 + 16 * q + 8 * half;
-          if (in && col < p.ep.inner) finish_gated<T>(p.ep, row, col, g[q], u[q]);
-        }
+        if (p.ep.codes) finish_codes(p.ep, row, col, in, g, u);
+        if (in) finish_gated<T>(p.ep, row, col, g, u);
       }
-    } else {
-#pragma unroll
-      for (int j = 0; j < NI; ++j)
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int col = at.col + wn * (BN / 2) + j * 32 + 16 * q + 8 * half;
-          float v[8];
-          columns8(acc[i][j], q, v);
-          if (in && col < p.n) {
-            if (p.splits > 1) {
-              store8<F32>(p.partial + at.split * p.partial_step + ((OVER_K ? at.expert * p.m : 0) + row) * p.n, col, true, v);
-            } else if constexpr (OVER_K) {
-              Epilogue ep = p.ep;
-              finish_linear<T>(ep, p.n, 0, true, at.expert * p.m + row, col, v);
-            } else {
-              finish_linear<T>(p.ep, p.n, at.expert, at.live, row, col, v);
-            }
-          }
-        }
     }
-  }
+  });
 }
 
 // ---- host: sizes of tiles, parts of k ----------------------------------------------

@@ -92,24 +92,14 @@ template <class T, bool GATED, bool OVER_K> __global__ __launch_bounds__(256) vo
     }
   }
   if constexpr (GATED) {
-    if (p.ep.codes) {
-      // 32 columns are those of four threads: inner % 32 == 0
-      for (int h = 0; h < 2; ++h) {
-        const float(&x)[8] = h ? u : v;
-        uint32_t top = top8(x);
-        top = umax(top, from_lane_xor(top, 1));
-        top = umax(top, from_lane_xor(top, 2));
-        const uint32_t byte = scale8(top);
-        const int64_t k = row * p.n + h * p.ep.inner + col;
-        if (in) {
-          store_codes8(p.ep.codes + k, x, scale8_inverse(byte));
-          if (k % 32 == 0) p.ep.scales[k / 32] = (uint8_t)byte;
-        }
-      }
-    }
+    if (p.ep.codes) finish_codes(p.ep, row, col, in, v, u);  // (inner % 32 == 0: a row's lanes come in fours)
     if (in) finish_gated<T>(p.ep, row, col, v, u);
   } else {
-    if (in) finish_linear<T>(p.ep, p.n, e, live, row, col, v);
+    if (!in) return;
+    float b[8] = {}, r[8] = {};
+    if (p.ep.bias && live) param8<T>(p.ep.bias, (int64_t)e * p.n + col, p.ep.bias_f32, true, b);
+    if (p.ep.residual && live) load8<T>(p.ep.residual, row * p.ep.ldr + col, true, r);
+    finish_linear<T>(p.ep, p.n, row, col, v, b, r);
   }
 }
 
