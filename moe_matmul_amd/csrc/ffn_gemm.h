@@ -301,19 +301,20 @@ template <int BM> __device__ __forceinline__ bool find_rows(const Rows& p, int64
   return false;
 }
 
-template <class T, int AL, int BL, bool GATED, int BM, int BN, int BK, int NS, int PER_CU>
-__global__ __launch_bounds__(256, PER_CU) void product_kernel(const Product p) {
-  constexpr int NW = 4, MI = BM / 64, NI = BN / 64, STEPS = BK / 16;
+template <class T, int AL, int BL, bool GATED, int BM, int BN, int WM, int WN, int BK, int NS, int PER_SIMD>
+__global__ __launch_bounds__(64 * WM * WN, PER_SIMD) void product_kernel(const Product p) {
+  constexpr int NW = WM * WN, TM = BM / WM, TN = BN / WN;  // a wave's part of the tile
+  constexpr int MI = TM / 32, NI = TN / 32, STEPS = BK / 16;
   using A = Operand<T, AL, BM, BK, NW>;
   using B = Operand<T, BL, BN, BK, NW>;
   constexpr int STAGE = A::kBytes + B::kBytes, L = A::kLoads + B::kLoads;
   static_assert(STEPS % 2 == 0 && NS >= 2 && (NS - 1) * L < 64 && A::kLoads <= MI && B::kLoads <= MI, "fragments alternate, loads are counted");
-  static_assert(!GATED || (AL == kInside && BL == kInside && NI % 2 == 0 && BK == 32), "gate and up blocks of a wave");
+  static_assert(!GATED || (AL == kInside && BL == kInside && NI % 2 == 0), "gate and up blocks of a wave");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[NS * STAGE];
   const uint32_t lds_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave >> 1, wn = wave & 1;
+  const int wm = wave / WN, wn = wave % WN;
 
   // ---- the tile
   Place at;
@@ -376,7 +377,7 @@ __global__ __launch_bounds__(256, PER_CU) void product_kernel(const Product p) {
   if constexpr (GATED) {
     // blocks of a wave's columns: gate rows in the first half, the same columns' up rows in the second
     b.set_inside(be + at.col * p.ldb, p.ldb, wave, lane, [&](int line) {
-      const int j = line % (BN / 2) / 32, col = line / (BN / 2) * (BN / 4) + j % (NI / 2) * 32 + line % 32;
+      const int j = line % TN / 32, col = line / TN * (TN / 2) + j % (NI / 2) * 32 + line % 32;
       return at.col + col < p.ep.inner ? (int64_t)col + (j < NI / 2 ? 0 : p.ep.inner) : (int64_t)-1;
     });
   } else if constexpr (BL == kInside) {
@@ -387,8 +388,8 @@ __global__ __launch_bounds__(256, PER_CU) void product_kernel(const Product p) {
   }
   Reader<AL, BM, BK, MI> ra;
   Reader<BL, BN, BK, NI> rb;
-  ra.set(wm * (BM / 2), lane);
-  rb.set(wn * (BN / 2), lane);
+  ra.set(wm * TM, lane);
+  rb.set(wn * TN, lane);
 
   f32x16 acc[MI][NI];
 #pragma unroll
@@ -465,14 +466,14 @@ __global__ __launch_bounds__(256, PER_CU) void product_kernel(const Product p) {
   // ---- the epilogue. A lane holds row lane % 32 of a block and four of every eight columns: 32 rows at a time go
   // through LDS (of the wave's own), so that a row's lanes then have eight columns each side by side, and global
   // loads and stores take whole lines. Rows are padded by 16 bytes: 16 lanes' writes take all banks once.
-  constexpr int C = BN / 2, ROOM = C + 4;             // columns of a wave
+  constexpr int C = TN, ROOM = C + 4;                 // columns of a wave
   constexpr int LANES = (GATED ? C / 2 : C) / 8;      // of a row
   constexpr int PASS = 64 / LANES, PASSES = 32 / PASS;
-  static_assert(4 * 32 * ROOM * 4 <= NS * STAGE, "the stages hold the waves' rooms");
+  static_assert(NW * 32 * ROOM * 4 <= NS * STAGE, "the stages hold the waves' rooms");
   float* room = (float*)lds + wave * 32 * ROOM;
   const int my_row = lane / LANES, my_col = lane % LANES * 8;
   const int col = at.col + wn * (GATED ? C / 2 : C) + my_col;
-  const int64_t row0 = at.row + wm * (BM / 2) + my_row;
+  const int64_t row0 = at.row + wm * TM + my_row;
   const bool in_cols = col < (GATED ? p.ep.inner : p.n), parts = p.splits > 1;
   const int64_t out0 = OVER_K ? at.expert * p.m : 0;  // output row of the tile's row 0
   float* partial = parts ? p.partial + at.split * p.partial_step + out0 * p.n : nullptr;
@@ -602,8 +603,8 @@ template <class T, int AL, int BL, bool GATED> inline int launch_product(Product
   }
   if (OVER_K || !p.rows.offsets) tiles *= p.splits;
   if (tiles > 0x7FFFFF) return NVFP4_ERR_INVALID;
-  if (t.big) product_kernel<T, AL, BL, GATED, 256, 256, 32, 4, 1><<<(int)tiles, 256, 0, stream>>>(p);
-  else product_kernel<T, AL, BL, GATED, 128, 128, 32, 4, 2><<<(int)tiles, 256, 0, stream>>>(p);
+  if (t.big) product_kernel<T, AL, BL, GATED, 256, 256, 2, 4, AL == kInside ? 64 : 32, AL == kInside ? 2 : 4, 2><<<(int)tiles, 512, 0, stream>>>(p);
+  else product_kernel<T, AL, BL, GATED, 128, 128, 2, 2, 32, 4, 2><<<(int)tiles, 256, 0, stream>>>(p);
   return launched();
 }
 
