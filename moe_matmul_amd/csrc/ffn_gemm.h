@@ -308,7 +308,7 @@ __global__ __launch_bounds__(64 * WM * WN, PER_SIMD) void product_kernel(const P
   using A = Operand<T, AL, BM, BK, NW>;
   using B = Operand<T, BL, BN, BK, NW>;
   constexpr int STAGE = A::kBytes + B::kBytes, L = A::kLoads + B::kLoads;
-  static_assert(STEPS % 2 == 0 && NS >= 2 && (NS - 1) * L < 64 && A::kLoads <= MI && B::kLoads <= MI, "fragments alternate, loads are counted");
+  static_assert(STEPS % 2 == 0 && NS >= 2 && (NS - 1) * L < 64, "fragments alternate, loads are counted");
   static_assert(!GATED || (AL == kInside && BL == kInside && NI % 2 == 0), "gate and up blocks of a wave");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[NS * STAGE];
   const uint32_t lds_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
@@ -432,7 +432,13 @@ __global__ __launch_bounds__(64 * WM * WN, PER_SIMD) void product_kernel(const P
     block_sync();
 #pragma unroll
     for (int f = 0; f < NI + MI; ++f) read(0, lds, 0, f);
-    uint32_t now = 0;  // LDS offset of the stage under way
+    // Blocks of 32 rows of this wave that the output has; a tile without some skips their reads and MFMAs (not its
+    // loads and barriers).
+    const int64_t rows_left = at.rows - at.row - wm * TM;
+    const int active = rows_left >= TM ? MI : rows_left > 0 ? (int)(rows_left + 31) / 32 : 0;
+    auto run = [&](auto whole) __attribute__((always_inline)) {
+      constexpr bool WHOLE = decltype(whole)::value;
+      uint32_t now = 0;  // LDS offset of the stage under way
     for (int s = 0; s < stages; ++s) {
       const uint32_t next = now == (NS - 1) * STAGE ? 0 : now + STAGE;
       Stage sb = stage_b(s + NS - 1), sa;
@@ -446,11 +452,17 @@ __global__ __launch_bounds__(64 * WM * WN, PER_SIMD) void product_kernel(const P
         }
         each<MI>([&](auto block) __attribute__((always_inline)) {
           constexpr int i = decltype(block)::value;
-          if constexpr (t == STEPS - 1 && i < A::kLoads) load_a(block, sa);
-          if constexpr (t == 0 && i < B::kLoads) load_b(block, sb);
+          if constexpr (t == STEPS - 1) each<A::kLoads>([&](auto u) __attribute__((always_inline)) {
+            if constexpr (decltype(u)::value * MI / A::kLoads == i) load_a(u, sa);
+          });
+          if constexpr (t == 0) each<B::kLoads>([&](auto u) __attribute__((always_inline)) {
+            if constexpr (decltype(u)::value * MI / B::kLoads == i) load_b(u, sb);
+          });
 #pragma unroll
           for (int f = i * (NI + MI) / MI; f < (i + 1) * (NI + MI) / MI; ++f)
-            read((t + 1) & 1, lds + (t == STEPS - 1 ? next : now), (t + 1) % STEPS, f);
+            if (WHOLE || (f < NI ? 0 : f - NI) < active)
+              read((t + 1) & 1, lds + (t == STEPS - 1 ? next : now), (t + 1) % STEPS, f);
+          if (WHOLE || i < active)
 #pragma unroll
           for (int j = 0; j < NI; ++j) acc[i][j] = mfma32<T>(fb[t & 1][j], fa[t & 1][i], acc[i][j]);
           __builtin_amdgcn_sched_barrier(0);
@@ -458,6 +470,9 @@ __global__ __launch_bounds__(64 * WM * WN, PER_SIMD) void product_kernel(const P
       });
       now = next;
     }
+    };
+    if (at.rows - at.row >= BM) run(std::true_type{});
+    else run(std::false_type{});
     // nothing more is written to the stages, nor read from them
     wait_loads<0>();
     block_sync();
@@ -578,7 +593,7 @@ __global__ __launch_bounds__(64 * WM * WN, PER_SIMD) void product_kernel(const P
 
 // ---- host: sizes of tiles, parts of k ----------------------------------------------
 struct Tiling {
-  int big;     // 256 x 256 tiles, else 128 x 128
+  int shape;   // 0: 128 x 128, 1: 256 x 128, 2: 256 x 256
   int splits;
 };
 // For tiles of rows (at most `rows` of them, by experts) and cols, k long; over_k: rows x cols of each expert.
@@ -588,7 +603,7 @@ int finish_splits(const Product& p, int dtype, bool gated, bool over_k, void* st
 
 template <class T, int AL, int BL, bool GATED> inline int launch_product(Product& p, const Tiling& t, hipStream_t stream) {
   constexpr bool OVER_K = AL == kOutsideK;
-  const int bm = t.big ? 256 : 128, cols = (t.big ? 256 : 128) / (GATED ? 2 : 1);
+  const int bm = t.shape ? 256 : 128, cols = (t.shape == 2 ? 256 : 128) / (GATED ? 2 : 1);
   p.splits = t.splits;
   p.tiles_m = (int)ceil_div64(p.m, bm);
   p.tiles_n = ceil_div(GATED ? p.ep.inner : p.n, cols);
@@ -603,8 +618,11 @@ template <class T, int AL, int BL, bool GATED> inline int launch_product(Product
   }
   if (OVER_K || !p.rows.offsets) tiles *= p.splits;
   if (tiles > 0x7FFFFF) return NVFP4_ERR_INVALID;
-  if (t.big) product_kernel<T, AL, BL, GATED, 256, 256, 2, 4, AL == kInside ? 64 : 32, AL == kInside ? 2 : 4, 2><<<(int)tiles, 512, 0, stream>>>(p);
-  else product_kernel<T, AL, BL, GATED, 128, 128, 2, 2, 32, 4, 2><<<(int)tiles, 256, 0, stream>>>(p);
+  constexpr int BK = AL == kInside ? 64 : 32;
+  const dim3 grid((unsigned)tiles);
+  if (t.shape == 2) product_kernel<T, AL, BL, GATED, 256, 256, 2, 4, BK, 128 / BK, 2><<<grid, 512, 0, stream>>>(p);
+  else if (t.shape == 1) product_kernel<T, AL, BL, GATED, 256, 128, 4, 2, BK, 192 / BK, 2><<<grid, 512, 0, stream>>>(p);
+  else product_kernel<T, AL, BL, GATED, 128, 128, 2, 2, BK, 128 / BK, 2><<<grid, 256, 0, stream>>>(p);
   return launched();
 }
 

@@ -1,5 +1,7 @@
 // Entry points of the products of nvfp4_ffn.h: argument checks, the choice of tiles
 // and of parts of k, and the kernel that adds the parts.
+#include <math.h>
+
 #include "ffn_gemm.h"
 
 namespace moe {
@@ -43,22 +45,43 @@ int plan_rows(const nvfp4_ffn_plan* plan, int64_t rows, bool gathered, Rows* out
   return NVFP4_OK;
 }
 
+// The tiles and parts of k that take least by a model of the kernels' times in microseconds: a round of tiles over the
+// compute units (two small ones to a unit) has a fixed part and one for every 64 k, measured on products that
+// fill whole rounds (4096 x 4096 x 2048 and 8192: 59 and 214, 64 and 241, 66 and 259 for 256 x 256, 256 x 128 and
+// 128 x 128); a last row of tiles that is mostly empty costs about two fifths of a whole one; parts are written and
+// read at some 4 TB/s, in a launch of their own.
 Tiling choose_tiling(int64_t rows, int cols, int64_t k, int experts, bool over_k, int units) {
-  const int64_t e = over_k ? experts : 1, parts = over_k || experts == 1 ? 0 : (experts < rows ? experts : rows) / 2;
-  const int64_t big = (ceil_div64(rows, 256) + parts) * ceil_div(cols, 256) * e;
-  const int64_t small = (ceil_div64(rows, 128) + parts) * ceil_div(cols, 128) * e;
-  Tiling t{0, 1};
-  const double rounds_big = (double)ceil_div64(big, units), rounds_small = (double)ceil_div64(small, 2 * units) * 0.62;
-  if (big >= units / 2 && rounds_big <= rounds_small) {
-    t.big = 1;
-    return t;
+  static const double kFixed[3] = {7, 8, 9}, kStage[3] = {0.97, 0.92, 1.6}, kAlone[3] = {0.62, 0.92, 1.6};
+  const double e = over_k ? experts : 1;
+  const double stages = (double)ceil_div64(k > 0 ? k : 1, 64);
+  Tiling best{0, 1};
+  double least = 1e30;
+  for (int shape = 0; shape < 3; ++shape) {
+    const int bm = shape ? 256 : 128, bn = shape == 2 ? 256 : 128;
+    const double tail = (double)(rows % bm) / bm;
+    double high = rows / bm + (tail > 0 ? (tail > 0.4 ? tail : 0.4) : 0);
+    if (!over_k && experts > 1) {
+      // every expert has a last row of tiles, half full
+      const double some = (double)(experts < rows ? experts : rows);
+      high = (double)rows / bm + 0.4 * some;
+      if (high < some) high = some;
+    }
+    const double tiles = high * ceil_div(cols, bn) * e;
+    for (int splits = 1; splits <= 16; splits += splits < 4 ? 1 : splits < 8 ? 2 : 4) {
+      if (splits > 1 && stages / splits < 4) break;
+      const double all = tiles * splits, room = shape ? units : 2.0 * units;
+      const double whole = floor(all / room), rest = all - whole * room;
+      const double part = stages / splits;
+      double t = whole * (kFixed[shape] + part * kStage[shape]);
+      if (rest > 0.01) t += kFixed[shape] + part * (rest <= units ? kAlone[shape] : kStage[shape]);
+      if (splits > 1) t += 4 + (double)rows * cols * e * 4 * 2 * splits / 4e6;
+      if (t < least) {
+        least = t;
+        best = Tiling{shape, splits};
+      }
+    }
   }
-  const int64_t stages = ceil_div64(k, 32);
-  if (small < units) {
-    const int64_t s = min(min(2 * units / max(small, (int64_t)1), stages / 8), (int64_t)16);
-    t.splits = s > 1 ? (int)s : 1;
-  }
-  return t;
+  return best;
 }
 
 // ---- the parts of k ---------------------------------------------------------------
