@@ -135,7 +135,7 @@ int nvfp4_ffn_gated(const void* x, int64_t x_stride, const void* w, int act, voi
                     void* workspace, size_t workspace_bytes, void* stream);
 
 /* Bytes of workspace of a product [rows][k] x [n][k] (also of nvfp4_ffn_linear_dx with n and k in turn: [rows][n] x
- * [k][n]); experts 0 or 1: dense. */
+ * [k][n]); experts 0: dense, else the plan's. */
 size_t nvfp4_ffn_product_workspace_bytes(int64_t rows, int n, int k, int experts);
 
 /*

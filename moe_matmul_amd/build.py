@@ -25,7 +25,7 @@ MOE_SOURCES = [os.path.join(HERE, "csrc", f) for f in
 MOE_LIB = os.path.join(HERE, "libnvfp4_moe.so")
 # the feed-forward block in 16 bits and its training (include/nvfp4_ffn.h)
 FFN_SOURCES = [os.path.join(HERE, "csrc", f) for f in
-               ("ffn_product.hip", "ffn_gemm_forward.hip", "ffn_gemm_dx.hip", "ffn_gemm_dw.hip", "ffn_norm.hip",
+               ("ffn_product.hip", "ffn_few.hip", "ffn_gemm_forward.hip", "ffn_gemm_dx.hip", "ffn_gemm_dw.hip", "ffn_norm.hip",
                 "ffn_rows.hip")]
 FFN_LIB = os.path.join(HERE, "libnvfp4_ffn.so")
 # measurement kernels behind the mainloop choice (not part of the GEMM)

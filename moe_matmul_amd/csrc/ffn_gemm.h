@@ -593,17 +593,12 @@ __global__ __launch_bounds__(64 * WM * WN, PER_SIMD) void product_kernel(const P
 
 // ---- host: sizes of tiles, parts of k ----------------------------------------------
 struct Tiling {
-  int shape;   // 0: 128 x 128, 1: 256 x 128, 2: 256 x 256
+  int shape;   // 0: 128 x 128, 1: 256 x 128, 2: 256 x 256, 3: 64 x 128 (rows with k inside)
   int splits;
 };
-// For tiles of rows (at most `rows` of them, by experts) and cols, k long; over_k: rows x cols of each expert.
-Tiling choose_tiling(int64_t rows, int cols, int64_t k, int experts, bool over_k, int units);
-// Adds the parts of k and applies the epilogue.
-int finish_splits(const Product& p, int dtype, bool gated, bool over_k, void* stream);
-
 template <class T, int AL, int BL, bool GATED> inline int launch_product(Product& p, const Tiling& t, hipStream_t stream) {
   constexpr bool OVER_K = AL == kOutsideK;
-  const int bm = t.shape ? 256 : 128, cols = (t.shape == 2 ? 256 : 128) / (GATED ? 2 : 1);
+  const int bm = t.shape == 3 ? 64 : t.shape ? 256 : 128, cols = (t.shape == 2 ? 256 : 128) / (GATED ? 2 : 1);
   p.splits = t.splits;
   p.tiles_m = (int)ceil_div64(p.m, bm);
   p.tiles_n = ceil_div(GATED ? p.ep.inner : p.n, cols);
@@ -622,7 +617,8 @@ template <class T, int AL, int BL, bool GATED> inline int launch_product(Product
   const dim3 grid((unsigned)tiles);
   if (t.shape == 2) product_kernel<T, AL, BL, GATED, 256, 256, 2, 4, BK, 128 / BK, 2><<<grid, 512, 0, stream>>>(p);
   else if (t.shape == 1) product_kernel<T, AL, BL, GATED, 256, 128, 4, 2, BK, 192 / BK, 2><<<grid, 512, 0, stream>>>(p);
-  else product_kernel<T, AL, BL, GATED, 128, 128, 2, 2, BK, 128 / BK, 2><<<grid, 256, 0, stream>>>(p);
+  else if (t.shape == 0) product_kernel<T, AL, BL, GATED, 128, 128, 2, 2, BK, 128 / BK, 2><<<grid, 256, 0, stream>>>(p);
+  else if constexpr (AL == kInside) product_kernel<T, AL, BL, GATED, 64, 128, 2, 2, BK, 3, 2><<<grid, 256, 0, stream>>>(p);
   return launched();
 }
 

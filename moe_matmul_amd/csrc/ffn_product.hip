@@ -10,6 +10,7 @@ thread_local int t_last_hip_error = 0;
 
 namespace ffn {
 
+int run_few(const Product& p, int dtype, bool gated, hipStream_t stream);
 int run_forward(Product& p, const Tiling& t, int dtype, bool gated, hipStream_t stream);
 int run_dx(Product& p, const Tiling& t, int dtype, hipStream_t stream);
 int run_dw(Product& p, const Tiling& t, int dtype, hipStream_t stream);
@@ -48,16 +49,18 @@ int plan_rows(const nvfp4_ffn_plan* plan, int64_t rows, bool gathered, Rows* out
 // The tiles and parts of k that take least by a model of the kernels' times in microseconds: a round of tiles over the
 // compute units (two small ones to a unit) has a fixed part and one for every 64 k, measured on products that
 // fill whole rounds (4096 x 4096 x 2048 and 8192: 59 and 214, 64 and 241, 66 and 259 for 256 x 256, 256 x 128 and
-// 128 x 128); a last row of tiles that is mostly empty costs about two fifths of a whole one; parts are written and
+// 128 x 128; 64 x 4096 x 7168 in 4 and 8 parts of 64 x 128: 14 and 12); a last row of tiles that is mostly empty costs about two fifths of a whole one; parts are written and
 // read at some 4 TB/s, in a launch of their own.
-Tiling choose_tiling(int64_t rows, int cols, int64_t k, int experts, bool over_k, int units) {
-  static const double kFixed[3] = {7, 8, 9}, kStage[3] = {0.97, 0.92, 1.6}, kAlone[3] = {0.62, 0.92, 1.6};
+static Tiling choose_tiling(int64_t rows, int cols, int64_t k, int experts, bool over_k, int units, double* time) {
+  static const double kFixed[4] = {7, 8, 9, 4}, kStage[4] = {0.97, 0.92, 1.6, 0.7}, kAlone[4] = {0.62, 0.92, 1.6, 0.4};
   const double e = over_k ? experts : 1;
   const double stages = (double)ceil_div64(k > 0 ? k : 1, 64);
   Tiling best{0, 1};
   double least = 1e30;
-  for (int shape = 0; shape < 3; ++shape) {
-    const int bm = shape ? 256 : 128, bn = shape == 2 ? 256 : 128;
+  // the weights' (or rows') own bytes
+  const double streamed = 5 + (double)cols * k * 2 * (over_k ? e : experts < rows ? experts : rows) / 5e6;
+  for (int shape = 0; shape < (over_k ? 3 : 4); ++shape) {
+    const int bm = shape == 3 ? 64 : shape ? 256 : 128, bn = shape == 2 ? 256 : 128;
     const double tail = (double)(rows % bm) / bm;
     double high = rows / bm + (tail > 0 ? (tail > 0.4 ? tail : 0.4) : 0);
     if (!over_k && experts > 1) {
@@ -69,11 +72,12 @@ Tiling choose_tiling(int64_t rows, int cols, int64_t k, int experts, bool over_k
     const double tiles = high * ceil_div(cols, bn) * e;
     for (int splits = 1; splits <= 16; splits += splits < 4 ? 1 : splits < 8 ? 2 : 4) {
       if (splits > 1 && stages / splits < 4) break;
-      const double all = tiles * splits, room = shape ? units : 2.0 * units;
+      const double all = tiles * splits, room = shape == 1 || shape == 2 ? units : 2.0 * units;
       const double whole = floor(all / room), rest = all - whole * room;
       const double part = stages / splits;
       double t = whole * (kFixed[shape] + part * kStage[shape]);
       if (rest > 0.01) t += kFixed[shape] + part * (rest <= units ? kAlone[shape] : kStage[shape]);
+      if (t < streamed) t = streamed;
       if (splits > 1) t += 4 + (double)rows * cols * e * 4 * 2 * splits / 4e6;
       if (t < least) {
         least = t;
@@ -81,7 +85,59 @@ Tiling choose_tiling(int64_t rows, int cols, int64_t k, int experts, bool over_k
       }
     }
   }
+  *time = least;
   return best;
+}
+
+// ---- how a product is computed ------------------------------------------------------
+enum Kind { kForward, kForwardCodes, kDx, kDw };
+
+// Whether the kernel of few rows is the faster one: for up to so many rows (4096 x 7168, bf16: 1 row 15 us, 4 rows 16, 16
+// rows 22, against 18 in 64 x 128 tiles and parts of k). By experts (0: dense) their mean counts: one that has more
+// takes several passes.
+constexpr int kFewRows = 8;
+static bool few_rows(Kind kind, int64_t rows, int experts) {
+  return kind == kForward && rows <= kFewRows * (experts > 1 ? experts : 1);
+}
+
+// Rows row0 .. row0 + rows - 1 of the output, by few rows or by tiles.
+struct Part {
+  int64_t row0, rows;
+  bool few;
+  Tiling tiling;
+};
+
+// One part, or two: whole tiles and the rows that are left over, where those would take a round of tiles of their own.
+static int choose_parts(Kind kind, int64_t rows, int cols, int64_t k, int experts, int units, Part* parts) {
+  const bool over_k = kind == kDw;
+  auto one = [&](int64_t row0, int64_t n, Part* part) {
+    *part = Part{row0, n, few_rows(kind, n, experts), Tiling{0, 1}};
+    if (part->few) return 4 + (double)cols * k * 2 / 5e6;
+    double time;
+    part->tiling = choose_tiling(n, cols, k, experts ? experts : 1, over_k, units, &time);
+    return time;
+  };
+  const double whole = one(0, rows, parts);
+  const int64_t left = rows % 256, main = rows - left;
+  if (!experts && main && left && left <= 128) {
+    Part two[2];
+    if (one(0, main, two) + one(main, left, two + 1) + 3 < whole) {
+      parts[0] = two[0];
+      parts[1] = two[1];
+      return 2;
+    }
+  }
+  return 1;
+}
+
+static size_t parts_workspace(const Part* parts, int count, int cols, int experts_out) {
+  size_t most = 0;
+  for (int i = 0; i < count; ++i)
+    if (!parts[i].few && parts[i].tiling.splits > 1) {
+      const size_t need = (size_t)parts[i].tiling.splits * parts[i].rows * experts_out * cols * 4;
+      if (need > most) most = need;
+    }
+  return most;
 }
 
 // ---- the parts of k ---------------------------------------------------------------
@@ -126,14 +182,14 @@ template <class T, bool GATED, bool OVER_K> __global__ __launch_bounds__(256) vo
   }
 }
 
-int finish_splits(const Product& p, int dtype, bool gated, bool over_k, void* stream) {
+static int finish_splits(const Product& p, int dtype, bool gated, bool over_k, hipStream_t stream) {
   const int64_t rows = over_k ? p.m * p.rows.experts : p.m;
   const int64_t blocks = ceil_div64(rows * ((gated ? p.ep.inner : p.n) / 8), 256);
   if (blocks > 0x7FFFFF) return NVFP4_ERR_INVALID;
   with_type16(dtype, [&](auto type) {
     using T = decltype(type);
     const dim3 grid((unsigned)blocks);
-    hipStream_t s = (hipStream_t)stream;
+    hipStream_t s = stream;
     if (gated) parts_kernel<T, true, false><<<grid, 256, 0, s>>>(p, rows);
     else if (over_k) parts_kernel<T, false, true><<<grid, 256, 0, s>>>(p, rows);
     else parts_kernel<T, false, false><<<grid, 256, 0, s>>>(p, rows);
@@ -148,14 +204,55 @@ static bool rows_ok(int64_t rows) { return rows >= 0 && rows < ((int64_t)1 << 31
 static bool stride_ok(int64_t stride, int width) { return stride >= width && stride < kMaxStride; }
 static bool wide16(const void* p) { return aligned(p, 16); }
 
-static size_t workspace_of(const Tiling& t, int64_t rows, int64_t cols) {
-  return t.splits > 1 ? (size_t)t.splits * rows * cols * 4 : 0;
-}
-
 static int check_workspace(const void* ws, size_t have, size_t need) {
   if (!need) return NVFP4_OK;
   if (!ws || have < need) return NVFP4_ERR_WORKSPACE;
   return aligned(ws, 256) ? NVFP4_OK : NVFP4_ERR_MISALIGNED;
+}
+
+// Enqueues the parts of a checked product; `workspace` holds what parts_workspace says.
+static int run_product(Kind kind, const Product& whole, bool gated, int dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  Part parts[2];
+  const int e = whole.rows.experts, cols = whole.n;
+  const int64_t k = kind == kDw ? whole.rows.rows / e : whole.k;
+  const int count = choose_parts(kind, whole.m, cols, k, whole.rows.offsets ? e : 0, compute_units(), parts);
+  if (const int rc = check_workspace(workspace, workspace_bytes, parts_workspace(parts, count, cols, kind == kDw ? e : 1))) return rc;
+  for (int i = 0; i < count; ++i) {
+    const Part& part = parts[i];
+    Product p = whole;
+    if (count > 1) {  // dense
+      const int64_t r = part.row0;
+      p.m = part.rows;
+      auto skip = [](auto& at, int64_t bytes) {
+        if (at) at = (std::decay_t<decltype(at)>)((uintptr_t)at + bytes);
+      };
+      skip(p.a, kind == kDw ? r * 2 : r * p.lda * 2);
+      skip(p.ep.y, r * p.ep.ldy * (p.ep.y_f32 ? 4 : 2));
+      skip(p.ep.z, r * p.n * 2);
+      skip(p.ep.residual, r * p.ep.ldr * 2);
+      skip(p.ep.kept, r * p.n * 2);
+      skip(p.ep.codes, r * p.n);
+      skip(p.ep.scales, r * p.n / 32);
+      if (kind != kDw) p.rows.rows = p.rows.sources = part.rows;
+    }
+    p.partial = (float*)workspace;
+    p.partial_step = p.m * (kind == kDw ? e : 1) * cols;
+    int rc;
+    hipStream_t s = (hipStream_t)stream;
+    if (part.few) rc = run_few(p, dtype, gated, s);
+    else if (kind == kDx) rc = run_dx(p, part.tiling, dtype, s);
+    else if (kind == kDw) rc = run_dw(p, part.tiling, dtype, s);
+    else rc = run_forward(p, part.tiling, dtype, gated, s);
+    if (!rc && !part.few && part.tiling.splits > 1) rc = finish_splits(p, dtype, gated, kind == kDw, s);
+    if (rc) return rc;
+  }
+  return NVFP4_OK;
+}
+
+static size_t product_workspace(Kind kind, int64_t rows, int cols, int64_t k, int experts) {
+  Part parts[2];
+  const int count = choose_parts(kind, rows, cols, k, experts, compute_units(), parts);
+  return parts_workspace(parts, count, cols, kind == kDw && experts ? experts : 1);
 }
 
 }  // namespace ffn
@@ -168,13 +265,18 @@ int nvfp4_ffn_last_hip_error(void) { return t_last_hip_error; }
 
 size_t nvfp4_ffn_product_workspace_bytes(int64_t rows, int n, int k, int experts) {
   if (rows < 1 || !rows_ok(rows) || !side_ok(n) || !side_ok(k) || experts > NVFP4_MOE_MAX_EXPERTS) return 0;
-  return workspace_of(choose_tiling(rows, n, k, experts < 1 ? 1 : experts, false, compute_units()), rows, n);
+  const int e = experts < 1 ? 0 : experts;
+  size_t most = 0;
+  for (const Kind kind : {kForward, kForwardCodes, kDx}) {
+    const size_t need = product_workspace(kind, rows, n, k, e);
+    if (need > most) most = need;
+  }
+  return most;
 }
 
 size_t nvfp4_ffn_dw_workspace_bytes(int64_t rows, int n, int k, int experts) {
   if (rows < 1 || !rows_ok(rows) || !side_ok(n) || !side_ok(k) || experts > NVFP4_MOE_MAX_EXPERTS) return 0;
-  const int e = experts < 1 ? 1 : experts;
-  return workspace_of(choose_tiling(n, k, rows / e, e, true, compute_units()), (int64_t)e * n, k);
+  return product_workspace(kDw, n, k, experts < 1 ? rows : rows / experts, experts < 1 ? 0 : experts);
 }
 
 int nvfp4_ffn_linear(const void* x, int64_t x_stride, const void* w, const void* bias, int bias_f32, int act,
@@ -189,15 +291,11 @@ int nvfp4_ffn_linear(const void* x, int64_t x_stride, const void* w, const void*
   if (!wide16(x) || !wide16(w) || !wide16(y) || !wide16(bias) || !wide16(z) || !wide16(residual) || x_stride % 8 ||
       (residual && residual_stride % 8))
     return NVFP4_ERR_MISALIGNED;
-  const Tiling t = choose_tiling(rows, n, k, p.rows.experts, false, compute_units());
-  if (const int rc = check_workspace(workspace, workspace_bytes, workspace_of(t, rows, n))) return rc;
   p.a = x; p.b = w; p.lda = x_stride; p.ldb = k; p.m = rows; p.n = n; p.k = k; p.b_step = (int64_t)n * k;
   p.rows.clear = clear != 0;
-  p.partial = (float*)workspace; p.partial_step = rows * n;
   p.ep.y = y; p.ep.ldy = n; p.ep.bias = bias; p.ep.bias_f32 = bias_f32; p.ep.act = act;
   p.ep.residual = residual; p.ep.ldr = residual_stride; p.ep.z = z;
-  const int rc = run_forward(p, t, dtype, false, (hipStream_t)stream);
-  return rc || t.splits == 1 ? rc : finish_splits(p, dtype, false, false, stream);
+  return run_product(kForward, p, false, dtype, workspace, workspace_bytes, stream);
 }
 
 int nvfp4_ffn_gated(const void* x, int64_t x_stride, const void* w, int act, void* h, void* kept, void* codes,
@@ -212,15 +310,11 @@ int nvfp4_ffn_gated(const void* x, int64_t x_stride, const void* w, int act, voi
   if (!x || !w || !h || !stride_ok(x_stride, k) || (int64_t)2 * inner * k * 2 > kMaxBytes) return NVFP4_ERR_INVALID;
   if (plan && p.rows.sources * x_stride * 2 > kMaxBytes) return NVFP4_ERR_INVALID;
   if (!wide16(x) || !wide16(w) || !wide16(h) || !wide16(kept) || !aligned(codes, 8) || x_stride % 8) return NVFP4_ERR_MISALIGNED;
-  const Tiling t = choose_tiling(rows, 2 * inner, k, p.rows.experts, false, compute_units());
-  if (const int rc = check_workspace(workspace, workspace_bytes, workspace_of(t, rows, 2 * inner))) return rc;
   p.a = x; p.b = w; p.lda = x_stride; p.ldb = k; p.m = rows; p.n = 2 * inner; p.k = k; p.b_step = (int64_t)2 * inner * k;
   p.rows.clear = clear != 0;
-  p.partial = (float*)workspace; p.partial_step = rows * 2 * inner;
   p.ep.y = h; p.ep.ldy = inner; p.ep.act = act; p.ep.inner = inner; p.ep.kept = kept;
   p.ep.codes = (uint8_t*)codes; p.ep.scales = (uint8_t*)scales;
-  const int rc = run_forward(p, t, dtype, true, (hipStream_t)stream);
-  return rc || t.splits == 1 ? rc : finish_splits(p, dtype, true, false, stream);
+  return run_product(codes ? kForwardCodes : kForward, p, true, dtype, workspace, workspace_bytes, stream);
 }
 
 int nvfp4_ffn_linear_dx(const void* dz, int64_t dz_stride, const void* w, void* dx, int dtype, int64_t rows, int n, int k,
@@ -231,15 +325,11 @@ int nvfp4_ffn_linear_dx(const void* dz, int64_t dz_stride, const void* w, void* 
   if (rows == 0) return NVFP4_OK;
   if (!dz || !w || !dx || !stride_ok(dz_stride, n) || (int64_t)n * k * 2 > kMaxBytes) return NVFP4_ERR_INVALID;
   if (!wide16(dz) || !wide16(w) || !wide16(dx) || dz_stride % 8) return NVFP4_ERR_MISALIGNED;
-  const Tiling t = choose_tiling(rows, k, n, p.rows.experts, false, compute_units());
-  if (const int rc = check_workspace(workspace, workspace_bytes, workspace_of(t, rows, k))) return rc;
   // the reduction is over n, the output's columns are k
   p.a = dz; p.b = w; p.lda = dz_stride; p.ldb = k; p.m = rows; p.n = k; p.k = n; p.b_step = (int64_t)n * k;
   p.rows.clear = clear != 0;
-  p.partial = (float*)workspace; p.partial_step = rows * k;
   p.ep.y = dx; p.ep.ldy = k;
-  const int rc = run_dx(p, t, dtype, (hipStream_t)stream);
-  return rc || t.splits == 1 ? rc : finish_splits(p, dtype, false, false, stream);
+  return run_product(kDx, p, false, dtype, workspace, workspace_bytes, stream);
 }
 
 int nvfp4_ffn_linear_dw(const void* dz, int64_t dz_stride, const void* x, int64_t x_stride, void* dw, int dw_f32, int dtype,
@@ -251,15 +341,9 @@ int nvfp4_ffn_linear_dw(const void* dz, int64_t dz_stride, const void* x, int64_
   if ((rows && (!dz || !x)) || (rows && (!stride_ok(dz_stride, n) || !stride_ok(x_stride, k))) || (int64_t)n * k * 2 > kMaxBytes)
     return NVFP4_ERR_INVALID;
   if (!wide16(dz) || !wide16(x) || !wide16(dw) || (rows && (dz_stride % 8 || x_stride % 8))) return NVFP4_ERR_MISALIGNED;
-  Tiling t{0, 1};
-  if (rows) t = choose_tiling(n, k, rows / p.rows.experts, p.rows.experts, true, compute_units());
-  const int64_t out_rows = (int64_t)p.rows.experts * n;
-  if (const int rc = check_workspace(workspace, workspace_bytes, workspace_of(t, out_rows, k))) return rc;
   p.a = dz; p.b = x; p.lda = dz_stride; p.ldb = x_stride; p.m = n; p.n = k; p.k = 0;
-  p.partial = (float*)workspace; p.partial_step = out_rows * k;
   p.ep.y = dw; p.ep.ldy = k; p.ep.y_f32 = dw_f32;
-  const int rc = run_dw(p, t, dtype, (hipStream_t)stream);
-  return rc || t.splits == 1 ? rc : finish_splits(p, dtype, false, true, stream);
+  return run_product(kDw, p, false, dtype, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"
