@@ -122,7 +122,7 @@ int nvfp4_ffn_linear(const void* x, int64_t x_stride, const void* w, const void*
 
 /*
  * nvfp4_ffn_gated - g = x Wg^T, u = x Wu^T, h = act(g) * u; act not NVFP4_FFN_NONE.
- *   x         device [rows][k]; with a plan [tokens][k], rows = tokens * topk, each row its token's
+ *   x         device [rows][k]; with a plan [tokens][k] below 2^31 bytes, rows = tokens * topk, each row its token's
  *   w         device [2 * inner][k], Wg's rows first; with a plan [experts][2 * inner][k]
  *   h         device [rows][inner]
  *   kept      device [rows][2 * inner] of dtype: g, then u, rounded; or NULL
@@ -137,6 +137,18 @@ int nvfp4_ffn_gated(const void* x, int64_t x_stride, const void* w, int act, voi
 /* Bytes of workspace of a product [rows][k] x [n][k] (also of nvfp4_ffn_linear_dx with n and k in turn: [rows][n] x
  * [k][n]); experts 0: dense, else the plan's. */
 size_t nvfp4_ffn_product_workspace_bytes(int64_t rows, int n, int k, int experts);
+
+/*
+ * nvfp4_ffn_product_parts - how a product is computed: the number of its launches over rows (1 or 2; 0 for arguments
+ * that are none), and for each four values in `parts` (host, int32 [8]): its rows, the tile's rows and columns
+ * (0, 0: the kernel of few rows), the parts of k. Those are the choice for a device of the current one's compute units.
+ *   kind   NVFP4_FFN_FORWARD, _FORWARD_CODES (gated with codes), _DX or _DW; rows, n, k, experts as for the call
+ */
+#define NVFP4_FFN_FORWARD 0
+#define NVFP4_FFN_FORWARD_CODES 1
+#define NVFP4_FFN_DX 2
+#define NVFP4_FFN_DW 3
+int nvfp4_ffn_product_parts(int kind, int64_t rows, int n, int k, int experts, int32_t* parts);
 
 /*
  * nvfp4_ffn_linear_dz - dz = dy act'(z), rounded to dtype, and dbias = sum over an expert's

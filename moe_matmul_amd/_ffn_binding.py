@@ -16,6 +16,7 @@ from ._binding import NVFP4_ERR_HIP, NVFP4_OK, Nvfp4Error, nvfp4_error_string
 FFN_LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnvfp4_ffn.so")
 
 NVFP4_FFN_NONE, NVFP4_FFN_RELU, NVFP4_FFN_SILU, NVFP4_FFN_GELU = 0, 1, 2, 3
+NVFP4_FFN_FORWARD, NVFP4_FFN_FORWARD_CODES, NVFP4_FFN_DX, NVFP4_FFN_DW = 0, 1, 2, 3
 
 
 class Nvfp4FfnError(Nvfp4Error):
@@ -46,6 +47,7 @@ _SIGNATURES = {
     "nvfp4_ffn_gated": (_int, [_ptr, _i64, _ptr, _int, _ptr, _ptr, _ptr, _ptr, _int, _i64, _int, _int, _plan, _int, _ptr,
                                _size, _ptr]),
     "nvfp4_ffn_product_workspace_bytes": (_size, [_i64, _int, _int, _int]),
+    "nvfp4_ffn_product_parts": (_int, [_int, _i64, _int, _int, _int, ctypes.POINTER(ctypes.c_int32)]),
     "nvfp4_ffn_linear_dz": (_int, [_ptr, _i64, _ptr, _int, _ptr, _ptr, _int, _int, _i64, _int, _plan, _ptr, _size, _ptr]),
     "nvfp4_ffn_dz_workspace_bytes": (_size, [_i64, _int, _int]),
     "nvfp4_ffn_gated_dz": (_int, [_ptr, _i64, _ptr, _ptr, _ptr, _int, _ptr, _int, _i64, _int, _plan, _ptr]),
@@ -96,7 +98,7 @@ nvfp4_ffn_linear_dx = _checked("nvfp4_ffn_linear_dx")
 nvfp4_ffn_linear_dw = _checked("nvfp4_ffn_linear_dw")
 
 
-# the device's compute units go into these: kept by device
+# Buffer sizes, kept by the index of the device whose compute units go into them: it has to be the current one.
 @functools.lru_cache(maxsize=4096)
 def nvfp4_ffn_rmsnorm_workspace_bytes(rows: int, n: int, device: int = 0) -> int:
     return load_ffn_library().nvfp4_ffn_rmsnorm_workspace_bytes(rows, n)
@@ -108,13 +110,20 @@ def nvfp4_ffn_product_workspace_bytes(rows: int, n: int, k: int, experts: int, d
 
 
 @functools.lru_cache(maxsize=4096)
-def nvfp4_ffn_dz_workspace_bytes(rows: int, n: int, experts: int) -> int:
+def nvfp4_ffn_dz_workspace_bytes(rows: int, n: int, experts: int, device: int = 0) -> int:
     return load_ffn_library().nvfp4_ffn_dz_workspace_bytes(rows, n, experts)
 
 
 @functools.lru_cache(maxsize=4096)
 def nvfp4_ffn_dw_workspace_bytes(rows: int, n: int, k: int, experts: int, device: int = 0) -> int:
     return load_ffn_library().nvfp4_ffn_dw_workspace_bytes(rows, n, k, experts)
+
+
+def nvfp4_ffn_product_parts(kind: int, rows: int, n: int, k: int, experts: int) -> list:
+    """[(rows, tile rows, tile columns, parts of k)] of a product's launches; a tile of (0, 0): the kernel of few rows."""
+    out = (ctypes.c_int32 * 8)()
+    count = load_ffn_library().nvfp4_ffn_product_parts(kind, rows, n, k, experts, out)
+    return [tuple(out[4 * i:4 * i + 4]) for i in range(count)]
 
 
 def nvfp4_ffn_last_hip_error() -> int:

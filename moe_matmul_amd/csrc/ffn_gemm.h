@@ -596,9 +596,12 @@ struct Tiling {
   int shape;   // 0: 128 x 128, 1: 256 x 128, 2: 256 x 256, 3: 64 x 128 (rows with k inside)
   int splits;
 };
+inline int tile_rows(int shape) { return shape == 3 ? 64 : shape ? 256 : 128; }
+inline int tile_cols(int shape) { return shape == 2 ? 256 : 128; }
+
 template <class T, int AL, int BL, bool GATED> inline int launch_product(Product& p, const Tiling& t, hipStream_t stream) {
   constexpr bool OVER_K = AL == kOutsideK;
-  const int bm = t.shape == 3 ? 64 : t.shape ? 256 : 128, cols = (t.shape == 2 ? 256 : 128) / (GATED ? 2 : 1);
+  const int bm = tile_rows(t.shape), cols = tile_cols(t.shape) / (GATED ? 2 : 1);
   p.splits = t.splits;
   p.tiles_m = (int)ceil_div64(p.m, bm);
   p.tiles_n = ceil_div(GATED ? p.ep.inner : p.n, cols);

@@ -258,10 +258,10 @@ int nvfp4_ffn_rmsnorm(const void* x, int dtype, int64_t rows, int n, int64_t x_s
                       int64_t residual_stride, const void* weight, int weight_f32, float eps, void* sum, void* y,
                       void* codes, void* scales, float* rstd, void* stream) {
   if (!known_type(dtype) || rows < 0 || rows >= (int64_t)1 << 31 || n < 1 || n > kMaxNorm || !(eps >= 0.f) ||
-      !codes != !scales || (codes && n % kBlock8) || (!y && !codes && !rstd))
+      !codes != !scales || (codes && n % kBlock8))
     return NVFP4_ERR_INVALID;
   if (rows == 0) return NVFP4_OK;
-  if (!x || x_stride < n || (residual && (residual_stride < n || !sum))) return NVFP4_ERR_INVALID;
+  if (!x || (!y && !codes && !rstd) || x_stride < n || (residual && (residual_stride < n || !sum))) return NVFP4_ERR_INVALID;
   const size_t element = element_bytes(dtype);
   if (!aligned(x, element) || !aligned(residual, element) || !aligned(sum, element) || !aligned(y, element) ||
       !aligned(weight, weight_f32 ? 4 : element) || !aligned(codes, 8) || !aligned(rstd, 4))

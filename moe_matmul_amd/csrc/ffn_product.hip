@@ -60,7 +60,7 @@ static Tiling choose_tiling(int64_t rows, int cols, int64_t k, int experts, bool
   // the weights' (or rows') own bytes
   const double streamed = 5 + (double)cols * k * 2 * (over_k ? e : experts < rows ? experts : rows) / 5e6;
   for (int shape = 0; shape < (over_k ? 3 : 4); ++shape) {
-    const int bm = shape == 3 ? 64 : shape ? 256 : 128, bn = shape == 2 ? 256 : 128;
+    const int bm = tile_rows(shape), bn = tile_cols(shape);
     const double tail = (double)(rows % bm) / bm;
     double high = rows / bm + (tail > 0 ? (tail > 0.4 ? tail : 0.4) : 0);
     if (!over_k && experts > 1) {
@@ -76,7 +76,9 @@ static Tiling choose_tiling(int64_t rows, int cols, int64_t k, int experts, bool
       const double whole = floor(all / room), rest = all - whole * room;
       const double part = stages / splits;
       double t = whole * (kFixed[shape] + part * kStage[shape]);
-      if (rest > 0.01) t += kFixed[shape] + part * (rest <= units ? kAlone[shape] : kStage[shape]);
+      // (units that are alone on the memory and the power are faster: 136 tiles of 256 x 256 1.3 a stage)
+      if (rest > 0.01)
+        t += kFixed[shape] + part * (rest > units ? kStage[shape] : kAlone[shape] * (room > units ? 1 : 0.66 + 0.34 * rest / units));
       if (t < streamed) t = streamed;
       if (splits > 1) t += 4 + (double)rows * cols * e * 4 * 2 * splits / 4e6;
       if (t < least) {
@@ -90,7 +92,7 @@ static Tiling choose_tiling(int64_t rows, int cols, int64_t k, int experts, bool
 }
 
 // ---- how a product is computed ------------------------------------------------------
-enum Kind { kForward, kForwardCodes, kDx, kDw };
+enum Kind { kForward = NVFP4_FFN_FORWARD, kForwardCodes = NVFP4_FFN_FORWARD_CODES, kDx = NVFP4_FFN_DX, kDw = NVFP4_FFN_DW };
 
 // Whether the kernel of few rows is the faster one: for up to so many rows (4096 x 7168, bf16: 1 row 15 us, 4 rows 16, 16
 // rows 22, against 18 in 64 x 128 tiles and parts of k). By experts (0: dense) their mean counts: one that has more
@@ -121,7 +123,7 @@ static int choose_parts(Kind kind, int64_t rows, int cols, int64_t k, int expert
   const int64_t left = rows % 256, main = rows - left;
   if (!experts && main && left && left <= 128) {
     Part two[2];
-    if (one(0, main, two) + one(main, left, two + 1) + 3 < whole) {
+    if (one(0, main, two) + one(main, left, two + 1) + 6 < whole) {
       parts[0] = two[0];
       parts[1] = two[1];
       return 2;
@@ -277,6 +279,25 @@ size_t nvfp4_ffn_product_workspace_bytes(int64_t rows, int n, int k, int experts
 size_t nvfp4_ffn_dw_workspace_bytes(int64_t rows, int n, int k, int experts) {
   if (rows < 1 || !rows_ok(rows) || !side_ok(n) || !side_ok(k) || experts > NVFP4_MOE_MAX_EXPERTS) return 0;
   return product_workspace(kDw, n, k, experts < 1 ? rows : rows / experts, experts < 1 ? 0 : experts);
+}
+
+int nvfp4_ffn_product_parts(int kind, int64_t rows, int n, int k, int experts, int32_t* out) {
+  if (kind < kForward || kind > kDw || rows < 1 || !rows_ok(rows) || !side_ok(n) || !side_ok(k) || experts < 0 ||
+      experts > NVFP4_MOE_MAX_EXPERTS || !out)
+    return 0;
+  Part parts[2];
+  const int units = compute_units();
+  const int count = kind == kDw   ? choose_parts(kDw, n, k, experts ? rows / experts : rows, experts, units, parts)
+                    : kind == kDx ? choose_parts(kDx, rows, k, n, experts, units, parts)
+                                  : choose_parts((Kind)kind, rows, n, k, experts, units, parts);
+  for (int i = 0; i < count; ++i) {
+    const int shape = parts[i].tiling.shape;
+    out[4 * i] = (int32_t)parts[i].rows;
+    out[4 * i + 1] = parts[i].few ? 0 : tile_rows(shape);
+    out[4 * i + 2] = parts[i].few ? 0 : tile_cols(shape);
+    out[4 * i + 3] = parts[i].few ? 1 : parts[i].tiling.splits;
+  }
+  return count;
 }
 
 int nvfp4_ffn_linear(const void* x, int64_t x_stride, const void* w, const void* bias, int bias_f32, int act,

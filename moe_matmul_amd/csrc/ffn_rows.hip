@@ -222,7 +222,10 @@ static unsigned blocks_for(int64_t items) {
 }
 static bool rows_ok(int64_t rows) { return rows >= 0 && rows < (int64_t)1 << 31; }
 static bool width_ok(int n, int step) { return n >= step && n <= 1 << 20 && n % step == 0; }
-static int64_t chunks_of(int64_t rows, int experts) { return rows / kChunkRows + (experts < rows ? experts : rows); }
+// Chunks of so many rows, with a plan (experts, else 0) the most there can be.
+static int64_t chunks_of(int64_t rows, int experts) {
+  return experts ? rows / kChunkRows + (experts < rows ? experts : rows) : ceil_div64(rows, kChunkRows);
+}
 
 }  // namespace ffn
 
@@ -285,7 +288,7 @@ int nvfp4_ffn_gather(const void* x, int64_t x_stride, const void* codes, const v
 
 size_t nvfp4_ffn_dz_workspace_bytes(int64_t rows, int n, int experts) {
   if (rows < 1 || !rows_ok(rows) || !width_ok(n, 8) || experts > NVFP4_MOE_MAX_EXPERTS) return 0;
-  return (size_t)chunks_of(rows, experts < 1 ? 1 : experts) * n * 4;
+  return (size_t)chunks_of(rows, experts < 1 ? 0 : experts) * n * 4;
 }
 
 int nvfp4_ffn_linear_dz(const void* dy, int64_t dy_stride, const void* z, int act, void* dz, void* dbias, int bias_f32,
@@ -304,7 +307,7 @@ int nvfp4_ffn_linear_dz(const void* dy, int64_t dy_stride, const void* z, int ac
   }
   if (!dy || dy_stride < n || (act != NVFP4_FFN_NONE && (!z || !dz))) return NVFP4_ERR_INVALID;
   if (!aligned(dy, 16) || dy_stride % 8 || !aligned(z, 16) || !aligned(dz, 16)) return NVFP4_ERR_MISALIGNED;
-  const int64_t chunks = chunks_of(rows, p.experts);
+  const int64_t chunks = chunks_of(rows, p.offsets ? p.experts : 0);
   if (dbias) {
     if (!workspace || workspace_bytes < (size_t)chunks * n * 4) return NVFP4_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return NVFP4_ERR_MISALIGNED;

@@ -28,7 +28,7 @@ import torch
 
 from . import _ffn_binding as c
 from . import moe
-from .moe import _at, _enqueue, _gpu, _like, _on_stream, _out, _rows, _type
+from .moe import _at, _current_device, _enqueue, _gpu, _like, _on_stream, _out, _rows, _type
 
 _ACTIVATIONS = {None: c.NVFP4_FFN_NONE, "relu": c.NVFP4_FFN_RELU, "silu": c.NVFP4_FFN_SILU, "gelu": c.NVFP4_FFN_GELU}
 _16 = (torch.float16, torch.bfloat16)
@@ -80,6 +80,14 @@ def _plan(plan):
     if entry is None:
         entry = plan._ffn_entry = c.nvfp4_ffn_plan(plan.experts, plan.topk, plan.addresses[0], plan.addresses[3])
     return ctypes.byref(entry)
+
+
+def _need(size, device, *args) -> int:
+    """Bytes of a workspace on that device."""
+    if device.index == _current_device():
+        return size(*args, device.index)
+    with torch.cuda.device(device):
+        return size(*args, device.index)
 
 
 def _room(need, device):
@@ -193,7 +201,7 @@ def rmsnorm_backward(dy, sum, weight, rstd, *, dsum=None, stream=None):
     dweight, need = None, 0
     if weight is not None:
         dweight = torch.empty(n, dtype=weight.dtype, device=device)
-        need = c.nvfp4_ffn_rmsnorm_workspace_bytes(rows, n, device.index)
+        need = _need(c.nvfp4_ffn_rmsnorm_workspace_bytes, device, rows, n)
     room = _room(need, device)
     _enqueue(c.nvfp4_ffn_rmsnorm_backward, device, dy.data_ptr(), dy_stride, sum.data_ptr(), stride, kind, rows, n,
              _at(weight), f32, rstd.data_ptr(), _at(dsum), dsum_stride, dx.data_ptr(), _at(dweight), _at(room), need)
@@ -222,7 +230,7 @@ def linear(x, w, *, bias=None, activation=None, residual=None, plan=None, save=F
     clear = out is None
     out = _out(out, "out", (rows, n), x.dtype, device)
     z = _out(None, "z", (rows, n), x.dtype, device) if save else None
-    need = c.nvfp4_ffn_product_workspace_bytes(rows, n, k, experts, device.index)
+    need = _need(c.nvfp4_ffn_product_workspace_bytes, device, rows, n, k, experts)
     room = _room(need, device)
     _enqueue(c.nvfp4_ffn_linear, device, x.data_ptr(), stride, w.data_ptr(), _at(bias), f32, act, _at(residual),
              residual_stride, _at(z), out.data_ptr(), kind, rows, n, k, _plan(plan), clear, _at(room), need)
@@ -241,8 +249,8 @@ def _products_back(dz, dz_stride, x, x_stride, w, plan, kind, experts, dw):
     device, (rows, n), k = dz.device, dz.shape, w.shape[-1]
     dw, f32 = _dw(dw, w, dz.dtype)
     dx = _out(None, "dx", (rows, k), dz.dtype, device)
-    need = c.nvfp4_ffn_product_workspace_bytes(rows, k, n, experts, device.index)
-    need_dw = c.nvfp4_ffn_dw_workspace_bytes(rows, n, k, experts, device.index)
+    need = _need(c.nvfp4_ffn_product_workspace_bytes, device, rows, k, n, experts)
+    need_dw = _need(c.nvfp4_ffn_dw_workspace_bytes, device, rows, n, k, experts)
     room = _room(max(need, need_dw), device)
     _enqueue(c.nvfp4_ffn_linear_dx, device, dz.data_ptr(), dz_stride, w.data_ptr(), dx.data_ptr(), kind, rows, n, k,
              _plan(plan), 1, _at(room), need)
@@ -280,7 +288,7 @@ def linear_backward(dy, x, w, *, bias=None, z=None, activation=None, plan=None, 
     if bias is not None:
         f32 = _param(bias, "bias", w.shape[:-1], dy)
         dbias = torch.empty(w.shape[:-1], dtype=bias.dtype, device=device)
-        need = c.nvfp4_ffn_dz_workspace_bytes(rows, n, experts)
+        need = _need(c.nvfp4_ffn_dz_workspace_bytes, device, rows, n, experts)
     if dz is not dy or dbias is not None:
         room = _room(need, device)
         _enqueue(c.nvfp4_ffn_linear_dz, device, dy.data_ptr(), stride, _at(z) if act else 0, act,
@@ -293,7 +301,7 @@ def linear_backward(dy, x, w, *, bias=None, z=None, activation=None, plan=None, 
 
 def _gated(x, stride, w, act, kind, rows, inner, k, plan, experts, h, kept, kept8, clear):
     device = w.device
-    need = c.nvfp4_ffn_product_workspace_bytes(rows, 2 * inner, k, experts, device.index)
+    need = _need(c.nvfp4_ffn_product_workspace_bytes, device, rows, 2 * inner, k, experts)
     room = _room(need, device)
     _enqueue(c.nvfp4_ffn_gated, device, x.data_ptr(), stride, w.data_ptr(), act, h.data_ptr(), _at(kept),
              _at(kept8 and kept8.codes), _at(kept8 and kept8.scales), kind, rows, inner, k, _plan(plan), clear, _at(room), need)
