@@ -92,10 +92,7 @@ __device__ __forceinline__ void finish_linear(const Epilogue& p, int n, int64_t 
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] += b[j];
   if (p.z) *(u32x4*)((uint16_t*)p.z + row * n + col) = pack16x8<T>(v);
-  if (p.act != NVFP4_FFN_NONE) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = activation(v[j], p.act);
-  }
+  activation8(v, p.act);
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] += r[j];
   if (p.y_f32) store8<F32>(p.y, row * p.ldy + col, true, v);
@@ -111,7 +108,10 @@ __device__ __forceinline__ void finish_gated(const Epilogue& p, int64_t row, int
   }
   float h[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) h[j] = activation(g[j], p.act) * u[j];
+  for (int j = 0; j < 8; ++j) h[j] = g[j];
+  activation8(h, p.act);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) h[j] *= u[j];
   *(u32x4*)((uint16_t*)p.y + row * p.ldy + col) = pack16x8<T>(h);
 }
 __device__ __forceinline__ uint32_t top8(const float* v) {
