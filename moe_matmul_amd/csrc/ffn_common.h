@@ -114,7 +114,6 @@ template <bool SLOPE> __device__ __forceinline__ void activate(float z, int kind
       return;
   }
 }
-__device__ __forceinline__ void activation_slope(float z, int kind, float& a, float& s) { activate<true>(z, kind, a, s); }
 __device__ __forceinline__ float activation(float z, int kind) {
   float a, s;
   activate<false>(z, kind, a, s);
@@ -137,6 +136,28 @@ __device__ __forceinline__ void activation8(float* v, int kind) {
       return;
     default: return;
   }
+}
+
+// Of eight z their slopes, in place, and their activations (a).
+template <int KIND> __device__ __forceinline__ void values_slopes(float* z, float* a) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    float v, s;
+    activate<true>(z[j], KIND, v, s);
+    z[j] = s;
+    a[j] = v;
+  }
+}
+__device__ __forceinline__ void values_slopes8(float* z, float* a, int kind) {
+  switch (kind) {
+    case NVFP4_FFN_RELU: values_slopes<NVFP4_FFN_RELU>(z, a); return;
+    case NVFP4_FFN_SILU: values_slopes<NVFP4_FFN_SILU>(z, a); return;
+    default: values_slopes<NVFP4_FFN_GELU>(z, a); return;
+  }
+}
+__device__ __forceinline__ void slopes8(float* z, int kind) {
+  float a[8];
+  values_slopes8(z, a, kind);
 }
 
 // ---- rows in 8 bits -----------------------------------------------------------

@@ -109,22 +109,33 @@ template <class T> __global__ __launch_bounds__(256) void linear_dz_kernel(const
   const int col = blockIdx.x * kChunkCols + threadIdx.x % 32 * 8, first = threadIdx.x / 32;
   float sum[8] = {};
   if (col < n) {
-    for (int64_t r = row + first; r < end; r += 8) {
-      float d[8];
-      load8<T>(dy, r * dy_stride + col, true, d);
-      if (act != NVFP4_FFN_NONE) {
-        float v[8];
-        load8<T>(z, r * n + col, true, v);
+    // the loads of four rows are under way together
+    for (int64_t r0 = row + first; r0 < end; r0 += 32) {
+      u32x4 d4[4], z4[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          float a, s;
-          activation_slope(v[j], act, a, s);
-          d[j] *= s;
-        }
+      for (int u = 0; u < 4; ++u) {
+        const int64_t r = r0 + 8 * u;
+        if (r >= end) continue;
+        d4[u] = *(const u32x4*)((const uint16_t*)dy + r * dy_stride + col);
+        if (act != NVFP4_FFN_NONE) z4[u] = *(const u32x4*)((const uint16_t*)z + r * n + col);
       }
-      if (dz) store8<T>(dz, r * n + col, true, d);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum[j] += d[j];
+      for (int u = 0; u < 4; ++u) {
+        const int64_t r = r0 + 8 * u;
+        if (r >= end) continue;
+        float d[8];
+        unpack16x8<T>(d4[u], d);
+        if (act != NVFP4_FFN_NONE) {
+          float v[8];
+          unpack16x8<T>(z4[u], v);
+          slopes8(v, act);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) d[j] *= v[j];
+        }
+        if (dz) *(u32x4*)((uint16_t*)dz + r * n + col) = pack16x8<T>(d);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[j] += d[j];
+      }
     }
   }
   if (!partial) return;
@@ -158,23 +169,25 @@ __global__ __launch_bounds__(256) void gated_dz_kernel(const void* dh, int64_t d
       load8<T>(kept, (row * 2 * wide + c) * 8, true, g);
       load8<T>(kept, (row * 2 * wide + wide + c) * 8, true, u);
     }
+    float a[8];
+    values_slopes8(g, a, act);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      float a, s;
-      activation_slope(g[j], act, a, s);
-      g[j] = d[j] * u[j] * s;
-      u[j] = d[j] * a;
+      g[j] *= d[j] * u[j];
+      u[j] = d[j] * a[j];
     }
-    store8<T>(dz, (row * 2 * wide + c) * 8, true, g);
-    store8<T>(dz, (row * 2 * wide + wide + c) * 8, true, u);
+    ((u32x4*)dz)[row * 2 * wide + c] = pack16x8<T>(g);
+    ((u32x4*)dz)[row * 2 * wide + wide + c] = pack16x8<T>(u);
   }
 }
 
 // ---- sums of parts ------------------------------------------------------------------------
-// out[e][col] = the sum of the parts of expert e in their order, in four interleaved chains of eight threads each: 32
-// columns a workgroup. Without a plan one expert has all `parts`.
-__global__ __launch_bounds__(256) void add_columns_kernel(const float* partial, int64_t parts, int n, Rows p, void* out, int type) {
-  __shared__ float room[8][32];
+// out[e][col] = the sum of the parts of expert e, 32 columns a workgroup: 32 threads for each column, four interleaved
+// chains each, so that few loads wait for one another (1024 parts of 4096: 8 threads took 11 us). Without a plan one
+// expert has all `parts`.
+constexpr int kAddThreads = 1024, kAddRows = kAddThreads / 32;
+__global__ __launch_bounds__(kAddThreads) void add_columns_kernel(const float* partial, int64_t parts, int n, Rows p, void* out, int type) {
+  __shared__ float room[kAddRows][33];
   const int col = blockIdx.x * 32 + threadIdx.x % 32, first = threadIdx.x / 32, e = blockIdx.y;
   int64_t begin = 0, end = parts;
   if (p.offsets) {
@@ -193,18 +206,18 @@ __global__ __launch_bounds__(256) void add_columns_kernel(const float* partial, 
   float v[4] = {};
   if (col < n) {
     int64_t i = begin + first;
-    for (; i + 24 < end; i += 32) {
+    for (; i + 3 * kAddRows < end; i += 4 * kAddRows) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] += partial[(i + 8 * j) * n + col];
+      for (int j = 0; j < 4; ++j) v[j] += partial[(i + kAddRows * j) * n + col];
     }
-    for (; i < end; i += 8) v[0] += partial[i * n + col];
+    for (; i < end; i += kAddRows) v[0] += partial[i * n + col];
   }
   room[first][threadIdx.x % 32] = (v[0] + v[1]) + (v[2] + v[3]);
   __syncthreads();
   if (threadIdx.x >= 32 || col >= n) return;
   float sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) sum += room[i][threadIdx.x];
+  for (int i = 0; i < kAddRows; ++i) sum += room[i][threadIdx.x];
   const int64_t at = (int64_t)e * n + col;
   if (type == NVFP4_MOE_F32) store1<F32>(out, at, sum);
   else if (type == NVFP4_MOE_F16) store1<F16>(out, at, sum);
@@ -212,7 +225,7 @@ __global__ __launch_bounds__(256) void add_columns_kernel(const float* partial, 
 }
 
 void add_columns(const float* partial, int64_t parts, int n, void* out, int out_type, hipStream_t stream) {
-  add_columns_kernel<<<dim3(ceil_div(n, 32), 1), 256, 0, stream>>>(partial, parts, n, Rows{nullptr, nullptr, 1, 1, 0, 0, 0}, out, out_type);
+  add_columns_kernel<<<dim3(ceil_div(n, 32), 1), kAddThreads, 0, stream>>>(partial, parts, n, Rows{nullptr, nullptr, 1, 1, 0, 0, 0}, out, out_type);
 }
 
 // Workgroups of 256 threads for `items` threads' work, as many as keep the card full.
@@ -302,7 +315,7 @@ int nvfp4_ffn_linear_dz(const void* dy, int64_t dy_stride, const void* z, int ac
   if (rows == 0) {
     if (!dbias) return NVFP4_OK;
     p.offsets = nullptr;  // an empty sum for every expert
-    add_columns_kernel<<<dim3(ceil_div(n, 32), p.experts), 256, 0, (hipStream_t)stream>>>(nullptr, 0, n, p, dbias, bias_type);
+    add_columns_kernel<<<dim3(ceil_div(n, 32), p.experts), kAddThreads, 0, (hipStream_t)stream>>>(nullptr, 0, n, p, dbias, bias_type);
     return launched();
   }
   if (!dy || dy_stride < n || (act != NVFP4_FFN_NONE && (!z || !dz))) return NVFP4_ERR_INVALID;
@@ -323,7 +336,7 @@ int nvfp4_ffn_linear_dz(const void* dy, int64_t dy_stride, const void* z, int ac
   });
   if (const int rc = launched()) return rc;
   if (!dbias) return NVFP4_OK;
-  add_columns_kernel<<<dim3(ceil_div(n, 32), p.experts), 256, 0, (hipStream_t)stream>>>((const float*)workspace, chunks, n, p, dbias, bias_type);
+  add_columns_kernel<<<dim3(ceil_div(n, 32), p.experts), kAddThreads, 0, (hipStream_t)stream>>>((const float*)workspace, chunks, n, p, dbias, bias_type);
   return launched();
 }
 
