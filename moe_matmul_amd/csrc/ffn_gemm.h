@@ -301,16 +301,16 @@ template <int BM> __device__ __forceinline__ bool find_rows(const Rows& p, int64
   return false;
 }
 
-template <class T, int AL, int BL, bool GATED, int BM, int BN, int WM, int WN, int BK, int NS, int PER_SIMD>
+template <class T, int AL, int BL, bool GATED, int BM, int BN, int WM, int WN, int BK, int SA, int SB, int PER_SIMD>
 __global__ __launch_bounds__(64 * WM * WN, PER_SIMD) void product_kernel(const Product p) {
   constexpr int NW = WM * WN, TM = BM / WM, TN = BN / WN;  // a wave's part of the tile
   constexpr int MI = TM / 32, NI = TN / 32, STEPS = BK / 16;
   using A = Operand<T, AL, BM, BK, NW>;
   using B = Operand<T, BL, BN, BK, NW>;
-  constexpr int STAGE = A::kBytes + B::kBytes, L = A::kLoads + B::kLoads;
-  static_assert(STEPS % 2 == 0 && NS >= 2 && (NS - 1) * L < 64, "fragments alternate, loads are counted");
+  constexpr int B_AT = SA * A::kBytes, LDS = B_AT + SB * B::kBytes;  // A's stages, then B's
+  static_assert(STEPS % 2 == 0 && SB >= 2 && (SA == SB || SA == SB + 1) && SA * A::kLoads + SB * B::kLoads < 64, "fragments alternate, loads are counted");
   static_assert(!GATED || (AL == kInside && BL == kInside && NI % 2 == 0), "gate and up blocks of a wave");
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[NS * STAGE];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[LDS];
   const uint32_t lds_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -405,70 +405,72 @@ __global__ __launch_bounds__(64 * WM * WN, PER_SIMD) void product_kernel(const P
     struct Stage { i32x4 buffer; uint32_t lds; int64_t left; };
     auto stage_a = [&](int s) __attribute__((always_inline)) {
       const int64_t k = (int64_t)(first + s) * BK;
-      return Stage{a.stage(k, k_end - k), lds_at + (uint32_t)(s % NS) * STAGE, k_end - k};
+      return Stage{a.stage(k, k_end - k), lds_at + (uint32_t)(s % SA) * A::kBytes, k_end - k};
     };
     auto stage_b = [&](int s) __attribute__((always_inline)) {
       const int64_t k = (int64_t)(first + s) * BK;
-      return Stage{b.stage(k, k_end - k), lds_at + (uint32_t)(s % NS) * STAGE + A::kBytes, k_end - k};
+      return Stage{b.stage(k, k_end - k), lds_at + B_AT + (uint32_t)(s % SB) * B::kBytes, k_end - k};
     };
     auto load_a = [&](auto u, const Stage& s) __attribute__((always_inline)) { a.template load<decltype(u)::value>(s.buffer, s.lds, wave, s.left); };
     auto load_b = [&](auto u, const Stage& s) __attribute__((always_inline)) { b.template load<decltype(u)::value>(s.buffer, s.lds, wave, s.left); };
 #pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      const Stage sa = stage_a(s);
-      each<A::kLoads>([&](auto u) __attribute__((always_inline)) { load_a(u, sa); });
-      if (s < NS - 1) {
-        const Stage sb = stage_b(s);
-        each<B::kLoads>([&](auto u) __attribute__((always_inline)) { load_b(u, sb); });
+    for (int s = 0; s < SB; ++s) {
+      if (s < SA - 1) {
+        const Stage sa = stage_a(s);
+        each<A::kLoads>([&](auto u) __attribute__((always_inline)) { load_a(u, sa); });
       }
+      const Stage sb = stage_b(s);
+      each<B::kLoads>([&](auto u) __attribute__((always_inline)) { load_b(u, sb); });
     }
     s16x8 fa[2][MI], fb[2][NI];
     // Fragment f of a step: B's, then A's, as the MFMAs want them.
-    auto read = [&](int buf, const uint8_t* stage, int step, int f) __attribute__((always_inline)) {
-      if (f < NI) fb[buf][f] = rb.read(stage + A::kBytes, f, step);
-      else fa[buf][f - NI] = ra.read(stage, f - NI, step);
+    auto read = [&](int buf, uint32_t in_a, uint32_t in_b, int step, int f) __attribute__((always_inline)) {
+      if (f < NI) fb[buf][f] = rb.read(lds + in_b, f, step);
+      else fa[buf][f - NI] = ra.read(lds + in_a, f - NI, step);
     };
-    wait_loads<(NS - 2) * L + A::kLoads>();
+    wait_loads<(SA - 2) * A::kLoads + (SB - 1) * B::kLoads>();
     block_sync();
 #pragma unroll
-    for (int f = 0; f < NI + MI; ++f) read(0, lds, 0, f);
+    for (int f = 0; f < NI + MI; ++f) read(0, 0, B_AT, 0, f);
     // Blocks of 32 rows of this wave that the output has; a tile without some skips their reads and MFMAs (not its
     // loads and barriers).
     const int64_t rows_left = at.rows - at.row - wm * TM;
     const int active = rows_left >= TM ? MI : rows_left > 0 ? (int)(rows_left + 31) / 32 : 0;
     auto run = [&](auto whole) __attribute__((always_inline)) {
       constexpr bool WHOLE = decltype(whole)::value;
-      uint32_t now = 0;  // LDS offset of the stage under way
+      uint32_t now_a = 0, now_b = B_AT;  // LDS offsets of the stage under way
     for (int s = 0; s < stages; ++s) {
-      const uint32_t next = now == (NS - 1) * STAGE ? 0 : now + STAGE;
-      Stage sb = stage_b(s + NS - 1), sa;
+      const uint32_t next_a = now_a == (SA - 1) * A::kBytes ? 0 : now_a + A::kBytes;
+      const uint32_t next_b = now_b == B_AT + (SB - 1) * B::kBytes ? B_AT : now_b + B::kBytes;
+      Stage sa = stage_a(s + SA - 1), sb;
       // a step: for every row block its share of the next step's reads, a load, its MFMAs
       each<STEPS>([&](auto step) __attribute__((always_inline)) {
         constexpr int t = decltype(step)::value;
         if constexpr (t == STEPS - 1) {
-          sa = stage_a(s + NS);
-          wait_loads<(NS - 2) * L>();
+          sb = stage_b(s + SB);
+          wait_loads<(SA - 2) * A::kLoads + (SB - 2) * B::kLoads>();
           block_sync();
         }
         each<MI>([&](auto block) __attribute__((always_inline)) {
           constexpr int i = decltype(block)::value;
-          if constexpr (t == STEPS - 1) each<A::kLoads>([&](auto u) __attribute__((always_inline)) {
-            if constexpr (decltype(u)::value * MI / A::kLoads == i) load_a(u, sa);
-          });
-          if constexpr (t == 0) each<B::kLoads>([&](auto u) __attribute__((always_inline)) {
+          if constexpr (t == STEPS - 1) each<B::kLoads>([&](auto u) __attribute__((always_inline)) {
             if constexpr (decltype(u)::value * MI / B::kLoads == i) load_b(u, sb);
+          });
+          if constexpr (t == 0) each<A::kLoads>([&](auto u) __attribute__((always_inline)) {
+            if constexpr (decltype(u)::value * MI / A::kLoads == i) load_a(u, sa);
           });
 #pragma unroll
           for (int f = i * (NI + MI) / MI; f < (i + 1) * (NI + MI) / MI; ++f)
             if (WHOLE || (f < NI ? 0 : f - NI) < active)
-              read((t + 1) & 1, lds + (t == STEPS - 1 ? next : now), (t + 1) % STEPS, f);
+              read((t + 1) & 1, t == STEPS - 1 ? next_a : now_a, t == STEPS - 1 ? next_b : now_b, (t + 1) % STEPS, f);
           if (WHOLE || i < active)
 #pragma unroll
           for (int j = 0; j < NI; ++j) acc[i][j] = mfma32<T>(fb[t & 1][j], fa[t & 1][i], acc[i][j]);
           __builtin_amdgcn_sched_barrier(0);
         });
       });
-      now = next;
+      now_a = next_a;
+      now_b = next_b;
     }
     };
     if (at.rows - at.row >= BM) run(std::true_type{});
@@ -484,7 +486,7 @@ __global__ __launch_bounds__(64 * WM * WN, PER_SIMD) void product_kernel(const P
   constexpr int C = TN, ROOM = C + 4;                 // columns of a wave
   constexpr int LANES = (GATED ? C / 2 : C) / 8;      // of a row
   constexpr int PASS = 64 / LANES, PASSES = 32 / PASS;
-  static_assert(NW * 32 * ROOM * 4 <= NS * STAGE, "the stages hold the waves' rooms");
+  static_assert(NW * 32 * ROOM * 4 <= LDS, "the stages hold the waves' rooms");
   float* room = (float*)lds + wave * 32 * ROOM;
   const int my_row = lane / LANES, my_col = lane % LANES * 8;
   const int col = at.col + wn * (GATED ? C / 2 : C) + my_col;
@@ -616,12 +618,11 @@ template <class T, int AL, int BL, bool GATED> inline int launch_product(Product
   }
   if (OVER_K || !p.rows.offsets) tiles *= p.splits;
   if (tiles > 0x7FFFFF) return NVFP4_ERR_INVALID;
-  constexpr int BK = AL == kInside ? 64 : 32;
   const dim3 grid((unsigned)tiles);
-  if (t.shape == 2) product_kernel<T, AL, BL, GATED, 256, 256, 2, 4, BK, 128 / BK, 2><<<grid, 512, 0, stream>>>(p);
-  else if (t.shape == 1) product_kernel<T, AL, BL, GATED, 256, 128, 4, 2, BK, 192 / BK, 2><<<grid, 512, 0, stream>>>(p);
-  else if (t.shape == 0) product_kernel<T, AL, BL, GATED, 128, 128, 2, 2, BK, 128 / BK, 2><<<grid, 256, 0, stream>>>(p);
-  else if constexpr (AL == kInside) product_kernel<T, AL, BL, GATED, 64, 128, 2, 2, BK, 3, 2><<<grid, 256, 0, stream>>>(p);
+  if (t.shape == 2) product_kernel<T, AL, BL, GATED, 256, 256, 2, 4, 64, 3, 2, 2><<<grid, 512, 0, stream>>>(p);
+  else if (t.shape == 1) product_kernel<T, AL, BL, GATED, 256, 128, 4, 2, 64, 3, 3, 2><<<grid, 512, 0, stream>>>(p);
+  else if (t.shape == 0) product_kernel<T, AL, BL, GATED, 128, 128, 2, 2, 64, 2, 2, 2><<<grid, 256, 0, stream>>>(p);
+  else if constexpr (AL == kInside) product_kernel<T, AL, BL, GATED, 64, 128, 2, 2, 64, 3, 3, 2><<<grid, 256, 0, stream>>>(p);
   return launched();
 }
 
