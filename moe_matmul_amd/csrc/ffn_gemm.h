@@ -325,12 +325,19 @@ __global__ __launch_bounds__(64 * WM * WN, PER_SIMD) void product_kernel(const P
   at.k_row = 0;
   at.k = p.k;
   if (OVER_K || !p.rows.offsets) {
-    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
-    int64_t v = xcd_order(blockIdx.x, gridDim.x);
+    int64_t v;
+    if (OVER_K && p.rows.offsets) {
+      // experts have more and fewer rows: every XCD has its share of each one's tiles
+      const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n * p.splits, share = (tiles + kXcds - 1) / kXcds;
+      const int64_t i = blockIdx.x / kXcds;
+      at.expert = (int)(i / share);
+      v = blockIdx.x % kXcds * share + i % share;
+      if (v >= tiles) return;
+    } else {
+      v = xcd_order(blockIdx.x, gridDim.x);
+    }
     at.split = (int)(v % p.splits);
     v /= p.splits;
-    at.expert = (int)(v / tiles);
-    v -= at.expert * tiles;
     // down columns of kRasterWidth tiles
     const int64_t wide = (int64_t)p.tiles_m * kRasterWidth;
     const int super = (int)(v / wide), width = min(kRasterWidth, p.tiles_n - super * kRasterWidth);
@@ -609,14 +616,14 @@ template <class T, int AL, int BL, bool GATED> inline int launch_product(Product
   p.tiles_n = ceil_div(GATED ? p.ep.inner : p.n, cols);
   int64_t tiles;
   if (OVER_K) {
-    tiles = (int64_t)p.tiles_m * p.tiles_n * (p.rows.offsets ? p.rows.experts : 1);
+    tiles = (int64_t)p.tiles_m * p.tiles_n * p.splits;
+    if (p.rows.offsets) tiles = ceil_div64(tiles, kXcds) * kXcds * p.rows.experts;
   } else if (p.rows.offsets) {
     const int64_t most = p.m / bm + (p.rows.experts < p.m ? p.rows.experts : p.m) + 1;  // whole tiles, and a part of one for each
     tiles = ceil_div64(most * p.tiles_n * p.splits, 8 * kXcds) * (8 * kXcds);
   } else {
-    tiles = (int64_t)p.tiles_m * p.tiles_n;
+    tiles = (int64_t)p.tiles_m * p.tiles_n * p.splits;
   }
-  if (OVER_K || !p.rows.offsets) tiles *= p.splits;
   if (tiles > 0x7FFFFF) return NVFP4_ERR_INVALID;
   const dim3 grid((unsigned)tiles);
   if (t.shape == 2) product_kernel<T, AL, BL, GATED, 256, 256, 2, 4, 64, 3, 2, 2><<<grid, 512, 0, stream>>>(p);
