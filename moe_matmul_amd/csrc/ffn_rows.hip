@@ -44,7 +44,9 @@ template <class T> __global__ __launch_bounds__(256) void dequantize8_kernel(con
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < eights; i += step) {
     float v[8];
     values8(codes, scales, i, v);
-    store8<T>(out, stride == (int64_t)wide * 8 ? i * 8 : i / wide * stride + i % wide * 8, vec, v);
+    const int64_t at = stride == (int64_t)wide * 8 ? i * 8 : i / wide * stride + i % wide * 8;
+    if (vec && T::kBytes == 2) *(u32x4*)((uint16_t*)out + at) = pack16x8<T>(v);
+    else store8<T>(out, at, vec, v);
   }
 }
 
@@ -60,7 +62,7 @@ __global__ __launch_bounds__(256) void gather_kernel(const void* x, int64_t stri
       if constexpr (EIGHT) {
         float v[8];
         values8(codes, scales, from * wide + c, v);
-        store8<T>(out, (row * wide + c) * 8, true, v);
+        ((u32x4*)out)[row * wide + c] = pack16x8<T>(v);
       } else {
         ((u32x4*)out)[row * wide + c] = *(const u32x4*)((const uint16_t*)x + from * stride + c * 8);
       }
