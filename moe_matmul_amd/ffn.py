@@ -210,6 +210,12 @@ def rmsnorm_backward(dy, sum, weight, rstd, *, dsum=None, stream=None):
 
 # ---- products --------------------------------------------------------------------------
 
+def _kept(shape, like, cleared):
+    """What is kept beside an output: where that is given, and keeps its rows of no expert, cleared."""
+    make = torch.zeros if cleared else torch.empty
+    return make(shape, dtype=like.dtype, device=like.device)
+
+
 @_on_stream
 def linear(x, w, *, bias=None, activation=None, residual=None, plan=None, save=False, out=None, stream=None):
     """``y = act(x w^T + bias) + residual`` in one product; with ``save`` (y, z), z the activation's argument as
@@ -217,7 +223,7 @@ def linear(x, w, *, bias=None, activation=None, residual=None, plan=None, save=F
 
     ``x`` [rows, k] (fp16 or bf16), ``w`` [n, k], ``bias`` [n] (fp32 or x's type), ``residual`` [rows, n];
     ``activation``: None, "relu", "silu" or "gelu". With a ``plan``: rows sorted by expert, ``w`` [experts, n, k],
-    ``bias`` [experts, n]; rows of no expert are 0, or left as they are in an ``out`` that is given."""
+    ``bias`` [experts, n]; rows of no expert are 0 (in an ``out`` that is given they stay as they were)."""
     device = _gpu(x, "x")
     kind, act = _type16(x, "x"), _activation(activation)
     experts, n, k = _weights(w, plan, device, x.dtype)
@@ -229,7 +235,7 @@ def linear(x, w, *, bias=None, activation=None, residual=None, plan=None, save=F
     residual_stride = 0 if residual is None else _same(residual, "residual", (rows, n), x)
     clear = out is None
     out = _out(out, "out", (rows, n), x.dtype, device)
-    z = _out(None, "z", (rows, n), x.dtype, device) if save else None
+    z = _kept((rows, n), x, plan is not None and not clear) if save else None
     need = _need(c.nvfp4_ffn_product_workspace_bytes, device, rows, n, k, experts)
     room = _room(need, device)
     _enqueue(c.nvfp4_ffn_linear, device, x.data_ptr(), stride, w.data_ptr(), _at(bias), f32, act, _at(residual),
@@ -313,7 +319,7 @@ def gated(x, w, *, activation="silu", plan=None, save=None, out=None, stream=Non
 
     ``x`` [tokens, k] (fp16 or bf16), ``w`` [2 * inner, k]: the gate's rows, then the other's; h [tokens, inner]. With a
     ``plan``: ``w`` [experts, 2 * inner, k], and h [tokens * topk, inner] has the rows of every slot sorted by expert,
-    each from its token's row; rows of no expert are 0, or left as they are in an ``out`` that is given.
+    each from its token's row; rows of no expert are 0 (in an ``out`` that is given they stay as they were).
     ``save``: "rows" or "rows8" gives (h, kept), both projections [rows, 2 * inner] in 16 bits or as a Rows8, for
     ``gated_backward``."""
     device = _gpu(x, "x")
@@ -329,10 +335,13 @@ def gated(x, w, *, activation="silu", plan=None, save=None, out=None, stream=Non
     rows = x.shape[0] if plan is None else plan.rows
     clear = out is None
     h = _out(out, "out", (rows, n // 2), x.dtype, device)
-    kept = _out(None, "kept", (rows, n), x.dtype, device) if save == "rows" else None
+    kept = _kept((rows, n), x, plan is not None and not clear) if save == "rows" else None
     if save == "rows8" and n % 64:
         raise ValueError(f"projections in 8 bits must have a multiple of 32 columns each, not {n // 2}")
     kept8 = _out8(None, "kept", (rows, n), device) if save == "rows8" else None
+    if kept8 is not None and plan is not None and not clear:
+        kept8.codes.zero_()
+        kept8.scales.zero_()
     _gated(x, stride, w, act, kind, rows, n // 2, k, plan, experts, h, kept, kept8, clear)
     return h if save is None else (h, kept if kept8 is None else kept8)
 

@@ -415,6 +415,37 @@ def test_experts(i, dtype):
         out = torch.full((rows, width), math.nan, device="cuda", dtype=t)
         call(out)
         assert bool(out[end:].isnan().all()) and not bool(out[:end].isnan().any())
+    out = torch.empty(rows, inner, device="cuda", dtype=t)
+    same(ffn.gated(x, w1, plan=p, out=out, save="rows")[1], kept)
+    again8 = ffn.gated(x, w1, plan=p, out=out, save="rows8")[1]
+    same(again8.codes, kept8.codes)
+    assert bool((FO.values8(*again8)[end:] == 0).all())
+    out = torch.empty(rows, hidden, device="cuda", dtype=t)
+    same(ffn.linear(h, w2, bias=bias, activation="gelu", residual=residual, plan=p, out=out, save=True)[1], z)
+
+
+@pytest.mark.parametrize("rows", [1, 2, 7, 8])
+@pytest.mark.parametrize("k", [8, 56, 1992, 2048, 2056, 8184, 8192, 8200, 16384, 24616])
+def test_few_rows_of_any_length(rows, k):
+    """One chunk of k, several, and ragged last ones; captured by the first call of its kind."""
+    r = rng(rows, k)
+    x, w = r(rows, k).bfloat16(), (r(48, k) * k ** -0.5).bfloat16()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, h = ffn.linear(x, w), ffn.gated(x, w)
+    graph.replay()
+    f = lambda v: v.double()  # noqa: E731
+    bz = (k + 16) * H * (f(x).abs() @ f(w).abs().T)
+    z = f(x) @ f(w).T
+    close(y, z, bz)
+    (g, u), (bg, bu) = z.chunk(2, 1), bz.chunk(2, 1)
+    want = FO.gated(f(x), f(w))[0]
+    close(h, want, act_error(g, bg, "silu") * (u.abs() + bu) + FO.activation(g, "silu").abs() * bu + 2 * H * want.abs())
+    p = moe.plan(torch.arange(rows, device="cuda", dtype=torch.int32).view(-1, 1) % 3, 3)
+    w3 = torch.stack((w, w * 2, w * 4))
+    rows_of = p.row_slots.long()
+    scale = torch.tensor([1.0, 2.0, 4.0], device="cuda", dtype=torch.float64)[rows_of % 3].unsqueeze(1)
+    same(ffn.linear(x[rows_of].contiguous(), w3, plan=p), (f(ffn.linear(x, w))[rows_of] * scale).bfloat16())
 
 
 def test_a_plan_of_one_expert_is_dense():
