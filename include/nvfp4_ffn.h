@@ -8,7 +8,7 @@
  *   nvfp4_ffn_rmsnorm          s = x + residual, its norm, in 16 or 8 bits
  *   nvfp4_ffn_gated            h = act(x Wg^T) * (x Wu^T)
  *   nvfp4_ffn_linear           y = act(h W^T + bias) + residual
- *   nvfp4_ffn_linear_dz, _dx, _dw;  nvfp4_ffn_gated_dz, _dx, _dw (those of linear)
+ *   nvfp4_ffn_linear_dz, _dx, _dw;  nvfp4_ffn_gated_dz or _again, _dx, _dw (those of linear)
  *   nvfp4_ffn_rmsnorm_backward
  *
  * Types. Rows and weights are fp16 or bf16 (`dtype`: NVFP4_MOE_F16, NVFP4_MOE_BF16;
@@ -169,6 +169,14 @@ size_t nvfp4_ffn_dz_workspace_bytes(int64_t rows, int n, int experts);
  */
 int nvfp4_ffn_gated_dz(const void* dh, int64_t dh_stride, const void* kept, const void* codes, const void* scales, int act,
                        void* dz, int dtype, int64_t rows, int inner, const nvfp4_ffn_plan* plan, void* stream);
+
+/*
+ * nvfp4_ffn_gated_again - the same dz with g and u computed again from x (as in nvfp4_ffn_gated) and not rounded on the
+ * way: nothing of the forward pass need be kept but x. Rows of no expert are not written.
+ */
+int nvfp4_ffn_gated_again(const void* dh, int64_t dh_stride, const void* x, int64_t x_stride, const void* w, int act,
+                          void* dz, int dtype, int64_t rows, int inner, int k, const nvfp4_ffn_plan* plan,
+                          void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * nvfp4_ffn_linear_dx - dx [rows][k] = dz W; dz device [rows][n], rows dz_stride apart; w as in nvfp4_ffn_linear.

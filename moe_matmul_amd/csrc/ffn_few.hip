@@ -46,12 +46,12 @@ template <class T, int U, int R, bool GATED> __global__ __launch_bounds__(1024, 
   const uint8_t* x_at = xs + i % R * stride + q * 16;  // (rows from R on are never stored: any of them will do)
 
   for (int64_t row0 = lo; row0 < hi; row0 += R) {
-    // the residual of the finishing threads, before the weights
+    // the residual (or dh) of the finishing threads, before the weights
     constexpr int EIGHTS = GATED ? 1 : 2;
     const int my_row = threadIdx.x / EIGHTS, my_col = n0 + threadIdx.x % EIGHTS * 8;
     const bool mine = my_row < R && row0 + my_row < hi && my_col < (GATED ? p.ep.inner : p.n);
     u32x4 residual = {0, 0, 0, 0};
-    if (!GATED && mine && live && p.ep.residual)
+    if (mine && live && p.ep.residual)
       residual = *(const u32x4*)((const uint16_t*)p.ep.residual + (row0 + my_row) * p.ep.ldr + my_col);
     f32x4 acc = {0, 0, 0, 0};
     if (live) {
@@ -101,7 +101,8 @@ template <class T, int U, int R, bool GATED> __global__ __launch_bounds__(1024, 
       load8<F32>(&room[0][my_row][GATED ? 0 : my_col - n0], 0, true, v);
       if (GATED) load8<F32>(&room[0][my_row][8], 0, true, u);
       if constexpr (GATED) {
-        finish_gated<T>(p.ep, row0 + my_row, my_col, v, u);
+        if (p.ep.residual) finish_gated_dz<T>(p.ep, row0 + my_row, my_col, v, u, residual);
+        else finish_gated<T>(p.ep, row0 + my_row, my_col, v, u);
       } else {
         float bias[8] = {}, r[8];
         if (p.ep.bias && live) param8<T>(p.ep.bias, (int64_t)e * p.n + my_col, p.ep.bias_f32, true, bias);

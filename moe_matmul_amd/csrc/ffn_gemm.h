@@ -76,7 +76,7 @@ struct Epilogue {
   int y_f32;               // fp32 in place of the rows' type
   const void* bias;        // [n] of each expert
   int bias_f32, act;
-  const void* residual;    // rows ldr apart
+  const void* residual;    // rows ldr apart; gated: dh, and y is dz [m][2 * inner] instead of h
   int64_t ldr;
   void* z;                 // [m][n]
   // gated: n = 2 * inner columns, y [m][inner]
@@ -97,6 +97,21 @@ __device__ __forceinline__ void finish_linear(const Epilogue& p, int n, int64_t 
   for (int j = 0; j < 8; ++j) v[j] += r[j];
   if (p.y_f32) store8<F32>(p.y, row * p.ldy + col, true, v);
   else *(u32x4*)((uint16_t*)p.y + row * p.ldy + col) = pack16x8<T>(v);
+}
+// dz of eight columns from g, u and dh.
+template <class T>
+__device__ __forceinline__ void finish_gated_dz(const Epilogue& p, int64_t row, int col, float* g, float* u, u32x4 dh) {
+  float d[8], a[8];
+  unpack16x8<T>(dh, d);
+  values_slopes8(g, a, p.act);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    g[j] *= d[j] * u[j];
+    u[j] = d[j] * a[j];
+  }
+  uint16_t* at = (uint16_t*)p.y + row * p.ldy + col;
+  *(u32x4*)at = pack16x8<T>(g);
+  *(u32x4*)(at + p.inner) = pack16x8<T>(u);
 }
 // h, and g and u where they are kept in 16 bits, of eight columns.
 template <class T>
@@ -502,7 +517,7 @@ __global__ __launch_bounds__(64 * WM * WN, PER_SIMD) void product_kernel(const P
   const int64_t out0 = OVER_K ? at.expert * p.m : 0;  // output row of the tile's row 0
   float* partial = parts ? p.partial + at.split * p.partial_step + out0 * p.n : nullptr;
   const bool has_bias = !GATED && BL == kInside && p.ep.bias && at.live && !parts;
-  const bool has_residual = !GATED && BL == kInside && p.ep.residual && at.live && !parts;
+  const bool has_residual = BL == kInside && p.ep.residual && at.live && !parts;
   float bias[8] = {};
   if (has_bias && in_cols) param8<T>(p.ep.bias, (int64_t)at.expert * p.n + col, p.ep.bias_f32, true, bias);
   // the residual of a pass; out of range: 0
@@ -579,10 +594,13 @@ __global__ __launch_bounds__(64 * WM * WN, PER_SIMD) void product_kernel(const P
         finish_linear<T>(p.ep, p.n, out0 + row, col, v, bias, r);
       }
     } else {
+      u32x4 next = has_residual ? residual_at(first_of) : u32x4{0, 0, 0, 0};
 #pragma unroll 1
       for (int q = 0; q < PASSES; ++q) {
         const int64_t row = first_of + q * PASS;
         const bool in = row < at.rows && in_cols;
+        const u32x4 dh = next;
+        if (has_residual && q + 1 < PASSES) next = residual_at(row + PASS);
         float g[8], u[8];
         load8<F32>(from, q * PASS * ROOM, true, g);
         load8<F32>(from, q * PASS * ROOM + C / 2, true, u);
@@ -591,6 +609,10 @@ __global__ __launch_bounds__(64 * WM * WN, PER_SIMD) void product_kernel(const P
             store8<F32>(partial, row * p.n + col, true, g);
             store8<F32>(partial, row * p.n + p.ep.inner + col, true, u);
           }
+          continue;
+        }
+        if (has_residual) {
+          if (in) finish_gated_dz<T>(p.ep, row, col, g, u, dh);
           continue;
         }
         if (p.ep.codes) finish_codes(p.ep, row, col, in, g, u);

@@ -173,6 +173,10 @@ template <class T, bool GATED, bool OVER_K> __global__ __launch_bounds__(256) vo
     }
   }
   if constexpr (GATED) {
+    if (p.ep.residual) {
+      if (in) finish_gated_dz<T>(p.ep, row, col, v, u, *(const u32x4*)((const uint16_t*)p.ep.residual + row * p.ep.ldr + col));
+      return;
+    }
     if (p.ep.codes) finish_codes(p.ep, row, col, in, v, u);  // (inner % 32 == 0: a row's lanes come in fours)
     if (in) finish_gated<T>(p.ep, row, col, v, u);
   } else {
@@ -336,6 +340,24 @@ int nvfp4_ffn_gated(const void* x, int64_t x_stride, const void* w, int act, voi
   p.ep.y = h; p.ep.ldy = inner; p.ep.act = act; p.ep.inner = inner; p.ep.kept = kept;
   p.ep.codes = (uint8_t*)codes; p.ep.scales = (uint8_t*)scales;
   return run_product(codes ? kForwardCodes : kForward, p, true, dtype, workspace, workspace_bytes, stream);
+}
+
+int nvfp4_ffn_gated_again(const void* dh, int64_t dh_stride, const void* x, int64_t x_stride, const void* w, int act,
+                          void* dz, int dtype, int64_t rows, int inner, int k, const nvfp4_ffn_plan* plan,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+  if (!type16(dtype) || !known_activation(act) || act == NVFP4_FFN_NONE || !rows_ok(rows) || !side_ok(inner) ||
+      !side_ok(k) || 2 * inner > kMaxSide)
+    return NVFP4_ERR_INVALID;
+  Product p{};
+  if (const int rc = plan_rows(plan, rows, plan != nullptr, &p.rows)) return rc;
+  if (rows == 0) return NVFP4_OK;
+  if (!dh || !x || !w || !dz || dh_stride < inner || !stride_ok(x_stride, k) || (int64_t)2 * inner * k * 2 > kMaxBytes) return NVFP4_ERR_INVALID;
+  if (plan && p.rows.sources * x_stride * 2 > kMaxBytes) return NVFP4_ERR_INVALID;
+  if (!wide16(dh) || !wide16(x) || !wide16(w) || !wide16(dz) || x_stride % 8 || dh_stride % 8) return NVFP4_ERR_MISALIGNED;
+  p.a = x; p.b = w; p.lda = x_stride; p.ldb = k; p.m = rows; p.n = 2 * inner; p.k = k; p.b_step = (int64_t)2 * inner * k;
+  p.ep.y = dz; p.ep.ldy = 2 * inner; p.ep.act = act; p.ep.inner = inner;
+  p.ep.residual = dh; p.ep.ldr = dh_stride;
+  return run_product(kForward, p, true, dtype, workspace, workspace_bytes, stream);
 }
 
 int nvfp4_ffn_linear_dx(const void* dz, int64_t dz_stride, const void* w, void* dx, int dtype, int64_t rows, int n, int k,

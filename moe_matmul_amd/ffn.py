@@ -305,14 +305,6 @@ def linear_backward(dy, x, w, *, bias=None, z=None, activation=None, plan=None, 
 
 # ---- the gated projections -----------------------------------------------------------------
 
-def _gated(x, stride, w, act, kind, rows, inner, k, plan, experts, h, kept, kept8, clear):
-    device = w.device
-    need = _need(c.nvfp4_ffn_product_workspace_bytes, device, rows, 2 * inner, k, experts)
-    room = _room(need, device)
-    _enqueue(c.nvfp4_ffn_gated, device, x.data_ptr(), stride, w.data_ptr(), act, h.data_ptr(), _at(kept),
-             _at(kept8 and kept8.codes), _at(kept8 and kept8.scales), kind, rows, inner, k, _plan(plan), clear, _at(room), need)
-
-
 @_on_stream
 def gated(x, w, *, activation="silu", plan=None, save=None, out=None, stream=None):
     """``h = act(x wg^T) * (x wu^T)``, both projections, the activation and the product in one kernel.
@@ -342,7 +334,10 @@ def gated(x, w, *, activation="silu", plan=None, save=None, out=None, stream=Non
     if kept8 is not None and plan is not None and not clear:
         kept8.codes.zero_()
         kept8.scales.zero_()
-    _gated(x, stride, w, act, kind, rows, n // 2, k, plan, experts, h, kept, kept8, clear)
+    need = _need(c.nvfp4_ffn_product_workspace_bytes, device, rows, n, k, experts)
+    room = _room(need, device)
+    _enqueue(c.nvfp4_ffn_gated, device, x.data_ptr(), stride, w.data_ptr(), act, h.data_ptr(), _at(kept),
+             _at(kept8 and kept8.codes), _at(kept8 and kept8.scales), kind, rows, n // 2, k, _plan(plan), clear, _at(room), need)
     return h if save is None else (h, kept if kept8 is None else kept8)
 
 
@@ -351,7 +346,7 @@ def gated_backward(dh, x, w, kept=None, *, activation="silu", plan=None, dw=None
     """(dx, dw) of ``gated``: dx [tokens, k] (with a plan the sum over each token's slots), dw like w.
 
     ``x``: the rows as they were given, or a Rows8 of them (of the norm, or by ``quantize8``); ``kept``: what
-    ``gated(..., save=)`` gave, or None: both projections are computed again from x. ``dw``: a tensor to take w's
+    ``gated(..., save=)`` gave, or None: both projections are computed again from x, and not rounded. ``dw``: a tensor to take w's
     gradient, of w's type or fp32. The projections' gradients are rounded to 16 bits for the products, and with a plan
     the slots' dx before their sum."""
     device = _gpu(dh, "dh")
@@ -386,17 +381,19 @@ def gated_backward(dh, x, w, kept=None, *, activation="silu", plan=None, dw=None
         rows_x, rows_stride = xs, k
     else:
         rows_x, rows_stride = x, x_stride
-    if kept is None:
-        if isinstance(x, Rows8) and plan is not None:
-            x = dequantize8(x, dtype=dh.dtype)
-        again, again_stride = (rows_x, rows_stride) if plan is None else (x, k if x.dtype != dh.dtype else _rows(x, "x"))
-        kept = torch.empty((rows, n), dtype=dh.dtype, device=device)
-        h = torch.empty((rows, inner), dtype=dh.dtype, device=device)
-        _gated(again, again_stride, w, act, kind, rows, inner, k, plan, experts, h, kept, None, 0)
     dz = torch.empty((rows, n), dtype=dh.dtype, device=device)
-    eight = isinstance(kept, Rows8)
-    _enqueue(c.nvfp4_ffn_gated_dz, device, dh.data_ptr(), stride, 0 if eight else kept.data_ptr(),
-             kept.codes.data_ptr() if eight else 0, kept.scales.data_ptr() if eight else 0, act, dz.data_ptr(), kind, rows,
-             inner, _plan(plan))
+    if kept is None:
+        if plan is not None and isinstance(x, Rows8):
+            x = dequantize8(x, dtype=dh.dtype)
+        again, again_stride = (rows_x, rows_stride) if plan is None else (x, _rows(x, "x"))
+        need = _need(c.nvfp4_ffn_product_workspace_bytes, device, rows, n, k, experts)
+        room = _room(need, device)
+        _enqueue(c.nvfp4_ffn_gated_again, device, dh.data_ptr(), stride, again.data_ptr(), again_stride, w.data_ptr(), act,
+                 dz.data_ptr(), kind, rows, inner, k, _plan(plan), _at(room), need)
+    else:
+        eight = isinstance(kept, Rows8)
+        _enqueue(c.nvfp4_ffn_gated_dz, device, dh.data_ptr(), stride, 0 if eight else kept.data_ptr(),
+                 kept.codes.data_ptr() if eight else 0, kept.scales.data_ptr() if eight else 0, act, dz.data_ptr(), kind,
+                 rows, inner, _plan(plan))
     dx, dw = _products_back(dz, n, rows_x, rows_stride, w, plan, kind, experts, dw)
     return (dx if plan is None else moe.combine(dx, None, plan, dtype=dh.dtype)), dw

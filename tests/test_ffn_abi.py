@@ -181,6 +181,13 @@ def test_gradients_refuse():
         refused(INVALID, gdz, *args, BF16, 4, 64, None, 0)
     refused(INVALID, gdz, P, 40, 0, P, P, 2, P, BF16, 4, 40, None, 0)
     refused(MISALIGNED, gdz, P, 64, P + 8, 0, 0, 2, P, BF16, 4, 64, None, 0)
+    names = "dh dh_stride x x_stride w act dz dtype rows inner k plan ws ws_bytes stream"
+    ok = dict(dh=P, dh_stride=64, x=P, x_stride=64, w=P, act=2, dz=P, dtype=BF16, rows=4, inner=64, k=64, plan=None, ws=0, ws_bytes=0, stream=0)
+    for code, bad in ((INVALID, dict(dh=0)), (INVALID, dict(x=0)), (INVALID, dict(w=0)), (INVALID, dict(dz=0)), (INVALID, dict(act=0)),
+                      (INVALID, dict(dtype=F32)), (INVALID, dict(dh_stride=56)), (INVALID, dict(x_stride=56)), (INVALID, dict(inner=60)),
+                      (INVALID, dict(k=60)), (INVALID, dict(rows=-1)), (INVALID, dict(plan=plan_of(topk=3))), (MISALIGNED, dict(dh=P + 8)),
+                      (MISALIGNED, dict(dz=P + 8)), (MISALIGNED, dict(dh_stride=68)), (WORKSPACE, dict(rows=33, inner=2048, dh_stride=2048, k=7168, x_stride=7168))):
+        with_(c.nvfp4_ffn_gated_again, names, ok, code, **bad)
     gather = c.nvfp4_ffn_gather
     refused(INVALID, gather, P, 64, 0, 0, BF16, 4, 64, None, P, 0)
     refused(INVALID, gather, 0, 64, P, P, BF16, 4, 40, plan_of(), P, 0)
