@@ -36,7 +36,8 @@
  * gradients of weights, which are then 0. rows < 2^31.
  *
  * Products need n % 8 == 0 and k % 8 == 0, both 1 .. 2^20, and addresses and rows of
- * operands at multiples of 16 bytes; an expert's weights stay below 2^31 bytes.
+ * operands at multiples of 16 bytes; an expert's weights stay below 2^31 bytes. A product has fewer than 2^23 tiles of
+ * 256 x 256 (2^31 - 2^15 rows of up to 256 columns, 2^24 rows of 30000).
  */
 #ifndef NVFP4_FFN_H
 #define NVFP4_FFN_H

@@ -627,6 +627,7 @@ struct Tiling {
   int shape;   // 0: 128 x 128, 1: 256 x 128, 2: 256 x 256, 3: 64 x 128 (rows with k inside)
   int splits;
 };
+constexpr int64_t kMostTiles = 0x7FFFFF;  // workgroups of 512 threads in a launch: below 2^32 threads
 inline int tile_rows(int shape) { return shape == 3 ? 64 : shape ? 256 : 128; }
 inline int tile_cols(int shape) { return shape == 2 ? 256 : 128; }
 
@@ -646,7 +647,7 @@ template <class T, int AL, int BL, bool GATED> inline int launch_product(Product
   } else {
     tiles = (int64_t)p.tiles_m * p.tiles_n * p.splits;
   }
-  if (tiles > 0x7FFFFF) return NVFP4_ERR_INVALID;
+  if (tiles > kMostTiles) return NVFP4_ERR_INVALID;
   const dim3 grid((unsigned)tiles);
   if (t.shape == 2) product_kernel<T, AL, BL, GATED, 256, 256, 2, 4, 64, 3, 2, 2><<<grid, 512, 0, stream>>>(p);
   else if (t.shape == 1) product_kernel<T, AL, BL, GATED, 256, 128, 4, 2, 64, 3, 3, 2><<<grid, 512, 0, stream>>>(p);

@@ -70,6 +70,8 @@ static Tiling choose_tiling(int64_t rows, int cols, int64_t k, int experts, bool
       if (high < some) high = some;
     }
     const double tiles = high * ceil_div(cols, bn) * e;
+    // (of more than the largest tiles can cover, launch_product tells)
+    if (shape != 2 && ((double)rows / bm + experts + 1) * ceil_div(cols, bn) * e + 8 * kXcds > kMostTiles) continue;
     for (int splits = 1; splits <= 16; splits += splits < 4 ? 1 : splits < 8 ? 2 : 4) {
       if (splits > 1 && stages / splits < 4) break;
       const double all = tiles * splits, room = shape == 1 || shape == 2 ? units : 2.0 * units;

@@ -103,11 +103,12 @@ __device__ __forceinline__ bool find_chunk(const Rows& p, int64_t index, int lan
 // dz = dy act'(z), and with `partial` [chunks][n] the columns' sums of the chunk's rows: each thread every eighth row
 // of eight columns, the eight threads of a column in order.
 template <class T> __global__ __launch_bounds__(256) void linear_dz_kernel(const void* dy, int64_t dy_stride, const void* z, int act, void* dz,
-                                                                           int n, Rows p, float* partial) {
+                                                                           int n, Rows p, int64_t chunks, float* partial) {
   __shared__ float room[8][kChunkCols];
   const int64_t chunk = blockIdx.y + (int64_t)blockIdx.z * gridDim.y;
   int64_t row, end;
-  if (!find_chunk(p, chunk, threadIdx.x & 63, row, end)) return;
+  // (tables that do not fit together may name more chunks than there is room for)
+  if (chunk >= chunks || !find_chunk(p, chunk, threadIdx.x & 63, row, end)) return;
   const int col = blockIdx.x * kChunkCols + threadIdx.x % 32 * 8, first = threadIdx.x / 32;
   float sum[8] = {};
   if (col < n) {
@@ -200,7 +201,7 @@ __global__ __launch_bounds__(kAddThreads) void add_columns_kernel(const float* p
       before += hi > lo ? (hi - lo + kChunkRows - 1) / kChunkRows : 0;
     }
 #pragma unroll
-    for (int d = 32; d; d /= 2) before += __shfl_xor((int)before, d, 64);
+    for (int d = 32; d; d /= 2) before += __shfl_xor((long long)before, d, 64);
     const int64_t lo = first_row(p, e), hi = first_row(p, e + 1);
     begin = min(before, parts);
     end = min(begin + (hi > lo ? (hi - lo + kChunkRows - 1) / kChunkRows : 0), parts);
@@ -282,7 +283,7 @@ int nvfp4_ffn_dequantize8(const void* codes, const void* scales, int64_t rows, i
 
 int nvfp4_ffn_gather(const void* x, int64_t x_stride, const void* codes, const void* scales, int dtype, int64_t tokens,
                      int n, const nvfp4_ffn_plan* plan, void* out, void* stream) {
-  if (!type16(dtype) || tokens < 0 || !plan || plan->topk < 1 || plan->topk > NVFP4_MOE_MAX_TOPK ||
+  if (!type16(dtype) || !rows_ok(tokens) || !plan || plan->topk < 1 || plan->topk > NVFP4_MOE_MAX_TOPK ||
       !rows_ok(tokens * plan->topk) || !width_ok(n, x ? 8 : kBlock8))
     return NVFP4_ERR_INVALID;
   const int64_t rows = tokens * plan->topk;
@@ -332,7 +333,7 @@ int nvfp4_ffn_linear_dz(const void* dy, int64_t dy_stride, const void* z, int ac
   const unsigned high = 32768, grid_y = (unsigned)(chunks < high ? chunks : high);
   const dim3 grid(ceil_div(n, kChunkCols), grid_y, (unsigned)ceil_div64(chunks, grid_y));
   with_type16(dtype, [&](auto type) {
-    linear_dz_kernel<decltype(type)><<<grid, 256, 0, (hipStream_t)stream>>>(dy, dy_stride, z, act, dz, n, p,
+    linear_dz_kernel<decltype(type)><<<grid, 256, 0, (hipStream_t)stream>>>(dy, dy_stride, z, act, dz, n, p, chunks,
                                                                            dbias ? (float*)workspace : nullptr);
     return 0;
   });

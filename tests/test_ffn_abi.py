@@ -144,6 +144,12 @@ def test_plans_that_gather_are_refused(code, bad):
     refused(code, c.nvfp4_ffn_gated, P, 64, P, 2, P, 0, 0, 0, BF16, 4, 64, 64, plan_of(**bad), 1, 0, 0, 0)
 
 
+@pytest.mark.parametrize("tokens", [-1, 1 << 30, 1 << 31, 1 << 62, (1 << 63) - 1])
+def test_gather_refuses_more_rows_than_there_can_be(tokens):
+    """1 << 62 tokens of four slots are 0 rows in 64 bits."""
+    refused(INVALID, c.nvfp4_ffn_gather, P, 64, 0, 0, BF16, tokens, 64, plan_of(topk=4), P, 0)
+
+
 GATED_ARGS = "x x_stride w act h kept codes scales dtype rows inner k plan clear ws ws_bytes stream"
 GATED_OK = dict(x=P, x_stride=64, w=P, act=2, h=P, kept=P, codes=P, scales=P, dtype=F16, rows=4, inner=64, k=64, plan=None,
                 clear=1, ws=0, ws_bytes=0, stream=0)
@@ -224,6 +230,14 @@ def test_parts_cover_the_rows_and_fit_the_workspace(kind):
                     assert 1 <= splits <= 16
                     r *= max(experts, 1) if kind == c.NVFP4_FFN_DW else 1
                     assert splits == 1 or r * cols * 4 * splits <= have
+
+
+@pytest.mark.parametrize("rows,n,k", [(1 << 30, 8, 64), ((1 << 31) - (1 << 15), 8, 8), (1 << 25, 8192, 64), (1 << 24, 30000, 8)])
+@pytest.mark.parametrize("experts", [0, 8])
+def test_products_of_the_most_rows_fit_one_launch(rows, n, k, experts):
+    for kind in (c.NVFP4_FFN_FORWARD, c.NVFP4_FFN_FORWARD_CODES):
+        for r, tile, cols, splits in c.nvfp4_ffn_product_parts(kind, rows, n, k, experts):
+            assert (r // tile + experts + 1) * -(-n // cols) * splits + 64 < 1 << 23
 
 
 def test_gpu_cases_reach_every_kernel():

@@ -14,6 +14,7 @@ Tolerances. H(t) is half a step of a type relative to the value: fp32 2^-24, fp1
   in chains of 32 and 11 levels: 64 H of the terms' magnitude; dweight: chains of at most rows / 256 + 40 roundings.
 * column sums: chains of 8, 8 and rows / 64 / 32 + 16 roundings: (rows / 2048 + 40) H of the terms' magnitude.
 """
+import ctypes
 import math
 import sys
 import zlib
@@ -475,6 +476,21 @@ def test_tables_that_name_nothing_are_harmless():
     p.row_slots[3] = 1 << 20
     h = ffn.gated(x, w, plan=p)
     assert bool((h[3] == 0).all()) and not bool((h[4] == 0).all())
+
+
+def test_tables_that_name_too_many_rows_stay_in_the_workspace():
+    """Experts that overlap have more chunks of rows than the sums of bias gradients have room for, beside a launch that
+    is rounded up (32768 chunks and more)."""
+    rows, n, experts = 64 * 32768 + 128, 8, 4
+    offsets = torch.tensor([0, rows, 0, rows, 0], dtype=torch.int32, device="cuda")
+    plan = c.nvfp4_ffn_plan(experts, 1, offsets.data_ptr(), 0)
+    dy, z = torch.ones(rows, n, device="cuda").bfloat16(), torch.ones(rows, n, device="cuda").bfloat16()
+    dz, dbias = torch.zeros_like(z), torch.zeros(experts, n, device="cuda")
+    need = c.nvfp4_ffn_dz_workspace_bytes(rows, n, experts)
+    room = torch.full((need // 4 + 40000 * n,), 7.0, device="cuda")
+    c.nvfp4_ffn_linear_dz(dy.data_ptr(), n, z.data_ptr(), c.NVFP4_FFN_RELU, dz.data_ptr(), dbias.data_ptr(), 1, 2, rows, n,
+                          ctypes.byref(plan), room.data_ptr(), need, torch.cuda.current_stream().cuda_stream)
+    assert bool((room[need // 4:] == 7).all())
 
 
 # ---- strides, values that are none, types -----------------------------------------------------
