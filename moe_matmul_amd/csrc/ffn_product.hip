@@ -96,12 +96,13 @@ static Tiling choose_tiling(int64_t rows, int cols, int64_t k, int experts, bool
 // ---- how a product is computed ------------------------------------------------------
 enum Kind { kForward = NVFP4_FFN_FORWARD, kForwardCodes = NVFP4_FFN_FORWARD_CODES, kDx = NVFP4_FFN_DX, kDw = NVFP4_FFN_DW };
 
-// Whether the kernel of few rows is the faster one: for up to so many rows (4096 x 7168, bf16: 1 row 15 us, 4 rows 16, 16
-// rows 22, against 18 in 64 x 128 tiles and parts of k). By experts (0: dense) their mean counts: one that has more
-// takes several passes.
-constexpr int kFewRows = 8;
+// Whether the kernel of few rows is the faster one: for up to so many rows (8 rows, against 64 x 128 tiles and parts of
+// k: 4096 x 7168 17.8 and 23 us, 28672 x 4096 53 and 70; more than 8 read the weights twice). By experts their mean
+// counts, as one with more than 8 rows takes several passes: 4 rows an expert (64 of 2048 x 2048) 113 and 129, 8 rows
+// 170 and 130.
+constexpr int kFewRows = 8, kFewRowsOfExpert = 4;
 static bool few_rows(Kind kind, int64_t rows, int experts) {
-  return kind == kForward && rows <= kFewRows * (experts > 1 ? experts : 1);
+  return kind == kForward && rows <= (experts > 1 ? kFewRowsOfExpert * experts : kFewRows);
 }
 
 // Rows row0 .. row0 + rows - 1 of the output, by few rows or by tiles.

@@ -447,6 +447,52 @@ def test_few_rows_of_any_length(rows, k):
     same(ffn.linear(x[rows_of].contiguous(), w3, plan=p), (f(ffn.linear(x, w))[rows_of] * scale).bfloat16())
 
 
+# tokens, topk, experts, inner, hidden, share of slots dropped, the only expert: up to 4 rows an expert, of which many or
+# few have any, some more than one pass takes, and k that 16 waves and fewer share
+FEW = [(1, 8, 64, 1024, 256, 0.0, None), (3, 8, 256, 264, 520, 0.3, None), (64, 4, 64, 504, 72, 0.0, None), (60, 4, 300, 136, 2048, 0.1, None),
+       (13, 4, 16, 4096, 1000, 0.0, None), (1, 1, 8, 8, 8, 0.0, None), (32, 4, 32, 2056, 2056, 0.5, None), (50, 1, 64, 512, 136, 0.2, 63),
+       (2, 16, 256, 8, 24576, 0.0, None), (30, 1, 16, 1032, 40, 99.0, None), (1, 1, 1, 28680, 136, 0.0, None), (8, 1, 1, 40000, 1024, 0.0, None)]
+
+
+@pytest.mark.parametrize("i", range(len(FEW)), ids=lambda i: "-".join(map(str, FEW[i])))
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_few_rows_of_many_experts(i, dtype):
+    tokens, topk, experts, inner, hidden, dropped, only = FEW[i]
+    t, r = TYPES[dtype], rng(*FEW[i], dtype)
+    x = r(tokens, hidden).to(t)
+    w1, w2 = (r(experts, 2 * inner, hidden) * hidden ** -0.5).to(t), (r(experts, hidden, inner) * inner ** -0.5).to(t)
+    bias = r(experts, hidden)
+    p = moe.plan(pick(r, tokens, topk, experts, dropped, only), experts)
+    h, kept = ffn.gated(x, w1, plan=p, save="rows")
+    residual, dh = r(p.rows, hidden).to(t), r(p.rows, inner).to(t)
+    y = ffn.linear(h, w2, bias=bias, activation="silu", residual=residual, plan=p)
+    dx, dw = ffn.gated_backward(dh, x, w1, None, plan=p)
+    f = lambda v: v.double()  # noqa: E731
+    offsets = p.offsets.tolist()
+    for e in range(experts):
+        at = slice(offsets[e], offsets[e + 1])
+        m = at.stop - at.start
+        if not m:
+            assert bool((dw[e] == 0).all())
+            continue
+        xe = f(x)[p.row_slots[at].long() // topk]
+        want, zg = FO.gated(xe, f(w1[e]))
+        bz = (hidden + 16) * H * (xe.abs() @ f(w1[e]).abs().T)
+        (g, u), (bg, bu) = zg.chunk(2, 1), bz.chunk(2, 1)
+        close(kept[at], zg, bz)
+        close(h[at], want, act_error(g, bg, "silu") * (u.abs() + bu) + FO.activation(g, "silu").abs() * bu + 2 * H * want.abs())
+        wy, _, by, _ = linear_bounds(f(h[at]), f(w2[e]), f(bias[e]), "silu", f(residual[at]))
+        close(y[at], wy, by)
+        # dz by way of dw: its rounding and its slopes' error as in the tests above
+        d = f(dh[at]).abs()
+        dz = FO.gated_dz(f(dh[at]), zg)
+        size = torch.cat((d * u.abs(), d * FO.activation(g, "silu").abs()), 1)
+        err = H16[t] * dz.abs() + 512 * H * size + TINY[t] + torch.cat((d * (1.13 * bu + 1.13 * bg * (u.abs() + bu)), d * 1.13 * bg), 1)
+        close(dw[e], dz.T @ xe, (m + 16) * H * ((dz.abs() + err).T @ xe.abs()) + err.T @ xe.abs())
+    end = offsets[-1]
+    assert bool((h[end:] == 0).all()) and bool((kept[end:] == 0).all()) and bool((y[end:] == 0).all())
+
+
 def test_a_plan_of_one_expert_is_dense():
     r = rng(5)
     x, w = r(300, 96).bfloat16(), r(1, 128, 96).bfloat16()
