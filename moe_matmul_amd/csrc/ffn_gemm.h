@@ -166,6 +166,7 @@ struct Product {
   int64_t b_step;          // elements from an expert's B to the next's
   Rows rows;               // over the output's rows, or over k
   int tiles_m, tiles_n;    // dense, or of each expert where the plan is over k
+  int tile_rows;           // dense rows of a tile
   int splits;              // parts of k; more than one: fp32 sums to `partial` [splits][m][n]
   float* partial;
   int64_t partial_step;    // floats of one part
@@ -174,6 +175,7 @@ struct Product {
 
 constexpr int kInside = 0, kOutsideK = 1;
 
+constexpr int64_t kMostTiles = 0x7FFFFF;  // workgroups of 512 threads in a launch: below 2^32 threads
 constexpr int kXcds = 8;         // workgroups go round-robin over them; each has an L2
 constexpr int kRasterWidth = 8;  // columns of tiles walked down together: 32 workgroups of an XCD share 4 + 8 panels
 
@@ -281,11 +283,17 @@ template <int LAYOUT, int BX, int BK, int BLOCKS> struct Reader {
 // Which tile of which expert a workgroup has, and what it reads.
 struct Place {
   int expert, live;   // live 0: rows of no expert
-  int64_t row, rows;  // first output row, and the row after the expert's last
+  int64_t row, rows;  // first output row, and the row after the tile's last
   int col;
   int64_t k_row, k;   // first row of the reduction (plan over k), its length
   int split;
 };
+
+// Rows of a tile where so many are covered by as few tiles of up to BM as can be: the same in all but the last, in blocks of 32.
+__device__ __host__ __forceinline__ uint32_t even_rows(uint32_t rows, uint32_t bm) {
+  const uint32_t tiles = (rows + bm - 1) / bm;
+  return ((rows + tiles - 1) / tiles + 31) / 32 * 32;
+}
 
 // The plan is over the output's rows: the expert and rows of the tile `mt`, counted over all experts. False: no such tile.
 template <int BM> __device__ __forceinline__ bool find_rows(const Rows& p, int64_t mt, int lane, Place& at) {
@@ -304,14 +312,15 @@ template <int BM> __device__ __forceinline__ bool find_rows(const Rows& p, int64
     const uint64_t found = __ballot(before + upto > mt);
     if (found) {
       const int src = __builtin_ctzll(found);
-      const int64_t first = before + __shfl(upto - tiles, src, 64);
-      at.expert = __builtin_amdgcn_readfirstlane(c + src);
+      const int64_t first = before + __builtin_amdgcn_readlane(upto - tiles, src);
+      at.expert = c + src;
       at.live = at.expert < p.experts;
-      at.row = (int64_t)uniform((uint64_t)((int64_t)__shfl((int)lo, src, 64) + (mt - first) * BM));
-      at.rows = __builtin_amdgcn_readfirstlane(__shfl((int)hi, src, 64));
+      const int64_t from = __builtin_amdgcn_readlane((int)lo, src), end = __builtin_amdgcn_readlane((int)hi, src), rows = even_rows((uint32_t)(end - from), BM);
+      at.row = from + (mt - first) * rows;
+      at.rows = min(end, at.row + rows);
       return true;
     }
-    before += __shfl(upto, 63, 64);
+    before += __builtin_amdgcn_readlane(upto, 63);
   }
   return false;
 }
@@ -357,9 +366,10 @@ __global__ __launch_bounds__(64 * WM * WN, PER_SIMD) void product_kernel(const P
     const int64_t wide = (int64_t)p.tiles_m * kRasterWidth;
     const int super = (int)(v / wide), width = min(kRasterWidth, p.tiles_n - super * kRasterWidth);
     v -= super * wide;
-    at.row = (v / width) * BM;
     at.col = (int)(super * kRasterWidth + v % width) * tile_cols;
-    at.rows = p.m;
+    const int64_t rows = p.tile_rows;
+    at.row = (v / width) * rows;
+    at.rows = min(p.m, at.row + rows);
     if (OVER_K) {
       at.k_row = first_row(p.rows, at.expert);
       at.k = first_row(p.rows, at.expert + 1) - at.k_row;
@@ -372,7 +382,7 @@ __global__ __launch_bounds__(64 * WM * WN, PER_SIMD) void product_kernel(const P
     at.split = (int)(v % p.splits);
     v /= p.splits;
     at.col = (int)(v % p.tiles_n) * tile_cols;
-    if (!find_rows<BM>(p.rows, v / p.tiles_n, lane, at)) return;
+    if (!find_rows<BM>(p.rows, (int64_t)uniform((uint64_t)(v / p.tiles_n)), lane, at)) return;
     if (!at.live) at.k = 0;
   }
   const int stages_all = (int)((at.k + BK - 1) / BK);
@@ -410,7 +420,11 @@ __global__ __launch_bounds__(64 * WM * WN, PER_SIMD) void product_kernel(const P
   }
   Reader<AL, BM, BK, MI> ra;
   Reader<BL, BN, BK, NI> rb;
-  ra.set(wm * TM, lane);
+  // the tile's blocks of 32 rows are shared evenly by the rows of waves
+  const int tile_blocks = (int)((at.rows - at.row + 31) / 32), blocks = (tile_blocks + WM - 1) / WM;
+  const int wave_row = wm * blocks * 32;
+  const int64_t wave_end = min(at.rows, at.row + wave_row + blocks * 32);
+  ra.set(wave_row, lane);
   rb.set(wn * TN, lane);
 
   f32x16 acc[MI][NI];
@@ -454,49 +468,50 @@ __global__ __launch_bounds__(64 * WM * WN, PER_SIMD) void product_kernel(const P
     block_sync();
 #pragma unroll
     for (int f = 0; f < NI + MI; ++f) read(0, 0, B_AT, 0, f);
-    // Blocks of 32 rows of this wave that the output has; a tile without some skips their reads and MFMAs (not its
-    // loads and barriers).
-    const int64_t rows_left = at.rows - at.row - wm * TM;
-    const int active = rows_left >= TM ? MI : rows_left > 0 ? (int)(rows_left + 31) / 32 : 0;
-    auto run = [&](auto whole) __attribute__((always_inline)) {
-      constexpr bool WHOLE = decltype(whole)::value;
+    // The wave's blocks of 32 rows that the output has: a loop for each number of them, so that nothing in it depends on
+    // it (all in one with the others skipped takes registers that the largest tile does not have: 203 us where whole
+    // tiles take 141). A wave without rows loads its share and keeps the barriers.
+    auto run = [&](auto of) __attribute__((always_inline)) {
+      constexpr int ACTIVE = decltype(of)::value;
       uint32_t now_a = 0, now_b = B_AT;  // LDS offsets of the stage under way
-    for (int s = 0; s < stages; ++s) {
-      const uint32_t next_a = now_a == (SA - 1) * A::kBytes ? 0 : now_a + A::kBytes;
-      const uint32_t next_b = now_b == B_AT + (SB - 1) * B::kBytes ? B_AT : now_b + B::kBytes;
-      Stage sa = stage_a(s + SA - 1), sb;
-      // a step: for every row block its share of the next step's reads, a load, its MFMAs
-      each<STEPS>([&](auto step) __attribute__((always_inline)) {
-        constexpr int t = decltype(step)::value;
-        if constexpr (t == STEPS - 1) {
-          sb = stage_b(s + SB);
-          wait_loads<(SA - 2) * A::kLoads + (SB - 2) * B::kLoads>();
-          block_sync();
-        }
-        each<MI>([&](auto block) __attribute__((always_inline)) {
-          constexpr int i = decltype(block)::value;
-          if constexpr (t == STEPS - 1) each<B::kLoads>([&](auto u) __attribute__((always_inline)) {
-            if constexpr (decltype(u)::value * MI / B::kLoads == i) load_b(u, sb);
-          });
-          if constexpr (t == 0) each<A::kLoads>([&](auto u) __attribute__((always_inline)) {
-            if constexpr (decltype(u)::value * MI / A::kLoads == i) load_a(u, sa);
-          });
+      for (int s = 0; s < stages; ++s) {
+        const uint32_t next_a = now_a == (SA - 1) * A::kBytes ? 0 : now_a + A::kBytes;
+        const uint32_t next_b = now_b == B_AT + (SB - 1) * B::kBytes ? B_AT : now_b + B::kBytes;
+        Stage sa = stage_a(s + SA - 1), sb;
+        // a step: for every row block its share of the next step's reads, a load, its MFMAs
+        each<STEPS>([&](auto step) __attribute__((always_inline)) {
+          constexpr int t = decltype(step)::value;
+          if constexpr (t == STEPS - 1) {
+            sb = stage_b(s + SB);
+            wait_loads<(SA - 2) * A::kLoads + (SB - 2) * B::kLoads>();
+            block_sync();
+          }
+          each<MI>([&](auto block) __attribute__((always_inline)) {
+            constexpr int i = decltype(block)::value;
+            if constexpr (t == STEPS - 1) each<B::kLoads>([&](auto u) __attribute__((always_inline)) {
+              if constexpr (decltype(u)::value * MI / B::kLoads == i) load_b(u, sb);
+            });
+            if constexpr (t == 0) each<A::kLoads>([&](auto u) __attribute__((always_inline)) {
+              if constexpr (decltype(u)::value * MI / A::kLoads == i) load_a(u, sa);
+            });
 #pragma unroll
-          for (int f = i * (NI + MI) / MI; f < (i + 1) * (NI + MI) / MI; ++f)
-            if (WHOLE || (f < NI ? 0 : f - NI) < active)
-              read((t + 1) & 1, t == STEPS - 1 ? next_a : now_a, t == STEPS - 1 ? next_b : now_b, (t + 1) % STEPS, f);
-          if (WHOLE || i < active)
+            for (int f = i * (NI + MI) / MI; f < (i + 1) * (NI + MI) / MI; ++f)
+              if ((f < NI ? 0 : f - NI) < ACTIVE)
+                read((t + 1) & 1, t == STEPS - 1 ? next_a : now_a, t == STEPS - 1 ? next_b : now_b, (t + 1) % STEPS, f);
+            if (i < ACTIVE)
 #pragma unroll
-          for (int j = 0; j < NI; ++j) acc[i][j] = mfma32<T>(fb[t & 1][j], fa[t & 1][i], acc[i][j]);
-          __builtin_amdgcn_sched_barrier(0);
+              for (int j = 0; j < NI; ++j) acc[i][j] = mfma32<T>(fb[t & 1][j], fa[t & 1][i], acc[i][j]);
+            __builtin_amdgcn_sched_barrier(0);
+          });
         });
-      });
-      now_a = next_a;
-      now_b = next_b;
-    }
+        now_a = next_a;
+        now_b = next_b;
+      }
     };
-    if (at.rows - at.row >= BM) run(std::true_type{});
-    else run(std::false_type{});
+    const int active = at.row + wave_row < wave_end ? blocks : 0;
+    each<MI + 1>([&](auto of) __attribute__((always_inline)) {
+      if (active == decltype(of)::value) run(of);
+    });
     // nothing more is written to the stages, nor read from them
     wait_loads<0>();
     block_sync();
@@ -512,7 +527,7 @@ __global__ __launch_bounds__(64 * WM * WN, PER_SIMD) void product_kernel(const P
   float* room = (float*)lds + wave * 32 * ROOM;
   const int my_row = lane / LANES, my_col = lane % LANES * 8;
   const int col = at.col + wn * (GATED ? C / 2 : C) + my_col;
-  const int64_t row0 = at.row + wm * TM + my_row;
+  const int64_t row0 = at.row + wave_row + my_row;
   const bool in_cols = col < (GATED ? p.ep.inner : p.n), parts = p.splits > 1;
   const int64_t out0 = OVER_K ? at.expert * p.m : 0;  // output row of the tile's row 0
   float* partial = parts ? p.partial + at.split * p.partial_step + out0 * p.n : nullptr;
@@ -522,7 +537,7 @@ __global__ __launch_bounds__(64 * WM * WN, PER_SIMD) void product_kernel(const P
   if (has_bias && in_cols) param8<T>(p.ep.bias, (int64_t)at.expert * p.n + col, p.ep.bias_f32, true, bias);
   // the residual of a pass; out of range: 0
   auto residual_at = [&](int64_t row) __attribute__((always_inline)) {
-    return row < at.rows && in_cols ? *(const u32x4*)((const uint16_t*)p.ep.residual + row * p.ep.ldr + col) : u32x4{0, 0, 0, 0};
+    return row < wave_end && in_cols ? *(const u32x4*)((const uint16_t*)p.ep.residual + row * p.ep.ldr + col) : u32x4{0, 0, 0, 0};
   };
   constexpr bool GRADIENT = BL == kOutsideK;  // no bias, activation or residual
   const bool plain = !GATED && !parts && !p.ep.y_f32 && (GRADIENT || (p.ep.act == NVFP4_FFN_NONE && !p.ep.z));
@@ -533,6 +548,7 @@ __global__ __launch_bounds__(64 * WM * WN, PER_SIMD) void product_kernel(const P
   }
   each<MI>([&](auto block) __attribute__((always_inline)) {
     constexpr int i = decltype(block)::value;
+    if (at.row + wave_row + i * 32 >= wave_end) return;
     // a wave's LDS operations keep their order; the fence keeps the compiler to it
     wave_sync();
 #pragma unroll
@@ -569,7 +585,7 @@ __global__ __launch_bounds__(64 * WM * WN, PER_SIMD) void product_kernel(const P
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] += r[j];
           }
-          if (row < at.rows && in_cols) *(u32x4*)((uint16_t*)p.ep.y + (out0 + row) * p.ep.ldy + col) = pack16x8<T>(v);
+          if (row < wave_end && in_cols) *(u32x4*)((uint16_t*)p.ep.y + (out0 + row) * p.ep.ldy + col) = pack16x8<T>(v);
         }
         return;
       }
@@ -581,7 +597,7 @@ __global__ __launch_bounds__(64 * WM * WN, PER_SIMD) void product_kernel(const P
         if (has_residual && q + 1 < PASSES) next = residual_at(row + PASS);
         float v[8], r[8];
         load8<F32>(from, q * PASS * ROOM, true, v);
-        if (row >= at.rows || !in_cols) continue;
+        if (row >= wave_end || !in_cols) continue;
         if (parts) {
           store8<F32>(partial, row * p.n + col, true, v);
           continue;
@@ -598,7 +614,7 @@ __global__ __launch_bounds__(64 * WM * WN, PER_SIMD) void product_kernel(const P
 #pragma unroll 1
       for (int q = 0; q < PASSES; ++q) {
         const int64_t row = first_of + q * PASS;
-        const bool in = row < at.rows && in_cols;
+        const bool in = row < wave_end && in_cols;
         const u32x4 dh = next;
         if (has_residual && q + 1 < PASSES) next = residual_at(row + PASS);
         float g[8], u[8];
@@ -624,18 +640,19 @@ __global__ __launch_bounds__(64 * WM * WN, PER_SIMD) void product_kernel(const P
 
 // ---- host: sizes of tiles, parts of k ----------------------------------------------
 struct Tiling {
-  int shape;   // 0: 128 x 128, 1: 256 x 128, 2: 256 x 256, 3: 64 x 128 (rows with k inside)
+  int shape;   // 0: 128 x 128, 1: 256 x 128, 2: 256 x 256; of rows with k inside also 3: 64 x 128, 4: 320 x 128, 5: 320 x 256
   int splits;
 };
-constexpr int64_t kMostTiles = 0x7FFFFF;  // workgroups of 512 threads in a launch: below 2^32 threads
-inline int tile_rows(int shape) { return shape == 3 ? 64 : shape ? 256 : 128; }
-inline int tile_cols(int shape) { return shape == 2 ? 256 : 128; }
+constexpr int kShapes = 6, kShapesOverK = 3;
+inline int tile_rows(int shape) { return shape >= 4 ? 320 : shape == 3 ? 64 : shape ? 256 : 128; }
+inline int tile_cols(int shape) { return shape == 2 || shape == 5 ? 256 : 128; }
 
 template <class T, int AL, int BL, bool GATED> inline int launch_product(Product& p, const Tiling& t, hipStream_t stream) {
   constexpr bool OVER_K = AL == kOutsideK;
   const int bm = tile_rows(t.shape), cols = tile_cols(t.shape) / (GATED ? 2 : 1);
   p.splits = t.splits;
   p.tiles_m = (int)ceil_div64(p.m, bm);
+  p.tile_rows = (int)even_rows((uint32_t)p.m, bm);
   p.tiles_n = ceil_div(GATED ? p.ep.inner : p.n, cols);
   int64_t tiles;
   if (OVER_K) {
@@ -652,7 +669,11 @@ template <class T, int AL, int BL, bool GATED> inline int launch_product(Product
   if (t.shape == 2) product_kernel<T, AL, BL, GATED, 256, 256, 2, 4, 64, 3, 2, 2><<<grid, 512, 0, stream>>>(p);
   else if (t.shape == 1) product_kernel<T, AL, BL, GATED, 256, 128, 4, 2, 64, 3, 3, 2><<<grid, 512, 0, stream>>>(p);
   else if (t.shape == 0) product_kernel<T, AL, BL, GATED, 128, 128, 2, 2, 64, 2, 2, 2><<<grid, 256, 0, stream>>>(p);
-  else if constexpr (AL == kInside) product_kernel<T, AL, BL, GATED, 64, 128, 2, 2, 64, 3, 3, 2><<<grid, 256, 0, stream>>>(p);
+  else if constexpr (AL == kInside) {
+    if (t.shape == 3) product_kernel<T, AL, BL, GATED, 64, 128, 2, 2, 64, 3, 3, 2><<<grid, 256, 0, stream>>>(p);
+    else if (t.shape == 4) product_kernel<T, AL, BL, GATED, 320, 128, 2, 2, 64, 3, 2, 1><<<grid, 256, 0, stream>>>(p);
+    else product_kernel<T, AL, BL, GATED, 320, 256, 2, 4, 64, 2, 2, 2><<<grid, 512, 0, stream>>>(p);
+  }
   return launched();
 }
 

@@ -47,42 +47,51 @@ int plan_rows(const nvfp4_ffn_plan* plan, int64_t rows, bool gathered, Rows* out
 }
 
 // The tiles and parts of k that take least by a model of the kernels' times in microseconds: a round of tiles over the
-// compute units (two small ones to a unit) has a fixed part and one for every 64 k, measured on products that
-// fill whole rounds (4096 x 4096 x 2048 and 8192: 59 and 214, 64 and 241, 66 and 259 for 256 x 256, 256 x 128 and
-// 128 x 128; 64 x 4096 x 7168 in 4 and 8 parts of 64 x 128: 14 and 12); a last row of tiles that is mostly empty costs about two fifths of a whole one; parts are written and
-// read at some 4 TB/s, in a launch of their own.
+// compute units (two small ones to a unit) has a fixed part and one for every 64 k, fitted to products that fill whole
+// rounds (4096 x 4096 x 2048 and 8192: 256 x 256 59 and 205, 256 x 128 64 and 241, 128 x 128 66 and 259; 5120 x 4096 and
+// 2048 columns: 320 x 256 73 and 278, 320 x 128 43 and 142; 64 x 4096 x 7168 in 4 and 8 parts of 64 x 128: 14 and 12).
+// The tallest tiles are for rows that leave a part of a round in all others: 5120 x 4096 x 2048 89 at best without
+// them, 73 with; by experts, two tiles of 320 hold the 512 rows that they have on the average and the some more that
+// half of them have (eight of 2048 x 4096, 3900 rows: gradient of rows 97 without them, 76 with). A tile that is not
+// filled takes kEmpty of its time for its loads. Parts are written and read at some 4 TB/s, in a launch of their own.
 static Tiling choose_tiling(int64_t rows, int cols, int64_t k, int experts, bool over_k, int units, double* time) {
-  static const double kFixed[4] = {7, 8, 9, 4}, kStage[4] = {0.97, 0.92, 1.6, 0.7}, kAlone[4] = {0.62, 0.92, 1.6, 0.4};
+  static const double kFixed[kShapes] = {7, 8, 9, 4, 10, 11}, kStage[kShapes] = {0.97, 0.92, 1.6, 0.7, 1.03, 2.0}, kAlone[kShapes] = {0.64, 1, 1, 0.57, 1, 1}, kEmpty = 0.4;
   const double e = over_k ? experts : 1;
   const double stages = (double)ceil_div64(k > 0 ? k : 1, 64);
   Tiling best{0, 1};
   double least = 1e30;
   // the weights' (or rows') own bytes
   const double streamed = 5 + (double)cols * k * 2 * (over_k ? e : experts < rows ? experts : rows) / 5e6;
-  for (int shape = 0; shape < (over_k ? 3 : 4); ++shape) {
+  for (int shape = 0; shape < (over_k ? kShapesOverK : kShapes); ++shape) {
     const int bm = tile_rows(shape), bn = tile_cols(shape);
-    const double tail = (double)(rows % bm) / bm;
-    double high = rows / bm + (tail > 0 ? (tail > 0.4 ? tail : 0.4) : 0);
+    // rows of tiles, and how much of their height is used
+    double high, fill;
     if (!over_k && experts > 1) {
-      // every expert has a last row of tiles, half full
-      const double some = (double)(experts < rows ? experts : rows);
-      high = (double)rows / bm + 0.4 * some;
-      if (high < some) high = some;
+      // experts have about as many rows (half of them more: what a standard deviation more needs)
+      const double some = (double)(experts < rows ? experts : rows), each = rows / some, of_each = ceil((each + sqrt(each)) / bm);
+      high = of_each * some;
+      fill = ceil(each / of_each / 32) * 32 / bm;
+    } else {
+      const double all = ceil((double)rows / bm), even = even_rows((uint32_t)rows, bm), last = (rows - (all - 1) * even) / even;
+      high = all - 1 + (last > 0.4 ? last : 0.4);
+      fill = even / bm;
     }
+    const double stage = kStage[shape] * (kEmpty + (1 - kEmpty) * (fill < 1 ? fill : 1));
+    const double latency = !over_k && experts > 1 ? 0.5 : 0;  // of a stage of weights that no other tile has read
     const double tiles = high * ceil_div(cols, bn) * e;
     // (of more than the largest tiles can cover, launch_product tells)
     if (shape != 2 && ((double)rows / bm + experts + 1) * ceil_div(cols, bn) * e + 8 * kXcds > kMostTiles) continue;
     for (int splits = 1; splits <= 16; splits += splits < 4 ? 1 : splits < 8 ? 2 : 4) {
       if (splits > 1 && stages / splits < 4) break;
-      const double all = tiles * splits, room = shape == 1 || shape == 2 ? units : 2.0 * units;
+      const double all = tiles * splits, room = shape != 0 && shape != 3 ? units : 2.0 * units;
       const double whole = floor(all / room), rest = all - whole * room;
       const double part = stages / splits;
-      double t = whole * (kFixed[shape] + part * kStage[shape]);
+      double t = whole * (kFixed[shape] + part * fmax(stage, latency));
       // (units that are alone on the memory and the power are faster: 136 tiles of 256 x 256 1.3 a stage)
       if (rest > 0.01)
-        t += kFixed[shape] + part * (rest > units ? kStage[shape] : kAlone[shape] * (room > units ? 1 : 0.66 + 0.34 * rest / units));
-      if (t < streamed) t = streamed;
-      if (splits > 1) t += 4 + (double)rows * cols * e * 4 * 2 * splits / 4e6;
+        t += kFixed[shape] + part * fmax(latency, stage * (rest > units ? 1 : kAlone[shape] * (room > units ? 1 : 0.66 + 0.34 * rest / units)));
+      t = t < streamed ? streamed + 0.05 * t : 1.05 * t;  // (where the weights' bytes bound all, the least work)
+      if (splits > 1) t += 5 + splits + (double)rows * cols * e * 4 * 2 * splits / 4e6;
       if (t < least) {
         least = t;
         best = Tiling{shape, splits};

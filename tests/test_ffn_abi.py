@@ -251,7 +251,7 @@ def test_gpu_cases_reach_every_kernel():
     shapes = {(128, 128), (256, 128), (256, 256)}
     want = {(*s, False) for s in shapes} | {(128, 128, True)}
     for kind in PRODUCT_KINDS:
-        rows64 = {(64, 128, False), (64, 128, True)} if kind != c.NVFP4_FFN_DW else set()
+        rows64 = {(64, 128, False), (64, 128, True), (320, 128, False), (320, 256, False)} if kind != c.NVFP4_FFN_DW else set()
         few = {(0, 0, False)} if kind == c.NVFP4_FFN_FORWARD else set()
         missing = (want | rows64 | few) - seen[kind]
         assert not missing, (kind, missing)

@@ -493,6 +493,35 @@ def test_few_rows_of_many_experts(i, dtype):
     assert bool((h[end:] == 0).all()) and bool((kept[end:] == 0).all()) and bool((y[end:] == 0).all())
 
 
+@pytest.mark.parametrize("counts,n,k,tiles", [
+    ([320, 321, 0, 640, 641, 1, 1989], 2048, 264, [320, 128]), ([320, 321, 0, 640, 641, 1, 33], 6144, 64, [320, 256]),
+    ([64, 65, 0, 128, 129, 1, 33], 272, 64, [64, 128]), ([256, 257, 512, 513, 31, 2335], 2048, 64, [256, 256])])
+def test_an_experts_tiles_share_its_rows(counts, n, k, tiles):
+    """Rows of experts at the tiles' heights and beside them."""
+    r, rows = rng(tuple(counts), n, k), sum(counts)
+    assert c.nvfp4_ffn_product_parts(c.NVFP4_FFN_FORWARD, rows, n, k, len(counts))[0][1:3] == tuple(tiles)
+    ids = torch.repeat_interleave(torch.arange(len(counts)), torch.tensor(counts))[torch.randperm(rows)]
+    p = moe.plan(ids.to("cuda", torch.int32).view(-1, 1), len(counts))
+    x, w = r(rows, k).bfloat16(), (r(len(counts), n, k) * k ** -0.5).bfloat16()
+    residual, dy = r(rows, n).bfloat16(), r(rows, n).bfloat16()
+    y = ffn.linear(x, w, residual=residual, plan=p)
+    h = ffn.gated(x, w, plan=p)
+    dx, dw, _ = ffn.linear_backward(dy, x, w, plan=p)
+    f = lambda v: v.double()  # noqa: E731
+    offsets = p.offsets.tolist()
+    assert [b - a for a, b in zip(offsets, offsets[1:])] == counts
+    for e in range(len(counts)):
+        at = slice(offsets[e], offsets[e + 1])
+        want, _, by, _ = linear_bounds(f(x[at]), f(w[e]), None, None, f(residual[at]))
+        close(y[at], want, by)
+        xs = f(x)[p.row_slots[at].long()]
+        want, z = FO.gated(xs, f(w[e]))
+        (g, u), (bg, bu) = z.chunk(2, 1), ((k + 16) * H * (xs.abs() @ f(w[e]).abs().T)).chunk(2, 1)
+        close(h[at], want, act_error(g, bg, "silu") * (u.abs() + bu) + FO.activation(g, "silu").abs() * bu + 2 * H * want.abs())
+        close(dx[at], f(dy[at]) @ f(w[e]), (n + 16) * H * (f(dy[at]).abs() @ f(w[e]).abs()))
+        close(dw[e], f(dy[at]).T @ f(x[at]), (counts[e] + 16) * H * (f(dy[at]).abs().T @ f(x[at]).abs()))
+
+
 def test_a_plan_of_one_expert_is_dense():
     r = rng(5)
     x, w = r(300, 96).bfloat16(), r(1, 128, 96).bfloat16()
