@@ -4,7 +4,8 @@ The computation runs in the hand-written HIP library
 (``libnvfp4_grouped_gemm.so``, C ABI in ``include/nvfp4_grouped_gemm.h``);
 this package is its thin Python binding plus device-memory plumbing. The
 operators around it (``libnvfp4_moe.so``, C ABI in ``include/nvfp4_moe.h``) are in
-``moe_matmul_amd.moe``.
+``moe_matmul_amd.moe``, the feed-forward block in 16 bits and its training
+(``libnvfp4_ffn.so``, C ABI in ``include/nvfp4_ffn.h``) in ``moe_matmul_amd.ffn``.
 """
 from ._binding import (  # noqa: F401
     LIB_PATH, NVFP4_ERR_CONFIG, NVFP4_ERR_HIP, NVFP4_ERR_INVALID, NVFP4_ERR_MISALIGNED, NVFP4_ERR_WORKSPACE,

@@ -9,10 +9,12 @@ around it (``csrc/moe_*.hip``, ``csrc/nvfp4_quantize.hip``) into
 """
 from __future__ import annotations
 
+import concurrent.futures
 import os
 import shutil
 import subprocess
 import sys
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -34,7 +36,7 @@ PROBE_LIB = os.path.join(HERE, "libnvfp4_mainloop_probe.so")
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [
-    f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-shared",
+    f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
     # no packed-fp32 instructions: hipcc otherwise forms v_pk_*_f32 from float code
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     f"-I{INCLUDE}",
@@ -51,10 +53,10 @@ def hipcc() -> str:
 def build(verbose: bool = False) -> str:
     """Compile the library, the operators' libraries and the probe library (always,
     even if built copies exist); return the library's path."""
-    _compile(SOURCES, LIB, verbose)
-    build_moe(verbose)
-    build_ffn(verbose)
-    _compile(PROBE_SOURCES, PROBE_LIB, verbose)
+    libraries = ((SOURCES, LIB), (FFN_SOURCES, FFN_LIB), (MOE_SOURCES, MOE_LIB), (PROBE_SOURCES, PROBE_LIB))
+    with concurrent.futures.ThreadPoolExecutor(len(libraries)) as pool:
+        for done in [pool.submit(_compile, sources, lib, verbose) for sources, lib in libraries]:
+            done.result()
     return LIB
 
 
@@ -70,9 +72,8 @@ def build_ffn(verbose: bool = False) -> str:
     return FFN_LIB
 
 
-def _compile(sources, lib, verbose):
-    tmp = lib + ".tmp"
-    cmd = [hipcc(), *HIPCC_FLAGS, *sources, "-o", tmp]
+def _run(args, verbose):
+    cmd = [hipcc(), *HIPCC_FLAGS, *args]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
@@ -82,6 +83,17 @@ def _compile(sources, lib, verbose):
         out = "\n".join(l for l in (res.stdout + res.stderr).splitlines() if noise not in l)
         if out.strip():
             print(out)
+
+
+def _compile(sources, lib, verbose):
+    """The sources into objects, several at a time, and those into the library."""
+    tmp = lib + ".tmp"
+    with tempfile.TemporaryDirectory(prefix=os.path.basename(lib) + ".", dir=HERE) as room:
+        objects = [os.path.join(room, os.path.basename(s) + ".o") for s in sources]
+        with concurrent.futures.ThreadPoolExecutor(len(sources)) as pool:
+            for done in [pool.submit(_run, ["-c", s, "-o", o], verbose) for s, o in zip(sources, objects)]:
+                done.result()
+        _run(["-shared", *objects, "-o", tmp], verbose)
     os.replace(tmp, lib)
 
 

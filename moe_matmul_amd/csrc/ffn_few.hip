@@ -11,7 +11,8 @@
 // weights are under way while the other adds up: U = 4, the registers allow no more (1 row, 28672 x 4096: 44 us, 5.3
 // TB/s; U = 16 54. 32 experts of 4096 x 7168: 208 and 311). Where k is short, all sixteen waves would have little to do
 // for a few columns: fewer share k, and the workgroup has more columns (256 experts of 2048 x 512, 1024 rows: 98 us, 308
-// with 16 columns to a workgroup).
+// with 16 columns to a workgroup). Under a kernel trace: 1 x 7168 x 2048 8.5 us, gated 1 x 2 x 2048 x 7168 12.5 (58.7 MB:
+// 4.7 TB/s; a launch that does nothing takes 3).
 #include "ffn_gemm.h"
 
 namespace ffn {

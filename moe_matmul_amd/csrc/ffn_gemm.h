@@ -3,13 +3,16 @@
 // ("k inside": rows and weights of a forward product) or with adjacent m or n ("k
 // outside": weights of a gradient of rows, both operands of a gradient of weights).
 //
-// A workgroup of four waves computes a tile of BM x BN, each wave a quarter (2 x 2)
-// by v_mfma_f32_32x32x16. Operands go from memory to LDS by direct buffer loads in
-// stages of BK, NS stages deep; an operand with k outside keeps its layout in LDS and
-// is transposed by ds_read_b64_tr_b16 on the way to registers. One barrier a stage,
-// before its last step of 16 k: the fragments of a step are read during the MFMAs of
-// the one before, the loads of a stage are issued half in the last step of the stage
-// whose buffer they take, half in the step after.
+// A workgroup computes a tile of BM x BN by v_mfma_f32_32x32x16, its waves WM x WN parts of it. Operands go from memory to
+// LDS by direct buffer loads in stages of BK, SA and SB stages deep; an operand with k outside keeps its layout in LDS and
+// is transposed by ds_read_b64_tr_b16 on the way to registers. One barrier a stage, before its last step of 16 k: the
+// fragments of a step are read during the MFMAs of the one before; B's next loads are issued in the last step of the stage
+// whose buffer they take, A's in the step after, so that neither waits in one queue behind the other.
+//
+// What bounds it: the card's power in large products (8192 x 4096 x 7168: 1.28 to 1.37 PFLOP/s at 1.5 to 1.6 GHz, matrix
+// units busy 78% of the cycles; a large library product 1.42). LDS is next: 256 x 256 with waves of 128 x 64 reads 384
+// cycles and writes 128 of the 512 that the MFMAs of a step take. Hence that tile, A's stages one deeper than B's (3 and 2
+// fill the 160 KB). In products of few tiles the rounds of tiles bound, hence the other shapes: see launch_product.
 #pragma once
 
 #include <type_traits>
@@ -647,6 +650,14 @@ constexpr int kShapes = 6, kShapesOverK = 3;
 inline int tile_rows(int shape) { return shape >= 4 ? 320 : shape == 3 ? 64 : shape ? 256 : 128; }
 inline int tile_cols(int shape) { return shape == 2 || shape == 5 ? 256 : 128; }
 
+// Tile, waves, stages: time in us of a product that it fits, bf16, forward.
+//   256 x 256, 8, 3 + 2: 4096 x 4096 x 4096 106 (1.29 PFLOP/s)
+//   320 x 256, 8, 2 + 2: 5120 x 4096 x 2048 73 (1.18; 256 x 256 takes two rounds, 98)
+//   320 x 128, 4, 3 + 2: 5120 x 2048 x 2048 43 (1.01; 256 x 256 44, 128 x 128 57), 2051 x 4104 x 2048 41 (46, 58)
+//   256 x 128, 8, 3 + 3: 1500 x 1536 x 6144, in parts, 42 (128 x 128 43)
+//   128 x 128, 4, 2 + 2, two to a unit: 1000 x 4096 x 2048 27 (256 x 128 29)
+//    64 x 128, 4, 3 + 3, two to a unit: 128 x 4096 x 4096, in parts, 19 (128 x 128 21); experts of few rows
+// Four waves of 128 x 128 in place of eight of 128 x 64 take the same time in 256 x 256.
 template <class T, int AL, int BL, bool GATED> inline int launch_product(Product& p, const Tiling& t, hipStream_t stream) {
   constexpr bool OVER_K = AL == kOutsideK;
   const int bm = tile_rows(t.shape), cols = tile_cols(t.shape) / (GATED ? 2 : 1);

@@ -1,6 +1,8 @@
 // Operators on rows around the products of nvfp4_ffn.h: rows to 8 bits and back,
 // tokens' rows at their slots' rows, gradients of activations with their column sums.
-// All bound by memory: a thread takes eight adjacent elements.
+// All bound by memory: a thread takes eight adjacent elements. Measured, bf16: 16390 x 2048 to 8 bits 17.9 us and back
+// 16.5 (102 MB each: 5.7 and 6.2 TB/s); gather to 3900 rows of 4096 10.8; gated_dz of 4099 x 2 x 2048 from 8 bits 14.4
+// (68 MB); linear_dz of 2051 x 4104 with silu and column sums 15.6 and 4.6 (51 MB: a floor of 10).
 #include "ffn_common.h"
 
 namespace ffn {
