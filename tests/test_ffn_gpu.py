@@ -791,6 +791,66 @@ def test_steps_on_two_streams_at_once(experts):
             same(g[k], w[k])
 
 
+def apart(t, gap=24):
+    """The same rows, further apart, in memory of NaN."""
+    room = torch.full((t.shape[0], t.shape[1] + gap), math.nan, device="cuda", dtype=t.dtype)
+    room[:, :t.shape[1]] = t
+    return room[:, :t.shape[1]]
+
+
+@pytest.mark.parametrize("tokens,hidden,inner", [(3, 64, 32), (70, 256, 160), (600, 512, 288)])
+@pytest.mark.parametrize("experts", [0, 3])
+def test_less_usual_forms_are_the_usual_ones(tokens, hidden, inner, experts):
+    """Operands whose rows lie apart, rows in 8 bits in place of 16, gradients without what was kept, one tensor in two
+    places: bit for bit as the usual call on the same values."""
+    r = rng(tokens, hidden, inner, experts)
+    lead = (experts,) if experts else ()
+    p = moe.plan(pick(r, tokens, 2, experts, 0.2), experts) if experts else None
+    rows = p.rows if experts else tokens
+    x, w1 = r(tokens, hidden).bfloat16(), (r(*lead, 2 * inner, hidden) * hidden ** -0.5).bfloat16()
+    w2, bias = (r(*lead, hidden, inner) * inner ** -0.5).bfloat16(), r(*lead, hidden).bfloat16()
+    dh, dy, residual = r(rows, inner).bfloat16(), r(rows, hidden).bfloat16(), r(rows, hidden).bfloat16()
+    q = ffn.quantize8(x)
+    x = ffn.dequantize8(q)
+    h, kept = ffn.gated(x, w1, plan=p, save="rows")
+    for a, b in zip(ffn.gated(apart(x), w1, plan=p, save="rows"), (h, kept)):
+        same(a, b)
+    for k in (kept, None, ffn.gated(x, w1, plan=p, save="rows8")[1]):
+        want = ffn.gated_backward(dh, x, w1, k, plan=p)
+        for form in ((dh, q), (apart(dh), apart(x)), (apart(dh, 8), q)):
+            for a, b in zip(ffn.gated_backward(*form, w1, k, plan=p), want):
+                same(a, b)
+    how = dict(bias=bias, activation="gelu", plan=p)
+    y, z = ffn.linear(h, w2, residual=residual, save=True, **how)
+    for a, b in zip(ffn.linear(apart(h), w2, residual=apart(residual, 8), save=True, **how), (y, z)):
+        same(a, b)
+    want = ffn.linear_backward(dy, h, w2, z=z, **how)
+    for a, b in zip(ffn.linear_backward(apart(dy), apart(h), w2, z=z, **how), want):
+        same(a, b)
+    h8 = ffn.quantize8(h)
+    for a, b in zip(ffn.linear_backward(dy, h8, w2, z=z, **how), ffn.linear_backward(dy, ffn.dequantize8(h8), w2, z=z, **how)):
+        same(a, b)
+    # without an activation dy takes the place of dz, and lies apart itself
+    for a, b in zip(ffn.linear_backward(apart(dy), h, w2, bias=bias, plan=p), ffn.linear_backward(dy, h, w2, bias=bias, plan=p)):
+        same(a, b)
+    weight = r(hidden)
+    n = ffn.rmsnorm(x, weight, residual=x, rows8=True)
+    same(n.sum, (x.float() * 2).bfloat16())
+    m = ffn.rmsnorm(apart(x), weight, residual=apart(x, 8), rows=False, rows8=True)
+    same(m.y8.codes, n.y8.codes)
+    same(m.y8.scales, n.y8.scales)
+    same(m.sum, n.sum)
+    assert m.y is None
+    dn = r(tokens, hidden).bfloat16()
+    want = ffn.rmsnorm_backward(dn, n.sum, weight, n.rstd, dsum=dn)
+    for a, b in zip(ffn.rmsnorm_backward(apart(dn), apart(n.sum, 8), weight, n.rstd, dsum=apart(dn, 16)), want):
+        same(a, b)
+    same(ffn.rmsnorm_backward(dn, n.sum, None, n.rstd)[0], ffn.rmsnorm_backward(dn, n.sum, torch.ones_like(weight), n.rstd)[0])
+    room = torch.full((tokens, hidden + 8), 7.0, device="cuda")
+    ffn.dequantize8(q, out=room[:, :hidden])
+    assert bool((room[:, hidden:] == 7).all()) and torch.equal(room[:, :hidden].bfloat16(), x)
+
+
 def test_the_stream_argument():
     r = rng(4)
     x, w = r(300, 256).bfloat16(), r(512, 256).bfloat16()
