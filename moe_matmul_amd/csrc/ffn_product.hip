@@ -53,9 +53,12 @@ int plan_rows(const nvfp4_ffn_plan* plan, int64_t rows, bool gathered, Rows* out
 // The tallest tiles are for rows that leave a part of a round in all others: 5120 x 4096 x 2048 89 at best without
 // them, 73 with; by experts, two tiles of 320 hold the 512 rows that they have on the average and the some more that
 // half of them have (eight of 2048 x 4096, 3900 rows: gradient of rows 97 without them, 76 with). A tile that is not
-// filled takes kEmpty of its time for its loads. Parts are written and read at some 4 TB/s, in a launch of their own.
+// filled takes kEmpty of its time for its loads. Parts are written and read at some 4 TB/s, in a launch of their own;
+// by experts they cost more, as rows that are not there have parts too. Against the best tile that there is the choice
+// loses up to a tenth, in small products a fifth.
 static Tiling choose_tiling(int64_t rows, int cols, int64_t k, int experts, bool over_k, int units, double* time) {
-  static const double kFixed[kShapes] = {7, 8, 9, 4, 10, 11}, kStage[kShapes] = {0.97, 0.92, 1.6, 0.7, 1.03, 2.0}, kAlone[kShapes] = {0.64, 1, 1, 0.57, 1, 1}, kEmpty = 0.4;
+  static const double kFixed[kShapes] = {7, 8, 9, 4, 10, 10}, kStage[kShapes] = {0.97, 0.92, 1.6, 0.7, 1.03, 2.2};
+  static const double kAlone[kShapes] = {0.64, 1, 1, 0.57, 1, 1}, kEmpty = 0.4;
   const double e = over_k ? experts : 1;
   const double stages = (double)ceil_div64(k > 0 ? k : 1, 64);
   Tiling best{0, 1};
@@ -77,7 +80,7 @@ static Tiling choose_tiling(int64_t rows, int cols, int64_t k, int experts, bool
       fill = even / bm;
     }
     const double stage = kStage[shape] * (kEmpty + (1 - kEmpty) * (fill < 1 ? fill : 1));
-    const double latency = !over_k && experts > 1 ? 0.5 : 0;  // of a stage of weights that no other tile has read
+    const double latency = !over_k && experts > 1 ? 0.5 : 0;  // a stage of weights that no other tile has read: from memory
     const double tiles = high * ceil_div(cols, bn) * e;
     // (of more than the largest tiles can cover, launch_product tells)
     if (shape != 2 && ((double)rows / bm + experts + 1) * ceil_div(cols, bn) * e + 8 * kXcds > kMostTiles) continue;
@@ -87,11 +90,15 @@ static Tiling choose_tiling(int64_t rows, int cols, int64_t k, int experts, bool
       const double whole = floor(all / room), rest = all - whole * room;
       const double part = stages / splits;
       double t = whole * (kFixed[shape] + part * fmax(stage, latency));
-      // (units that are alone on the memory and the power are faster: 136 tiles of 256 x 256 1.3 a stage)
-      if (rest > 0.01)
-        t += kFixed[shape] + part * fmax(latency, stage * (rest > units ? 1 : kAlone[shape] * (room > units ? 1 : 0.66 + 0.34 * rest / units)));
+      if (rest > 0.01) {
+        // units that are alone on the memory and the power are faster: a stage of 160 tiles of 256 x 256 takes 1.07; two
+        // small tiles of a unit share it until there are fewer than units
+        const double r = rest / units;
+        const double alone = r > 1 ? 1 : kAlone[shape] * (room > units ? 1 : bn == 128 ? 0.66 + 0.34 * r : r > 0.5 ? 0.2 + 0.8 * r : 0.6);
+        t += kFixed[shape] + part * fmax(latency, stage * alone);
+      }
       t = t < streamed ? streamed + 0.05 * t : 1.05 * t;  // (where the weights' bytes bound all, the least work)
-      if (splits > 1) t += 5 + splits + (double)rows * cols * e * 4 * 2 * splits / 4e6;
+      if (splits > 1) t += (experts > 1 ? 5 + splits : 4 + 0.5 * splits) + (double)rows * cols * e * 4 * 2 * splits / 4e6;
       if (t < least) {
         least = t;
         best = Tiling{shape, splits};

@@ -169,18 +169,18 @@ def rmsnorm(x, weight=None, *, residual=None, eps=1e-6, rows=True, rows8=False, 
     """``s = x + residual`` (rounded to x's type), ``y = s / sqrt(mean(s^2) + eps) * weight`` of rows x [rows, n] (fp32,
     fp16 or bf16). ``weight`` [n]: fp32 or x's type, None for 1. ``rows``: y in x's type; ``rows8``: in 8 bits."""
     device = _gpu(x, "x")
-    kind, stride = _type(x, "x"), _rows(x, "x")
+    kind, stride, shape = _type(x, "x"), _rows(x, "x"), x.shape
     if not rows and not rows8:
         raise ValueError("rows or rows8 must be asked for")
-    f32 = 0 if weight is None else _param(weight, "weight", (x.shape[1],), x)
+    f32 = 0 if weight is None else _param(weight, "weight", shape[1:], x)
     total, residual_stride = x, 0
     if residual is not None:
-        residual_stride = _same(residual, "residual", x.shape, x)
-        total = _out(None, "sum", x.shape, x.dtype, device)
-    y = _out(None, "y", x.shape, x.dtype, device) if rows else None
-    y8 = _out8(None, "y8", x.shape, device) if rows8 else None
-    rstd = torch.empty(x.shape[0], dtype=torch.float32, device=device)
-    _enqueue(c.nvfp4_ffn_rmsnorm, device, x.data_ptr(), kind, *x.shape, stride, _at(residual), residual_stride,
+        residual_stride = _same(residual, "residual", shape, x)
+        total = _out(None, "sum", shape, x.dtype, device)
+    y = _out(None, "y", shape, x.dtype, device) if rows else None
+    y8 = _out8(None, "y8", shape, device) if rows8 else None
+    rstd = torch.empty_strided(shape[:1], (1,), dtype=torch.float32, device=device)
+    _enqueue(c.nvfp4_ffn_rmsnorm, device, x.data_ptr(), kind, *shape, stride, _at(residual), residual_stride,
              _at(weight), f32, eps, 0 if residual is None else total.data_ptr(), _at(y), _at(y8 and y8.codes),
              _at(y8 and y8.scales), rstd.data_ptr())
     return Norm(y, y8, total, rstd)

@@ -64,12 +64,13 @@ def _rows(t: torch.Tensor, what: str, width=None) -> int:
     """Row stride of a 2-d tensor with adjacent columns."""
     if t.dim() != 2 or (width is not None and t.shape[1] != width):
         raise ValueError(f"{what} must have shape [rows, {'columns' if width is None else width}], not {tuple(t.shape)}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    (rows, columns), (step, adjacent) = t.shape, t.stride()
+    if columns > 1 and adjacent != 1:
         raise ValueError(f"{what} must have adjacent columns (strides {tuple(t.stride())})")
     # a single row's stride says nothing, and broadcast rows are all the same
-    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+    if rows > 1 and step < columns:
         raise ValueError(f"{what} must have rows that do not overlap (strides {tuple(t.stride())})")
-    return max(t.stride(0), t.shape[1]) if t.shape[0] > 1 else t.shape[1]
+    return step if rows > 1 else columns
 
 
 def _at(t) -> int:

@@ -10,13 +10,14 @@ LINEAR = [
     (257, 64, 64), (257, 64, 1032), (257, 1024, 64), (257, 4096, 8192), (520, 4096, 1032), (520, 4104, 4096),
     (1024, 64, 64), (2051, 512, 2048), (2051, 64, 2048), (4099, 64, 2048), (4099, 256, 4096), (4099, 1024, 64),
     (4099, 1024, 512), (4099, 2048, 64), (4099, 4096, 128), (600, 4104, 5128), (4100, 2048, 136), (5100, 3136, 64),
-    (2051, 264, 4104), (4100, 264, 4104), (330, 8192, 1984), (2051, 1024, 4096), (8200, 2048, 4096),
+    (2051, 264, 4104), (4100, 264, 4104), (330, 8192, 1984), (2051, 1024, 4096), (8200, 2048, 4096), (4800, 2112, 512),
+    (2500, 1024, 4096), (8195, 512, 8192),
 ]
 # rows, inner, k of dense gated projections
 GATED = [
     (1, 8, 8), (1, 64, 4096), (3, 24, 40), (8, 136, 72), (9, 40, 200), (17, 96, 72), (33, 256, 2048), (64, 96, 264),
     (100, 32, 4096), (129, 160, 520), (300, 520, 64), (257, 32, 64), (257, 32, 1032), (257, 2048, 8192), (4099, 512, 64),
-    (4099, 512, 512), (4099, 1024, 64), (4099, 2048, 256), (330, 992, 8192), (4100, 1024, 160), (5100, 1568, 64),
+    (4099, 512, 512), (4099, 1024, 64), (4099, 2048, 256), (330, 992, 8192), (4100, 1024, 160), (5100, 1568, 64), (4800, 1056, 512),
 ]
 
 

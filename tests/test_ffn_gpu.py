@@ -494,7 +494,7 @@ def test_few_rows_of_many_experts(i, dtype):
 
 
 @pytest.mark.parametrize("counts,n,k,tiles", [
-    ([320, 321, 0, 640, 641, 1, 1989], 2048, 264, [320, 128]), ([320, 321, 0, 640, 641, 1, 33], 6144, 64, [320, 256]),
+    ([320, 321, 0, 640, 641, 1, 33], 4096, 520, [320, 128]), ([320, 321, 0, 640, 641, 1, 33], 6144, 64, [320, 256]),
     ([64, 65, 0, 128, 129, 1, 33], 272, 64, [64, 128]), ([256, 257, 512, 513, 31, 2335], 2048, 64, [256, 256])])
 def test_an_experts_tiles_share_its_rows(counts, n, k, tiles):
     """Rows of experts at the tiles' heights and beside them."""
