@@ -36,8 +36,9 @@
  * gradients of weights, which are then 0. rows < 2^31.
  *
  * Products need n % 8 == 0 and k % 8 == 0, both 1 .. 2^20, and addresses and rows of
- * operands at multiples of 16 bytes; an expert's weights stay below 2^31 bytes. A product has fewer than 2^23 tiles of
- * 256 x 256 (2^31 - 2^15 rows of up to 256 columns, 2^24 rows of 30000).
+ * operands at multiples of 16 bytes; an expert's weights stay below 2^31 bytes, and rows of x and dz lie less than 2^22
+ * elements apart. A product has fewer than 2^23 tiles of 256 x 256 (2^31 - 2^15 rows of up to 256 columns, 2^24 rows of
+ * 30000).
  */
 #ifndef NVFP4_FFN_H
 #define NVFP4_FFN_H
@@ -142,7 +143,9 @@ size_t nvfp4_ffn_product_workspace_bytes(int64_t rows, int n, int k, int experts
 /*
  * nvfp4_ffn_product_parts - how a product is computed: the number of its launches over rows (1 or 2; 0 for arguments
  * that are none), and for each four values in `parts` (host, int32 [8]): its rows, the tile's rows and columns
- * (0, 0: the kernel of few rows), the parts of k. Those are the choice for a device of the current one's compute units.
+ * (0, 0: the kernel of few rows), the parts of k. Those are the choice for a device of the current one's compute units
+ * and rows without gaps: where rows lie so far apart that 320 of them are beyond 32-bit offsets, tiles of 256 rows take
+ * the place of tiles of 320.
  *   kind   NVFP4_FFN_FORWARD, _FORWARD_CODES (gated with codes), _DX or _DW; rows, n, k, experts as for the call
  */
 #define NVFP4_FFN_FORWARD 0

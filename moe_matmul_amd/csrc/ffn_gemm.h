@@ -647,8 +647,8 @@ struct Tiling {
   int splits;
 };
 constexpr int kShapes = 6, kShapesOverK = 3;
-inline int tile_rows(int shape) { return shape >= 4 ? 320 : shape == 3 ? 64 : shape ? 256 : 128; }
-inline int tile_cols(int shape) { return shape == 2 || shape == 5 ? 256 : 128; }
+constexpr int tile_rows(int shape) { return shape >= 4 ? 320 : shape == 3 ? 64 : shape ? 256 : 128; }
+constexpr int tile_cols(int shape) { return shape == 2 || shape == 5 ? 256 : 128; }
 
 // Tile, waves, stages: time in us of a product that it fits, bf16, forward.
 //   256 x 256, 8, 3 + 2: 4096 x 4096 x 4096 106 (1.29 PFLOP/s)

@@ -16,7 +16,7 @@ int run_dx(Product& p, const Tiling& t, int dtype, hipStream_t stream);
 int run_dw(Product& p, const Tiling& t, int dtype, hipStream_t stream);
 
 constexpr int kMaxSide = 1 << 20;          // n and k
-constexpr int64_t kMaxStride = 1 << 22;    // a tile's offsets stay below 2^31 bytes
+constexpr int64_t kMaxStride = 1 << 22;    // of the products' rows: see reachable
 constexpr int64_t kMaxBytes = 0x7FFFFFFF;  // of what one resource reaches
 
 int compute_units() {
@@ -235,6 +235,18 @@ static int check_workspace(const void* ws, size_t have, size_t need) {
   return aligned(ws, 256) ? NVFP4_OK : NVFP4_ERR_MISALIGNED;
 }
 
+// Rows of A with k inside are reached by signed 32-bit offsets from their tile's first: the last one's 128 bytes of a
+// stage have to end within what a resource reaches. 256 rows do at any stride that is taken. At strides from 2^31 / 319
+// bytes on 320 do not, and their tiles give way to those of 256 rows and the same width; the parts of k, and so the
+// workspace, stay. (Gathered rows lie within that reach of their operand's first, dw has k outside.)
+constexpr bool within_reach(int high, int64_t stride) { return (high - 1) * stride * 2 + 128 <= kMaxBytes; }
+static_assert(within_reach(256, kMaxStride), "the tiles that others give way to");
+static Tiling reachable(Tiling t, Kind kind, const Product& p) {
+  const bool by_stride = kind != kDw && !p.rows.row_slots;
+  if (by_stride && tile_rows(t.shape) > 256 && !within_reach(tile_rows(t.shape), p.lda)) t.shape = tile_cols(t.shape) == 256 ? 2 : 1;
+  return t;
+}
+
 // Enqueues the parts of a checked product; `workspace` holds what parts_workspace says.
 static int run_product(Kind kind, const Product& whole, bool gated, int dtype, void* workspace, size_t workspace_bytes, void* stream) {
   Part parts[2];
@@ -264,10 +276,11 @@ static int run_product(Kind kind, const Product& whole, bool gated, int dtype, v
     p.partial_step = p.m * (kind == kDw ? e : 1) * cols;
     int rc;
     hipStream_t s = (hipStream_t)stream;
+    const Tiling tiling = reachable(part.tiling, kind, p);
     if (part.few) rc = run_few(p, dtype, gated, s);
-    else if (kind == kDx) rc = run_dx(p, part.tiling, dtype, s);
-    else if (kind == kDw) rc = run_dw(p, part.tiling, dtype, s);
-    else rc = run_forward(p, part.tiling, dtype, gated, s);
+    else if (kind == kDx) rc = run_dx(p, tiling, dtype, s);
+    else if (kind == kDw) rc = run_dw(p, tiling, dtype, s);
+    else rc = run_forward(p, tiling, dtype, gated, s);
     if (!rc && !part.few && part.tiling.splits > 1) rc = finish_splits(p, dtype, gated, kind == kDw, s);
     if (rc) return rc;
   }
