@@ -13,6 +13,8 @@
 // for a few columns: fewer share k, and the workgroup has more columns (256 experts of 2048 x 512, 1024 rows: 98 us, 308
 // with 16 columns to a workgroup). Under a kernel trace: 1 x 7168 x 2048 8.5 us, gated 1 x 2 x 2048 x 7168 12.5 (58.7 MB:
 // 4.7 TB/s; a launch that does nothing takes 3).
+#include <atomic>
+
 #include "ffn_gemm.h"
 
 namespace ffn {
@@ -35,7 +37,7 @@ __device__ __forceinline__ s16x8 load16(Buffer b, int offset) {
 constexpr int kFewWaves = 16;
 
 // Bytes between rows in LDS: 64 more than their elements', so that eight rows' chunks lie in different banks.
-__host__ __device__ inline int few_stride(int k, int chunk) { return ((k < chunk ? k : chunk) + 31) / 32 * 64 + 64; }
+__host__ __device__ constexpr int few_stride(int k, int chunk) { return ((k < chunk ? k : chunk) + 31) / 32 * 64 + 64; }
 
 // The expert of a workgroup and its rows: the blockIdx.y-th, or of those that have any, if there are fewer workgroups
 // than experts; with `clear` the last has the rows of none. False: no such expert, or no rows.
@@ -208,11 +210,16 @@ int run_few(const Product& p, int dtype, bool gated, hipStream_t stream) {
       const int rows_bytes = R * few_stride(p.k, 32 * U * kFewWaves), sums_bytes = kFewWaves * 16 * 20 * 4;
       const size_t lds = rows_bytes > sums_bytes ? rows_bytes : sums_bytes;
       auto kernel = gated ? few_kernel<T, U, R, true> : few_kernel<T, U, R, false>;
-      static thread_local size_t allowed[2][16];  // by device
-      int device = 0;
-      if (lds > 65536 && hipGetDevice(&device) == hipSuccess && (device >= 16 || allowed[gated][device] < lds)) {
-        if (hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) == hipSuccess && device < 16)
-          allowed[gated][device] = lds;
+      // what a kernel is allowed belongs to the process, so it is always the most that the kernel ever asks for
+      constexpr int most = R * few_stride(1 << 20, 32 * U * kFewWaves);
+      if constexpr (most > 65536) {
+        static std::atomic<bool> allowed[2][16];  // by device
+        int device = 0;
+        if (hipGetDevice(&device) != hipSuccess || device >= 16) device = -1;
+        if (device < 0 || !allowed[gated][device]) {
+          const bool done = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, most) == hipSuccess;
+          if (done && device >= 0) allowed[gated][device] = true;
+        }
       }
       kernel<<<grid, 1024, lds, stream>>>(p, share_log);
     };

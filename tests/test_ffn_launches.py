@@ -144,3 +144,30 @@ def test_rows_far_apart_are_within_reach_of_a_tiles_offsets(recorder, kind, rows
         assert (high - 1) * stride * 2 + 128 < 2 ** 31
         assert launches[0][1] == tiles(high), stride
         assert len(launches) == (1 if splits == 1 else 2)
+
+
+def test_threads_do_not_lower_each_others_shared_memory(recorder):
+    """What a kernel is allowed belongs to the process: a thread's product of few rows of a short k leaves another's of a
+    long k the shared memory that it asks for."""
+    launches = run(recorder, """
+        def product(gated, k):
+            if gated:
+                c.nvfp4_ffn_gated(P, k, P, 2, P, 0, 0, 0, 2, 8, 64, k, None, 0, 0, 0, 0)
+            else:
+                c.nvfp4_ffn_linear(P, k, P, 0, 0, 0, 0, 0, 0, P, 2, 8, 64, k, None, 0, 0, 0, 0)
+        def thread(*ks):
+            t = threading.Thread(target=lambda: [product(g, k) for k in ks for g in (False, True)])
+            t.start()
+            t.join()
+        product(False, 16384)
+        product(True, 16384)
+        thread(5120)
+        thread(4104, 8192)
+        thread(4104)
+        product(False, 16384)
+        product(True, 16384)
+        print(json.dumps(record()))
+    """)
+    assert len(launches) == 12 and max(l[5] for l in launches) > 65536
+    for _, _, _, _, _, shared, allowed in launches:
+        assert shared <= allowed, launches
