@@ -184,12 +184,16 @@ int nvfp4_ffn_gated_again(const void* dh, int64_t dh_stride, const void* x, int6
 
 /*
  * nvfp4_ffn_linear_dx - dx [rows][k] = dz W; dz device [rows][n], rows dz_stride apart; w as in nvfp4_ffn_linear.
+ * nvfp4_ffn_linear_dx_ex - the same, dx fp32 (dx_f32 = 1: rows of slots that are yet to be added) or of dtype.
  * nvfp4_ffn_linear_dw - dW [n][k], with a plan [experts][n][k], = dz^T x over an expert's rows (an expert
  * without rows: 0), fp32 (dw_f32 = 1) or of dtype; x device [rows][k], sorted by expert with a plan;
  * workspace: nvfp4_ffn_dw_workspace_bytes bytes (may be 0).
  */
 int nvfp4_ffn_linear_dx(const void* dz, int64_t dz_stride, const void* w, void* dx, int dtype, int64_t rows, int n, int k,
                         const nvfp4_ffn_plan* plan, int clear, void* workspace, size_t workspace_bytes, void* stream);
+int nvfp4_ffn_linear_dx_ex(const void* dz, int64_t dz_stride, const void* w, void* dx, int dx_f32, int dtype, int64_t rows,
+                           int n, int k, const nvfp4_ffn_plan* plan, int clear, void* workspace, size_t workspace_bytes,
+                           void* stream);
 int nvfp4_ffn_linear_dw(const void* dz, int64_t dz_stride, const void* x, int64_t x_stride, void* dw, int dw_f32, int dtype,
                         int64_t rows, int n, int k, const nvfp4_ffn_plan* plan, void* workspace, size_t workspace_bytes,
                         void* stream);

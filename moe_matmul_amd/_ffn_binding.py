@@ -54,6 +54,7 @@ _SIGNATURES = {
     "nvfp4_ffn_gated_again": (_int, [_ptr, _i64, _ptr, _i64, _ptr, _int, _ptr, _int, _i64, _int, _int, _plan, _ptr, _size,
                                      _ptr]),
     "nvfp4_ffn_linear_dx": (_int, [_ptr, _i64, _ptr, _ptr, _int, _i64, _int, _int, _plan, _int, _ptr, _size, _ptr]),
+    "nvfp4_ffn_linear_dx_ex": (_int, [_ptr, _i64, _ptr, _ptr, _int, _int, _i64, _int, _int, _plan, _int, _ptr, _size, _ptr]),
     "nvfp4_ffn_linear_dw": (_int, [_ptr, _i64, _ptr, _i64, _ptr, _int, _int, _i64, _int, _int, _plan, _ptr, _size, _ptr]),
     "nvfp4_ffn_dw_workspace_bytes": (_size, [_i64, _int, _int, _int]),
     "nvfp4_ffn_last_hip_error": (_int, []),
@@ -98,6 +99,7 @@ nvfp4_ffn_linear_dz = _checked("nvfp4_ffn_linear_dz")
 nvfp4_ffn_gated_dz = _checked("nvfp4_ffn_gated_dz")
 nvfp4_ffn_gated_again = _checked("nvfp4_ffn_gated_again")
 nvfp4_ffn_linear_dx = _checked("nvfp4_ffn_linear_dx")
+nvfp4_ffn_linear_dx_ex = _checked("nvfp4_ffn_linear_dx_ex")
 nvfp4_ffn_linear_dw = _checked("nvfp4_ffn_linear_dw")
 
 

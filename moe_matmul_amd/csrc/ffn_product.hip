@@ -392,8 +392,9 @@ int nvfp4_ffn_gated_again(const void* dh, int64_t dh_stride, const void* x, int6
   return run_product(kForward, p, true, dtype, workspace, workspace_bytes, stream);
 }
 
-int nvfp4_ffn_linear_dx(const void* dz, int64_t dz_stride, const void* w, void* dx, int dtype, int64_t rows, int n, int k,
-                        const nvfp4_ffn_plan* plan, int clear, void* workspace, size_t workspace_bytes, void* stream) {
+int nvfp4_ffn_linear_dx_ex(const void* dz, int64_t dz_stride, const void* w, void* dx, int dx_f32, int dtype, int64_t rows,
+                           int n, int k, const nvfp4_ffn_plan* plan, int clear, void* workspace, size_t workspace_bytes,
+                           void* stream) {
   if (!type16(dtype) || !rows_ok(rows) || !side_ok(n) || !side_ok(k)) return NVFP4_ERR_INVALID;
   Product p{};
   if (const int rc = plan_rows(plan, rows, false, &p.rows)) return rc;
@@ -403,8 +404,13 @@ int nvfp4_ffn_linear_dx(const void* dz, int64_t dz_stride, const void* w, void* 
   // the reduction is over n, the output's columns are k
   p.a = dz; p.b = w; p.lda = dz_stride; p.ldb = k; p.m = rows; p.n = k; p.k = n; p.b_step = (int64_t)n * k;
   p.rows.clear = clear != 0;
-  p.ep.y = dx; p.ep.ldy = k;
+  p.ep.y = dx; p.ep.ldy = k; p.ep.y_f32 = dx_f32;
   return run_product(kDx, p, false, dtype, workspace, workspace_bytes, stream);
+}
+
+int nvfp4_ffn_linear_dx(const void* dz, int64_t dz_stride, const void* w, void* dx, int dtype, int64_t rows, int n, int k,
+                        const nvfp4_ffn_plan* plan, int clear, void* workspace, size_t workspace_bytes, void* stream) {
+  return nvfp4_ffn_linear_dx_ex(dz, dz_stride, w, dx, 0, dtype, rows, n, k, plan, clear, workspace, workspace_bytes, stream);
 }
 
 int nvfp4_ffn_linear_dw(const void* dz, int64_t dz_stride, const void* x, int64_t x_stride, void* dw, int dw_f32, int dtype,

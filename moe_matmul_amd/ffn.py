@@ -250,15 +250,15 @@ def _dw(dw, w, dtype):
     return dw, _param(dw, "dw", w.shape, w)
 
 
-def _products_back(dz, dz_stride, x, x_stride, w, plan, kind, experts, dw):
-    """(dz w, dz^T x) over rows [rows, n] and [rows, k], sorted by expert with a plan."""
+def _products_back(dz, dz_stride, x, x_stride, w, plan, kind, experts, dw, dx_f32=False):
+    """(dz w, dz^T x) over rows [rows, n] and [rows, k], sorted by expert with a plan; dz w in fp32 or dz's type."""
     device, (rows, n), k = dz.device, dz.shape, w.shape[-1]
     dw, f32 = _dw(dw, w, dz.dtype)
-    dx = _out(None, "dx", (rows, k), dz.dtype, device)
+    dx = _out(None, "dx", (rows, k), torch.float32 if dx_f32 else dz.dtype, device)
     need = _need(c.nvfp4_ffn_product_workspace_bytes, device, rows, k, n, experts)
     need_dw = _need(c.nvfp4_ffn_dw_workspace_bytes, device, rows, n, k, experts)
     room = _room(max(need, need_dw), device)
-    _enqueue(c.nvfp4_ffn_linear_dx, device, dz.data_ptr(), dz_stride, w.data_ptr(), dx.data_ptr(), kind, rows, n, k,
+    _enqueue(c.nvfp4_ffn_linear_dx_ex, device, dz.data_ptr(), dz_stride, w.data_ptr(), dx.data_ptr(), dx_f32, kind, rows, n, k,
              _plan(plan), 1, _at(room), need)
     _enqueue(c.nvfp4_ffn_linear_dw, device, dz.data_ptr(), dz_stride, x.data_ptr(), x_stride, dw.data_ptr(), f32, kind, rows,
              n, k, _plan(plan), _at(room), need_dw)
@@ -347,8 +347,7 @@ def gated_backward(dh, x, w, kept=None, *, activation="silu", plan=None, dw=None
 
     ``x``: the rows as they were given, or a Rows8 of them (of the norm, or by ``quantize8``); ``kept``: what
     ``gated(..., save=)`` gave, or None: both projections are computed again from x, and not rounded. ``dw``: a tensor to take w's
-    gradient, of w's type or fp32. The projections' gradients are rounded to 16 bits for the products, and with a plan
-    the slots' dx before their sum."""
+    gradient, of w's type or fp32. The projections' gradients are rounded to 16 bits for the products."""
     device = _gpu(dh, "dh")
     kind, act = _type16(dh, "dh"), _activation(activation, gated=True)
     experts, n, k = _weights(w, plan, device, dh.dtype)
@@ -395,5 +394,6 @@ def gated_backward(dh, x, w, kept=None, *, activation="silu", plan=None, dw=None
         _enqueue(c.nvfp4_ffn_gated_dz, device, dh.data_ptr(), stride, 0 if eight else kept.data_ptr(),
                  kept.codes.data_ptr() if eight else 0, kept.scales.data_ptr() if eight else 0, act, dz.data_ptr(), kind,
                  rows, inner, _plan(plan))
-    dx, dw = _products_back(dz, n, rows_x, rows_stride, w, plan, kind, experts, dw)
+    # a token's dx is one sum over its slots: their parts of it stay in fp32
+    dx, dw = _products_back(dz, n, rows_x, rows_stride, w, plan, kind, experts, dw, plan is not None and plan.topk > 1)
     return (dx if plan is None else moe.combine(dx, None, plan, dtype=dh.dtype)), dw

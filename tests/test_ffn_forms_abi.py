@@ -1,0 +1,23 @@
+"""Forms of the block's entry points on the CPU: what they refuse, and how products are computed (no GPU needed)."""
+import pytest
+
+import moe_matmul_amd as mm
+from moe_matmul_amd import _ffn_binding as c
+
+P = 0x10000  # an address that no refused call reads
+INVALID, MISALIGNED, WORKSPACE = mm.NVFP4_ERR_INVALID, mm.NVFP4_ERR_MISALIGNED, mm.NVFP4_ERR_WORKSPACE
+
+DX = dict(dz=P, dz_stride=64, w=P, dx=P, dx_f32=1, dtype=2, rows=4, n=64, k=64, plan=None, clear=1, ws=0, ws_bytes=0, stream=0)
+
+
+@pytest.mark.parametrize("code,bad", [
+    (INVALID, dict(dtype=0)), (INVALID, dict(rows=-1)), (INVALID, dict(n=60)), (INVALID, dict(k=60)), (INVALID, dict(dz=0)),
+    (INVALID, dict(w=0)), (INVALID, dict(dx=0)), (INVALID, dict(dz_stride=56)), (INVALID, dict(dz_stride=1 << 22)),
+    (MISALIGNED, dict(dz=P + 8)), (MISALIGNED, dict(dx=P + 8)), (MISALIGNED, dict(dz_stride=68)),
+    (WORKSPACE, dict(rows=33, n=8192, dz_stride=8192, k=512))])
+@pytest.mark.parametrize("f32", [0, 1])
+def test_gradients_of_rows_refuse(code, bad, f32):
+    with pytest.raises(c.Nvfp4FfnError) as e:
+        c.nvfp4_ffn_linear_dx_ex(*{**DX, "dx_f32": f32, **bad}.values())
+    assert e.value.code == code
+    c.nvfp4_ffn_linear_dx_ex(*{**DX, "rows": 0}.values())
