@@ -10,7 +10,7 @@
 // (1 row, 4096 x 7168: 15.4 us; U = 4 16.9). Where there are several rounds of them, two share a unit, so that one's
 // weights are under way while the other adds up: U = 4, the registers allow no more (1 row, 28672 x 4096: 44 us, 5.3
 // TB/s; U = 16 54. 32 experts of 4096 x 7168: 208 and 311). Where k is short, all sixteen waves would have little to do
-// for a few columns: fewer share k, and the workgroup has more columns (256 experts of 2048 x 512, 1024 rows: 98 us, 308
+// for a few columns: fewer share k, and the workgroup has more columns (256 experts of 2048 x 512, 64 rows: 35 us, 90
 // with 16 columns to a workgroup). Under a kernel trace: 1 x 7168 x 2048 8.5 us, gated 1 x 2 x 2048 x 7168 12.5 (58.7 MB:
 // 4.7 TB/s; a launch that does nothing takes 3).
 #include <atomic>
@@ -200,7 +200,7 @@ int run_few(const Product& p, int dtype, bool gated, hipStream_t stream) {
   int share_log = 4;
   while (!deep && share_log > 1 && p.k <= 32 * kShallow << (share_log - 1) && (int64_t)blocks * busy >> (4 - share_log) >= 4 * units) --share_log;
   // To look for the experts that have rows costs every workgroup its time, idle workgroups cost a launch of theirs: 8 of 64
-  // experts (1 token, 2048 x 2048) 19 us and 26, 60 of 64 128 and 113; up to a quarter of the experts the search pays.
+  // experts (1 token, 2 x 1024 x 2048) 19 us and 25, 32 rows of 64 56 and 54; up to a quarter of the experts the search pays.
   const int high = p.m * 4 <= experts ? busy : experts;
   const dim3 grid(ceil_div(blocks, kFewWaves >> share_log), p.rows.offsets ? high + (p.rows.clear ? 1 : 0) : 1);
   with_type16(dtype, [&](auto type) {

@@ -114,11 +114,14 @@ enum Kind { kForward = NVFP4_FFN_FORWARD, kForwardCodes = NVFP4_FFN_FORWARD_CODE
 
 // Whether the kernel of few rows is the faster one: for up to so many rows (8 rows, against 64 x 128 tiles and parts of
 // k: 4096 x 7168 17.8 and 23 us, 28672 x 4096 53 and 70; more than 8 read the weights twice). By experts their mean
-// counts, as one with more than 8 rows takes several passes: 4 rows an expert (64 of 2048 x 2048) 113 and 129, 8 rows
-// 170 and 130.
-constexpr int kFewRows = 8, kFewRowsOfExpert = 4;
+// counts, as one with more than 8 rows takes several passes: 8 experts of 2 x 1024 x 4096, 4 rows each on the average 33
+// and 38, 6 rows 46 and 39. Their sum counts too, as they may all be one expert's, whose passes wait for one another: 64
+// experts of 2 x 1024 x 2048, 64 rows of any experts 76 and 86, of one 43 and 19; 256 rows 117 and 114, 151 and 19; 256
+// experts of 2 x 512 x 2048, 256 rows 139 and 154, 154 and 22; 1024 rows 223 and 233, 582 and 25.
+constexpr int kFewRows = 8, kFewRowsOfExpert = 4, kFewRowsOfExperts = 64;
 static bool few_rows(Kind kind, int64_t rows, int experts) {
-  return kind == kForward && rows <= (experts > 1 ? kFewRowsOfExpert * experts : kFewRows);
+  const int by_experts = kFewRowsOfExpert * experts < kFewRowsOfExperts ? kFewRowsOfExpert * experts : kFewRowsOfExperts;
+  return kind == kForward && rows <= (experts > 1 ? by_experts : kFewRows);
 }
 
 // Rows row0 .. row0 + rows - 1 of the output, by few rows or by tiles.

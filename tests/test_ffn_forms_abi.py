@@ -21,3 +21,14 @@ def test_gradients_of_rows_refuse(code, bad, f32):
         c.nvfp4_ffn_linear_dx_ex(*{**DX, "dx_f32": f32, **bad}.values())
     assert e.value.code == code
     c.nvfp4_ffn_linear_dx_ex(*{**DX, "rows": 0}.values())
+
+
+@pytest.mark.parametrize("n,k", [(2048, 512), (1024, 2048), (14336, 4096)])
+def test_few_rows_of_experts_are_few_in_all(n, k):
+    """The kernel of few rows takes an expert's eight at a time, one after the other: what all may be one expert's has to
+    be few itself."""
+    few = [(0, 0)]
+    for experts in (2, 8, 16, 17, 64, 256, 512):
+        for rows in (1, 2 * experts, 4 * experts, 4 * experts + 1, 63, 64, 65, 128, 1000, 2048):
+            parts = c.nvfp4_ffn_product_parts(c.NVFP4_FFN_FORWARD, rows, n, k, experts)
+            assert ([p[1:3] for p in parts] == few) == (rows <= min(64, 4 * experts)), (experts, rows, parts)
