@@ -1,6 +1,8 @@
 """Forms of the block's entry points on the CPU: what they refuse, and how products are computed (no GPU needed)."""
 import pytest
 
+import ffn_cases
+import ffn_parts_cases
 import moe_matmul_amd as mm
 from moe_matmul_amd import _ffn_binding as c
 
@@ -32,3 +34,21 @@ def test_few_rows_of_experts_are_few_in_all(n, k):
         for rows in (1, 2 * experts, 4 * experts, 4 * experts + 1, 63, 64, 65, 128, 1000, 2048):
             parts = c.nvfp4_ffn_product_parts(c.NVFP4_FFN_FORWARD, rows, n, k, experts)
             assert ([p[1:3] for p in parts] == few) == (rows <= min(64, 4 * experts)), (experts, rows, parts)
+
+
+def test_gpu_cases_reach_every_tile_with_and_without_parts():
+    """For a device of 256 compute units. (Dense rows in tiles of 320 x 256 never come in parts: they are there for rows
+    that leave a part of a round in all others, and parts fill rounds.)"""
+    seen = set()
+    for size in ffn_cases.LINEAR + ffn_parts_cases.LINEAR:
+        seen |= ffn_parts_cases.linear_kernels(*size)
+    for size in ffn_cases.GATED + ffn_parts_cases.GATED:
+        seen |= ffn_parts_cases.gated_kernels(*size)
+    for size in ffn_parts_cases.EXPERTS:
+        seen |= ffn_parts_cases.experts_kernels(*size)
+    tall = [(64, 128), (128, 128), (256, 128), (256, 256), (320, 128), (320, 256)]
+    want = {(name, by_experts, *tile, parts) for name in ("linear", "gated", "codes", "dx", "dw") for by_experts in (False, True)
+            for tile in (tall[1:4] if name == "dw" else tall) for parts in (False, True)}
+    want -= {(name, False, 320, 256, True) for name in ("linear", "gated", "codes", "dx")}
+    want |= {(name, by_experts, 0, 0, False) for name in ("linear", "gated") for by_experts in (False, True)}
+    assert not want - seen, sorted(want - seen)
