@@ -66,14 +66,16 @@ __device__ inline int expert_of(const Rows& p, int64_t r) {
 }
 
 // ---- activations --------------------------------------------------------------
-// e^x by the card's 2^x: the product with log2 e is rounded, so within (|x| + 2) 2^-24 of the value; below 2^-126 it is 0.
+// e^x by the card's 2^x: log2 e is rounded (0.23 |x| 2^-24 of the value) and so is the product (|x| 2^-24), so within
+// (1.25 |x| + 2) 2^-24 of it; below 2^-126 it is 0.
 __device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
 // 1 / (1 + e^-z). e^-z is infinite below -88.7, where the quotient is 0.
 __device__ __forceinline__ float logistic(float z) { return __builtin_amdgcn_rcpf(1.f + fast_exp(-z)); }
 // The normal distribution's function below z <= 0 and e = e^(-z^2/2): with t = -z / sqrt 2 and k = 1 / (1 + 0.3 t),
 // erfc(t) / 2 = e^(-t^2) k P(k), where P is the polynomial of degree 8 that is nearest to erfc(t) e^(t^2) / 2 k,
-// relative to it, for t of 0 to 11 (2 * 10^-8 off; by least squares, reweighted to even out the error). No
-// cancellation, so small values keep their bits: 5 instructions and 9 products where a library's erfc has 100.
+// relative to it, for t of 0 to 11 (by least squares, reweighted to even out the error; 4.4 * 10^-8 off with the
+// coefficients as they are rounded here, 0.75 * 2^-24). No cancellation, so small values keep their bits: 5 instructions
+// and 9 products where a library's erfc has 100.
 __device__ __forceinline__ float normal_tail(float z, float e) {
   const float k = __builtin_amdgcn_rcpf(fmaf(fabsf(z), 0.3f * 0.707106781f, 1.f));
   float v = -0.064777948f;
@@ -174,7 +176,7 @@ __device__ inline uint32_t scale8(uint32_t top) {
   const int e = (int)(top >> 23) - 8 + ((top & 0x7FFFFFu) > 0x600000u);
   return e < 1 ? 1 : e;
 }
-// 2^(byte - 127) and its inverse; byte 1 .. 246 as scale8 gives them.
+// 2^(byte - 127) and its inverse; byte 1 .. 247 as scale8 gives them (247: beyond 1.75 * 2^127), or 255.
 __device__ inline float scale8_value(uint32_t byte) { return __builtin_bit_cast(float, byte == 255 ? 0x7FC00000u : byte << 23); }
 __device__ inline float scale8_inverse(uint32_t byte) { return __builtin_bit_cast(float, byte == 255 ? 0x7FC00000u : (254u - byte) << 23); }
 // Four codes; the products are exact, so each code is rounded once (to nearest, ties to even).

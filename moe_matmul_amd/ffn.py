@@ -219,7 +219,7 @@ def _kept(shape, like, cleared):
 @_on_stream
 def linear(x, w, *, bias=None, activation=None, residual=None, plan=None, save=False, out=None, stream=None):
     """``y = act(x w^T + bias) + residual`` in one product; with ``save`` (y, z), z the activation's argument as
-    ``linear_backward`` needs it.
+    ``linear_backward`` needs it, rounded to x's type.
 
     ``x`` [rows, k] (fp16 or bf16), ``w`` [n, k], ``bias`` [n] (fp32 or x's type), ``residual`` [rows, n];
     ``activation``: None, "relu", "silu" or "gelu". With a ``plan``: rows sorted by expert, ``w`` [experts, n, k],
@@ -270,9 +270,9 @@ def linear_backward(dy, x, w, *, bias=None, z=None, activation=None, plan=None, 
     """(dx, dw, dbias) of ``linear``; the residual's gradient is dy.
 
     ``z`` as ``linear(..., save=True)`` gave it, with an activation; ``bias`` as it was given there (dbias has its
-    type; None without one); ``dw``: a tensor to take w's gradient, of w's type or fp32. dz = dy act'(z) is rounded to
-    16 bits for the products. With a ``plan``: rows sorted by expert; rows of no expert have dx 0, experts without
-    rows gradients of 0. ``x`` may be a Rows8."""
+    type; None without one); ``dw``: a tensor to take w's gradient, of w's type or fp32. The slope is that of the kept
+    z; dz = dy act'(z) is rounded to 16 bits for the products, not for dbias. With a ``plan``: rows sorted by expert;
+    rows of no expert have dx 0, experts without rows gradients of 0. ``x`` may be a Rows8."""
     device = _gpu(dy, "dy")
     kind, act = _type16(dy, "dy"), _activation(activation)
     experts, n, k = _weights(w, plan, device, dy.dtype)
